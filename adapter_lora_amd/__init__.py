@@ -13,15 +13,17 @@ from typing import List, Optional, Sequence
 
 import torch
 
-from ._abi import (LORA_BF16, LORA_F32, LORA_MAX_ADAPTERS, LORA_MAX_RANK,
+from ._abi import (LORA_BF16, LORA_E4M3, LORA_F32, LORA_MAX_ADAPTERS, LORA_MAX_RANK,
                    LORA_MAX_SLICES, LORA_DECODE_MAX_M, LORA_TILE_ROWS, LORA_DEVERR_WAIT,
                    LORA_DEVERR_BAD_ID, LORA_DEVERR_TABLE, LoraError, lib, lora_weights_t,
-                   lora_segments_t, lora_moe_weights_t, lora_moe_align_t, check)
+                   lora_segments_t, lora_moe_weights_t, lora_moe_align_t,
+                   lora_moe_experts_t, check)
 
 __all__ = [
-    "LORA_BF16", "LORA_F32", "LORA_DEVERR_WAIT", "LORA_DEVERR_BAD_ID", "LORA_DEVERR_TABLE", "LoraError", "LoraTable",
+    "LORA_BF16", "LORA_E4M3", "LORA_F32", "LORA_DEVERR_WAIT", "LORA_DEVERR_BAD_ID",
+    "LORA_DEVERR_TABLE", "LoraError", "LoraTable",
     "Segments", "Workspace",
-    "MoeWeights", "MoeAlign",
+    "MoeWeights", "MoeAlign", "MoeExperts",
     "lora_build_segments", "lora_tile_capacity", "lora_shrink", "lora_expand_add",
     "lora_shrink_expand_add", "lora_fused_decode", "lora_fused_decode_noalloc",
     "lora_pack_embedding_adapter", "lora_embedding_shrink", "lora_embedding_decode",
@@ -29,7 +31,8 @@ __all__ = [
     "lora_table_plan", "lora_pack_adapter",
     "lora_moe_align_capacity", "lora_moe_align", "lora_moe_workspace_size",
     "lora_moe_gate_up_add", "lora_moe_silu_and_mul", "lora_moe_down_add",
-    "lora_moe_topk_reduce", "stream_handle",
+    "lora_moe_topk_reduce", "lora_rms_norm", "lora_quantize_rows", "lora_linear_fp8",
+    "lora_moe_decode_workspace_size", "lora_moe_decode", "stream_handle",
 ]
 
 
@@ -532,3 +535,188 @@ def lora_moe_topk_reduce(cache3: torch.Tensor, topk_weights: torch.Tensor, out: 
     check(lib.lora_moe_topk_reduce(_dtype_code(cache3.dtype), _ptr(cache3), _rows(cache3, "cache3"),
                                    _ptr(topk_weights), _ptr(out), _rows(out, "out"), M, topk,
                                    out.shape[1], stream_handle(stream)), "lora_moe_topk_reduce")
+
+
+# ------------------------------------------------------------------------- 8-bit decoder layer
+E4M3 = torch.float8_e4m3fn
+
+
+def _check_e4m3(**named) -> None:
+    for name, t in named.items():
+        if t.dtype != E4M3:
+            raise LoraError(f"{name} is {t.dtype} but must be {E4M3}")
+
+
+def _scales(t: torch.Tensor, name: str, n: int) -> int:
+    """Device address of one fp32 scale per row of an 8-bit tensor."""
+    if t.dtype != torch.float32 or t.numel() < n or not t.is_contiguous():
+        raise LoraError(f"{name} must be contiguous fp32 with {n} values")
+    if not t.is_cuda:
+        raise LoraError(f"{name} must live on the GPU")
+    return t.data_ptr()
+
+
+def _matrix(t: Optional[torch.Tensor], name: str, shape, dtype):
+    """(address, leading dimension) of a row-major 2-D device operand of
+    exactly this shape and dtype; zeros for None."""
+    if t is None:
+        return 0, 0
+    if t.dtype != dtype:
+        raise LoraError(f"{name} is {t.dtype} but must be {dtype}")
+    if t.shape != shape:
+        raise LoraError(f"{name} must be a tensor of shape {tuple(shape)}, not {tuple(t.shape)}")
+    ld, unit = t.stride()
+    if unit != 1 and t.numel() > 0:
+        raise LoraError(f"{name} must have unit column stride")
+    if not t.is_cuda:
+        raise LoraError(f"{name} must live on the GPU")
+    return t.data_ptr(), max(ld, shape[1])
+
+
+def lora_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                  residual: Optional[torch.Tensor] = None,
+                  residual_out: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None, out8: Optional[torch.Tensor] = None,
+                  scale: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The residual's addition and the root-mean-square norm of x's rows:
+    h = x + residual, residual_out = h, v = h * weight / sqrt(mean(h^2) + eps),
+    out = v, and in 8 bits out8 = v / scale with scale = max|v| / 448 per row.
+    Each output is written when given; out or out8 (with scale) has to be.
+    residual_out may be `residual` or `x` itself, `out` may be `x`."""
+    shape, dtype = x.shape, x.dtype
+    if len(shape) != 2:
+        raise LoraError("x must be a 2-D tensor")
+    M, K = shape
+    code = _dtype_code(dtype)
+    if out is None and out8 is None:
+        raise LoraError("out or out8 is needed")
+    if (out8 is None) != (scale is None):
+        raise LoraError("out8 and scale are given together")
+    if residual_out is not None and residual is None:
+        raise LoraError("residual_out needs a residual")
+    if weight.dtype != dtype or weight.shape != (K,) or not weight.is_contiguous():
+        raise LoraError(f"weight must be a contiguous {dtype} vector of {K} values")
+    pr, ldr = _matrix(residual, "residual", shape, dtype)
+    pro, ldro = _matrix(residual_out, "residual_out", shape, dtype)
+    po, ldo = _matrix(out, "out", shape, dtype)
+    po8, ldo8 = _matrix(out8, "out8", shape, E4M3)
+    px, ldx = _matrix(x, "x", shape, dtype)
+    if not weight.is_cuda:
+        raise LoraError("weight must live on the GPU")
+    check(lib.lora_rms_norm(code, px, ldx, pr, ldr, weight.data_ptr(), eps, M, K, pro, ldro, po,
+                            ldo, po8, ldo8, 0 if scale is None else _scales(scale, "scale", M),
+                            stream_handle(stream)), "lora_rms_norm")
+
+
+def lora_quantize_rows(x: torch.Tensor, out8: torch.Tensor, scale: torch.Tensor,
+                       stream=None) -> None:
+    """Rows of x in 8 bits: scale = max|x| / 448 per row, out8 = x / scale."""
+    shape = x.shape
+    if len(shape) != 2:
+        raise LoraError("x must be a 2-D tensor")
+    code = _dtype_code(x.dtype)
+    po8, ldo8 = _matrix(out8, "out8", shape, E4M3)
+    px, ldx = _matrix(x, "x", shape, x.dtype)
+    check(lib.lora_quantize_rows(code, px, ldx, shape[0], shape[1], po8, ldo8,
+                                 _scales(scale, "scale", shape[0]), stream_handle(stream)),
+          "lora_quantize_rows")
+
+
+def lora_linear_fp8(table: LoraTable, W8: torch.Tensor, w_scale: torch.Tensor, x8: torch.Tensor,
+                    x_scale: torch.Tensor, x: torch.Tensor, seg: Segments, y: torch.Tensor,
+                    ws: Workspace, stream=None) -> None:
+    """y = (x8 W8^T) x_scale w_scale + (x A_i^T) B_i^T per token, y overwritten:
+    a shared projection in 8 bits ([N, K], the table's slices stacked in
+    order) beside the batch's adapters.  One launch for up to 64 tokens."""
+    K, N, dtype = table.K, table.N, table.dtype
+    _check_io(dtype, x=x, y=y)
+    _check_e4m3(W8=W8, x8=x8)
+    _cols(x, "x", K)
+    _cols(x8, "x8", K)
+    _cols(W8, "W8", K)
+    _cols(y, "y", N, exact=False)
+    M = x.shape[0]
+    if x8.shape[0] != M or y.shape[0] != M:
+        raise LoraError("x, x8 and y must have the same number of rows")
+    if W8.shape[0] != N:
+        raise LoraError("W8 must have one row per output column of the table")
+    ldx, ldx8, ldw, ldy = _rows(x, "x"), _rows(x8, "x8"), _rows(W8, "W8"), _rows(y, "y")
+    pw, px = _scales(w_scale, "w_scale", N), _scales(x_scale, "x_scale", M)
+    if seg.L != table.L or M > seg.sorted_idx.shape[0]:
+        raise LoraError("segment buffers do not match the table or the batch")
+    check(lib.lora_linear_fp8(table.ref, W8.data_ptr(), ldw, pw, x8.data_ptr(), ldx8, px,
+                              x.data_ptr(), ldx, M, seg.ref, y.data_ptr(), ldy, ws.ptr, ws.nbytes,
+                              stream_handle(stream)), "lora_linear_fp8")
+
+
+class MoeExperts:
+    """Router [E, H] and experts W_gu [E, 2I, H], W_d [E, H, I] of one MoE
+    layer: bf16, or e4m3 with one fp32 scale per row (s_gu [E, 2I], s_d
+    [E, H]; the router stays bf16)."""
+
+    def __init__(self, router: torch.Tensor, W_gu: torch.Tensor, W_d: torch.Tensor, topk: int,
+                 renormalize: bool = False, s_gu: Optional[torch.Tensor] = None,
+                 s_d: Optional[torch.Tensor] = None):
+        if router.dim() != 2 or W_gu.dim() != 3 or W_d.dim() != 3:
+            raise LoraError("router must be 2-D, W_gu and W_d 3-D")
+        E, H = router.shape
+        I = W_d.shape[2]
+        if tuple(W_gu.shape) != (E, 2 * I, H) or tuple(W_d.shape) != (E, H, I):
+            raise LoraError("inconsistent MoE expert shapes")
+        if W_gu.dtype != W_d.dtype or W_gu.dtype not in (torch.bfloat16, E4M3):
+            raise LoraError(f"experts must be bfloat16 or {E4M3}")
+        eight = W_gu.dtype == E4M3
+        if eight != (s_gu is not None) or eight != (s_d is not None):
+            raise LoraError("s_gu and s_d go with experts in 8 bits")
+        if router.dtype != torch.bfloat16:
+            raise LoraError("router must be bfloat16")
+        for n, t in (("router", router), ("W_gu", W_gu), ("W_d", W_d), ("s_gu", s_gu),
+                     ("s_d", s_d)):
+            if t is not None and not t.is_cuda:
+                raise LoraError(f"{n} must live on the GPU")
+        self.router, self.W_gu, self.W_d = router.contiguous(), W_gu.contiguous(), W_d.contiguous()
+        self.s_gu = self.s_d = None
+        if eight:
+            if tuple(s_gu.shape) != (E, 2 * I) or tuple(s_d.shape) != (E, H):
+                raise LoraError("s_gu must be [E, 2I] and s_d [E, H]")
+            self.s_gu, self.s_d = s_gu.float().contiguous(), s_d.float().contiguous()
+        self.E, self.H, self.I, self.topk = E, H, I, int(topk)
+        self.c = lora_moe_experts_t(LORA_E4M3 if eight else LORA_BF16, E, H, I, self.topk,
+                                    1 if renormalize else 0, _ptr(self.router), _ptr(self.W_gu),
+                                    _ptr(self.W_d), _ptr(self.s_gu), _ptr(self.s_d))
+        self.ref = ctypes.pointer(self.c)
+
+
+def lora_moe_decode_workspace_size(w: Optional[MoeWeights], experts: MoeExperts, M: int) -> int:
+    return int(lib.lora_moe_decode_workspace_size(ctypes.byref(w.c) if w is not None else None,
+                                                  experts.ref, M))
+
+
+def lora_moe_decode(w: Optional[MoeWeights], experts: MoeExperts, ids: Optional[torch.Tensor],
+                    x: torch.Tensor, out: torch.Tensor, ws: Workspace,
+                    topk_ids: Optional[torch.Tensor] = None,
+                    topk_weights: Optional[torch.Tensor] = None, stream=None) -> None:
+    """A whole MoE layer for up to 64 tokens in two launches: router, top-k,
+    experts and the adapters' deltas; `out` is overwritten.  w None: no
+    adapters (ids may be None).  topk_ids int32 and topk_weights fp32
+    [M, topk] receive the routing when given."""
+    _check_io(torch.bfloat16, x=x, out=out)
+    _cols(x, "x", experts.H)
+    _cols(out, "out", experts.H)
+    M = x.shape[0]
+    if out.shape[0] != M:
+        raise LoraError("x and out must have the same number of rows")
+    if w is not None:
+        if ids is None or _ids_arg(ids) != M:
+            raise LoraError("ids must have one entry per row of x")
+        _check_io(torch.bfloat16, adapters=w.A_gu)
+    ldx, ldo = _rows(x, "x"), _rows(out, "out")
+    for n, t, dt in (("topk_ids", topk_ids, torch.int32),
+                     ("topk_weights", topk_weights, torch.float32)):
+        if t is not None and (t.dtype != dt or tuple(t.shape) != (M, experts.topk)
+                              or not t.is_contiguous() or not t.is_cuda):
+            raise LoraError(f"{n} must be a contiguous {dt} device tensor [M, topk]")
+    check(lib.lora_moe_decode(ctypes.byref(w.c) if w is not None else None, experts.ref,
+                              _ptr(ids), _ptr(x), ldx, M, _ptr(out), ldo, _ptr(topk_ids),
+                              _ptr(topk_weights), ws.ptr, ws.nbytes, stream_handle(stream)),
+          "lora_moe_decode")

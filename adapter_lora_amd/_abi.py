@@ -11,7 +11,7 @@ LIB_PATH = os.environ.get("MLORA_LIB", os.path.join(HERE, "libmlora.so"))
 
 LORA_OK, LORA_INVALID_ARG, LORA_UNSUPPORTED, LORA_HIP_ERROR = 0, 1, 2, 3
 LORA_DEVERR_WAIT, LORA_DEVERR_BAD_ID, LORA_DEVERR_TABLE = 1, 2, 4
-LORA_F32, LORA_BF16 = 0, 1
+LORA_F32, LORA_BF16, LORA_E4M3 = 0, 1, 2
 LORA_MAX_SLICES = 4
 LORA_RANK_ALIGN = 16
 LORA_MAX_RANK = 64
@@ -19,7 +19,7 @@ LORA_MAX_ADAPTERS = 1024
 LORA_DECODE_MAX_M = 64
 LORA_NOALLOC_SCRATCH_BYTES = 1 << 20
 LORA_TILE_ROWS = 64
-MLORA_ABI_VERSION = 5
+MLORA_ABI_VERSION = 6
 
 
 class LoraError(RuntimeError):
@@ -64,10 +64,18 @@ class lora_moe_align_t(ctypes.Structure):
                 ("max_tokens_padded", I32), ("block_size_m", I32)]
 
 
+class lora_moe_experts_t(ctypes.Structure):
+    _fields_ = [("wdtype", I32), ("E", I32), ("H", I32), ("I", I32), ("topk", I32),
+                ("renormalize", I32),
+                ("router", P), ("W_gu", P), ("W_d", P), ("s_gu", P), ("s_d", P)]
+
+
 PW = ctypes.POINTER(lora_weights_t)
 PS = ctypes.POINTER(lora_segments_t)
 PMW = ctypes.POINTER(lora_moe_weights_t)
 PMA = ctypes.POINTER(lora_moe_align_t)
+PME = ctypes.POINTER(lora_moe_experts_t)
+F32 = ctypes.c_float
 
 # name -> (restype, argtypes); this table is also the list of exported symbols
 SIGNATURES = {
@@ -98,6 +106,11 @@ SIGNATURES = {
     "lora_moe_silu_and_mul": (I32, [I32, P, I64, P, I64, I32, I32, P]),
     "lora_moe_down_add": (I32, [PMW, P, I64, I32, I32, PMA, P, I64, P, SZ, P]),
     "lora_moe_topk_reduce": (I32, [I32, P, I64, P, P, I64, I32, I32, I32, P]),
+    "lora_rms_norm": (I32, [I32, P, I64, P, I64, P, F32, I32, I32, P, I64, P, I64, P, I64, P, P]),
+    "lora_quantize_rows": (I32, [I32, P, I64, I32, I32, P, I64, P, P]),
+    "lora_linear_fp8": (I32, [PW, P, I64, P, P, I64, P, P, I64, I32, PS, P, I64, P, SZ, P]),
+    "lora_moe_decode_workspace_size": (SZ, [PMW, PME, I32]),
+    "lora_moe_decode": (I32, [PMW, PME, P, P, I64, I32, P, I64, P, P, P, SZ, P]),
 }
 
 for _name, (_res, _args) in SIGNATURES.items():

@@ -662,4 +662,179 @@ lora_status lora_moe_topk_reduce(int32_t dtype, const void* cache3, int64_t ld3,
                                        stream));
 }
 
+// ------------------------------------------------------------------ 8-bit decoder layer
+lora_status lora_rms_norm(int32_t dtype, const void* x, int64_t ldx, const void* residual,
+                          int64_t ldr, const void* weight, float eps, int32_t M, int32_t K,
+                          void* residual_out, int64_t ldro, void* out, int64_t ldo, void* out8,
+                          int64_t ldo8, float* scale, hipStream_t stream) {
+    const Range range("lora_rms_norm");
+    if (dtype != LORA_F32 && dtype != LORA_BF16) return LORA_INVALID_ARG;
+    if (M < 0 || K <= 0 || K % 8) return LORA_INVALID_ARG;
+    if (K > kNormMaxK) return LORA_UNSUPPORTED;
+    if (M == 0) return LORA_OK;
+    if ((!out && !out8) || !scale != !out8 || (residual_out && !residual)) return LORA_INVALID_ARG;
+    if (!(eps >= 0.f)) return LORA_INVALID_ARG;
+    lora_status st = check_rows(x, ldx, K);
+    if (st == LORA_OK) st = check_rows(weight, K, K);
+    if (st == LORA_OK && residual) st = check_rows(residual, ldr, K);
+    if (st == LORA_OK && residual_out) st = check_rows(residual_out, ldro, K);
+    if (st == LORA_OK && out) st = check_rows(out, ldo, K);
+    if (st == LORA_OK && out8) st = check_rows(out8, ldo8, K);
+    if (st != LORA_OK) return st;
+    const NormParams p{x, ldx, residual, ldr, residual_out, ldro, weight, eps, out, ldo,
+                       static_cast<uint8_t*>(out8), ldo8, scale, M, K};
+    return from_hip(launch_rms_norm(dtype, p, stream));
+}
+
+lora_status lora_quantize_rows(int32_t dtype, const void* x, int64_t ldx, int32_t M, int32_t K,
+                               void* out8, int64_t ldo8, float* scale, hipStream_t stream) {
+    const Range range("lora_quantize_rows");
+    if (dtype != LORA_F32 && dtype != LORA_BF16) return LORA_INVALID_ARG;
+    if (M < 0 || K <= 0 || K % 8) return LORA_INVALID_ARG;
+    if (K > kNormMaxK) return LORA_UNSUPPORTED;
+    if (M == 0) return LORA_OK;
+    lora_status st = check_rows(x, ldx, K);
+    if (st == LORA_OK) st = check_rows(out8, ldo8, K);
+    if (st != LORA_OK) return st;
+    if (!scale) return LORA_INVALID_ARG;
+    const NormParams p{x, ldx, nullptr, 0, nullptr, 0, nullptr, 0.f, nullptr, 0,
+                       static_cast<uint8_t*>(out8), ldo8, scale, M, K};
+    return from_hip(launch_rms_norm(dtype, p, stream));
+}
+
+// rows of 8-bit values read 16 bytes at a time
+static lora_status check_rows8(const void* p, int64_t ld, int64_t width) {
+    if (!p || !aligned16(p) || ld < width || ld % 16 != 0) return LORA_INVALID_ARG;
+    return LORA_OK;
+}
+
+lora_status lora_linear_fp8(const lora_weights_t* w, const void* W8, int64_t ldw,
+                            const float* w_scale, const void* x8, int64_t ldx8,
+                            const float* x_scale, const void* x, int64_t ldx, int32_t M,
+                            const lora_segments_t* seg, void* y, int64_t ldy, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream) {
+    const Range range("lora_linear_fp8");
+    lora_status st = check_weights(w);
+    if (st != LORA_OK) return st;
+    if (w->dtype != LORA_BF16 || w->K % 16) return LORA_UNSUPPORTED;
+    if (M < 0 || M > (1 << 24)) return LORA_INVALID_ARG;
+    if ((st = check_segments(seg, w, M)) != LORA_OK) return st;
+    if (M == 0) return LORA_OK;
+    if ((st = check_rows8(W8, ldw, w->K)) != LORA_OK) return st;
+    if ((st = check_rows8(x8, ldx8, w->K)) != LORA_OK) return st;
+    if ((st = check_rows(x, ldx, w->K)) != LORA_OK) return st;
+    if ((st = check_rows(y, ldy, n_total(w))) != LORA_OK) return st;
+    if (!w_scale || !x_scale) return LORA_INVALID_ARG;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)))
+        return LORA_INVALID_ARG;
+    const LinearWs L = layout_for(w, M);
+    if (workspace_bytes < L.total) return LORA_INVALID_ARG;
+    LinearArgs a = make_args(w, seg, M);
+    a.err = ws_error(workspace);
+    if (M <= LORA_DECODE_MAX_M)
+        return from_hip(launch_linear_fp8(a, W8, ldw, w_scale, x8, ldx8, x_scale, x, ldx, y, ldy,
+                                          workspace, stream));
+    float* S = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + L.S);
+    hipError_t e = launch_shrink(a, x, ldx, S, workspace, stream);
+    if (e != hipSuccess) return LORA_HIP_ERROR;
+    return from_hip(launch_gemm_fp8(a, x8, ldx8, x_scale, W8, ldw, w_scale, S, y, ldy, stream));
+}
+
+static lora_status check_experts(const lora_moe_experts_t* ex, const lora_moe_weights_t* w) {
+    if (!ex) return LORA_INVALID_ARG;
+    if (ex->wdtype != LORA_BF16 && ex->wdtype != LORA_E4M3) return LORA_INVALID_ARG;
+    const int q = ex->wdtype == LORA_E4M3 ? 16 : 8;
+    if (ex->E < 1 || ex->E > 256 || ex->topk < 1 || ex->topk > 16 || ex->topk > ex->E)
+        return LORA_INVALID_ARG;
+    if (ex->H <= 0 || ex->H % q || ex->I <= 0 || ex->I % q) return LORA_INVALID_ARG;
+    if (!ex->router || !ex->W_gu || !ex->W_d || !aligned16(ex->router) || !aligned16(ex->W_gu) ||
+        !aligned16(ex->W_d))
+        return LORA_INVALID_ARG;
+    if ((ex->wdtype == LORA_E4M3) != (ex->s_gu != nullptr) || !ex->s_gu != !ex->s_d)
+        return LORA_INVALID_ARG;
+    if (!w) return LORA_OK;
+    const lora_status st = check_moe_weights(w);
+    if (st != LORA_OK) return st;
+    if (w->dtype != LORA_BF16) return LORA_UNSUPPORTED;
+    return w->E == ex->E && w->H == ex->H && w->I == ex->I ? LORA_OK : LORA_INVALID_ARG;
+}
+
+namespace {
+// header | routing slots [2][P] | chosen experts [P] | S of gate/up [P][r] |
+// S of down [P][r] | joined partial sums [splits - 1][M][H] | h [P][I]
+struct MoeDecodeWs {
+    size_t route, ids, s_gu, s_d, join, h, total;
+};
+
+MoeDecodeWs moe_decode_ws(const lora_moe_experts_t* ex, int r, int M) {
+    MoeDecodeWs l{};
+    const size_t P = (size_t)M * ex->topk;
+    size_t off = up(sizeof(WsHeader));
+    auto take = [&off](size_t bytes) {
+        const size_t at = off;
+        off += up(bytes);
+        return at;
+    };
+    l.route = take(2 * P * sizeof(slot_t));
+    l.ids = take(P * sizeof(int32_t));
+    l.s_gu = take(P * r * sizeof(slot_t));
+    l.s_d = take(P * r * sizeof(slot_t));
+    l.join = take((size_t)(moe_decode_splits(ex->H, ex->I) - 1) * M * ex->H * sizeof(slot_t));
+    l.h = take(P * ex->I * sizeof(uint16_t));
+    l.total = off;
+    return l;
+}
+}  // namespace
+
+size_t lora_moe_decode_workspace_size(const lora_moe_weights_t* w, const lora_moe_experts_t* ex,
+                                      int32_t M) {
+    if (check_experts(ex, w) != LORA_OK || M < 0 || M > LORA_DECODE_MAX_M) return 0;
+    return moe_decode_ws(ex, w ? w->r : 0, M).total;
+}
+
+lora_status lora_moe_decode(const lora_moe_weights_t* w, const lora_moe_experts_t* ex,
+                            const int32_t* ids, const void* x, int64_t ldx, int32_t M, void* out,
+                            int64_t ldo, int32_t* topk_ids, float* topk_weights, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream) {
+    const Range range("lora_moe_decode");
+    lora_status st = check_experts(ex, w);
+    if (st != LORA_OK) return st;
+    if (M < 0) return LORA_INVALID_ARG;
+    if (M > LORA_DECODE_MAX_M) return LORA_UNSUPPORTED;
+    if (M == 0) return LORA_OK;
+    if (w && !ids) return LORA_INVALID_ARG;
+    if ((st = check_rows(x, ldx, ex->H)) != LORA_OK) return st;
+    if ((st = check_rows(out, ldo, ex->H)) != LORA_OK) return st;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)))
+        return LORA_INVALID_ARG;
+    const MoeDecodeWs l = moe_decode_ws(ex, w ? w->r : 0, M);
+    if (workspace_bytes < l.total) return LORA_INVALID_ARG;
+    char* ws = static_cast<char*>(workspace);
+    auto u16 = [](const void* q) { return static_cast<const uint16_t*>(q); };
+    MoeDecodeParams p{};
+    p.M = M; p.topk = ex->topk; p.E = ex->E; p.H = ex->H; p.I = ex->I;
+    p.renorm = ex->renormalize != 0;
+    p.x = u16(x); p.ldx = ldx;
+    p.router = u16(ex->router);
+    p.W_gu = ex->W_gu; p.W_d = ex->W_d; p.s_gu = ex->s_gu; p.s_d = ex->s_d;
+    if (w) {
+        p.L = w->L; p.r = w->r; p.shared_outer = w->shared_outer != 0;
+        p.A_gu = u16(w->A_gu); p.B_gu = u16(w->B_gu); p.A_d = u16(w->A_d); p.B_d = u16(w->B_d);
+        p.enabled = w->adapter_enabled;
+    }
+    p.ids = ids;
+    p.out = static_cast<uint16_t*>(out); p.ldo = ldo;
+    p.out_ids = topk_ids; p.out_w = topk_weights;
+    p.err = ws_error(workspace);
+    p.route = reinterpret_cast<slot_t*>(ws + l.route);
+    p.route_ids = reinterpret_cast<int32_t*>(ws + l.ids);
+    p.S_gu = reinterpret_cast<slot_t*>(ws + l.s_gu);
+    p.S_d = reinterpret_cast<slot_t*>(ws + l.s_d);
+    p.join = reinterpret_cast<slot_t*>(ws + l.join);
+    p.h = reinterpret_cast<uint16_t*>(ws + l.h);
+    p.splits = moe_decode_splits(ex->H, ex->I);
+    p.wc = wait_ctl();
+    return from_hip(launch_moe_decode(p, stream));
+}
+
 }  // extern "C"

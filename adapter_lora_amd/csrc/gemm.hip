@@ -479,3 +479,5 @@ hipError_t launch_gemm_lora(const LinearArgs& a, const void* x, int64_t ldx, con
 }
 
 }  // namespace mlora
+
+#include "gemm_fp8.hpp"

@@ -203,4 +203,74 @@ hipError_t launch_silu_and_mul(int dtype, const void* c1, int64_t ld1, void* c2,
 hipError_t launch_topk_reduce(int dtype, const void* c3, int64_t ld3, const float* w, void* out,
                               int64_t ldo, int M, int topk, int H, hipStream_t st);
 
+// Root-mean-square norm of rows with the residual's addition and an output
+// in 8 bits (norm.hpp).  K <= kNormMaxK.
+constexpr int kNormMaxK = 32768;
+
+struct NormParams {
+    const void* x;
+    int64_t ldx;
+    const void* res;        // null: none
+    int64_t ldr;
+    void* res_out;          // null: none
+    int64_t ldro;
+    const void* w;          // null: quantization only
+    float eps;
+    void* out;              // null: none
+    int64_t ldo;
+    uint8_t* out8;          // null: none
+    int64_t ldo8;
+    float* scale;
+    int M, K;
+};
+
+hipError_t launch_rms_norm(int dtype, const NormParams& p, hipStream_t st);
+
+// y = xs ws (x8 W8^T) + S B_i^T on e4m3 operands.  M <= LORA_DECODE_MAX_M in
+// one launch (linear_fp8.hpp); any M from S (fp32 [M][cols], sorted rows) with
+// launch_gemm_fp8 (gemm_fp8.hpp).
+hipError_t launch_linear_fp8(const LinearArgs& a, const void* W8, int64_t ldw, const float* w_scale,
+                             const void* x8, int64_t ldx8, const float* x_scale, const void* x,
+                             int64_t ldx, void* y, int64_t ldy, void* ws, hipStream_t st);
+hipError_t launch_gemm_fp8(const LinearArgs& a, const void* x8, int64_t ldx8, const float* x_scale,
+                           const void* W8, int64_t ldw, const float* w_scale, const float* S, void* y,
+                           int64_t ldy, hipStream_t st);
+
+// A whole MoE layer for few tokens (moe_decode.hpp).
+struct MoeDecodeParams {
+    int M, topk, E, H, I, renorm;
+    int L, r, shared_outer;       // L == 0: no adapters
+    const uint16_t* x;
+    int64_t ldx;
+    const uint16_t* router;
+    const void* W_gu;
+    const void* W_d;
+    const float* s_gu;
+    const float* s_d;
+    const uint16_t* A_gu;
+    const uint16_t* B_gu;
+    const uint16_t* A_d;
+    const uint16_t* B_d;
+    const int32_t* enabled;
+    const int32_t* ids;
+    uint16_t* out;
+    int64_t ldo;
+    int32_t* out_ids;             // null: not wanted
+    float* out_w;                 // null: not wanted
+    int* err;
+    slot_t* route;                // [2][P]: expert, weight
+    int32_t* route_ids;           // [P], read by the second launch
+    slot_t* S_gu;                 // [P][r]
+    slot_t* S_d;                  // [P][r]
+    slot_t* join;                 // [splits - 1][M][H]
+    uint16_t* h;                  // [P][I]
+    int splits;
+    WaitCtl wc;
+};
+
+// Workgroups that share one tile of 16 output columns of the second launch.
+int moe_decode_splits(int H, int I);
+
+hipError_t launch_moe_decode(const MoeDecodeParams& p, hipStream_t st);
+
 }  // namespace mlora

@@ -560,3 +560,5 @@ hipError_t launch_topk_reduce(int dtype, const void* c3, int64_t ld3, const floa
 }
 
 }  // namespace mlora
+
+#include "moe_decode.hpp"

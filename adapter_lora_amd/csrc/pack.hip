@@ -95,3 +95,5 @@ hipError_t launch_pack_embedding_adapter(int dtype, int vocab, int64_t emb, int 
 }
 
 }  // namespace mlora
+
+#include "norm.hpp"

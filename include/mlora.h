@@ -53,7 +53,7 @@
 extern "C" {
 #endif
 
-#define MLORA_ABI_VERSION 5
+#define MLORA_ABI_VERSION 6
 
 typedef enum lora_status {
     LORA_OK = 0,
@@ -64,7 +64,8 @@ typedef enum lora_status {
 
 typedef enum lora_dtype {
     LORA_F32 = 0,
-    LORA_BF16 = 1
+    LORA_BF16 = 1,
+    LORA_E4M3 = 2 /* OCP e4m3 (largest value 448): 8-bit outputs and weights, with fp32 scales */
 } lora_dtype;
 
 #define LORA_MAX_SLICES 4      /* stacked output slices per call (QKV = 3, gate-up = 2) */
@@ -529,6 +530,119 @@ lora_status lora_moe_down_add(const lora_moe_weights_t* w, const void* cache2, i
 lora_status lora_moe_topk_reduce(int32_t dtype, const void* cache3, int64_t ld3,
                                  const float* topk_weights, void* out, int64_t ldo, int32_t M,
                                  int32_t topk, int32_t H, hipStream_t stream);
+
+/* ---------------------------------------------------------------- 8-bit decoder layer */
+
+/*
+ * lora_rms_norm: the residual's addition and the root-mean-square norm
+ * before a projection, with the two forms of its output that the projection
+ * and the adapters beside it read.  For every row m, in fp32:
+ *     h               = x[m] + residual[m]            (x[m] without a residual)
+ *     residual_out[m] = h                             rounded to dtype
+ *     v               = h * weight / sqrt(mean(h^2) + eps)
+ *     out[m]          = v                             rounded to dtype
+ *     scale[m]        = max|v| / 448
+ *     out8[m]         = v / scale[m]                  rounded to e4m3 (nearest even)
+ * A row of zeros has scale 1; a scale is at least 2^-126.  A NaN in v makes
+ * its row's scale NaN and with it the whole row of out8; an infinity makes the
+ * scale infinite and its own value NaN, the row's others 0.
+ *   x, weight [K], residual, residual_out, out: dtype (LORA_BF16, LORA_F32);
+ *   out8 device e4m3 [M, ldo8], scale device fp32 [M].
+ * residual NULL: no addition (residual_out must be NULL too).  residual_out,
+ * out and (out8 with scale) may each be NULL, but not all of out and out8.
+ * residual_out may be the buffer of residual or of x, and out that of x, each
+ * with the same leading dimension; other overlaps are not allowed.
+ * K a multiple of 8, at most 32768 (LORA_UNSUPPORTED past it); ld* >= K and a
+ * multiple of 8; every pointer 16-byte aligned (scale: 4).
+ */
+lora_status lora_rms_norm(int32_t dtype, const void* x, int64_t ldx, const void* residual,
+                          int64_t ldr, const void* weight, float eps, int32_t M, int32_t K,
+                          void* residual_out, int64_t ldro, void* out, int64_t ldo, void* out8,
+                          int64_t ldo8, float* scale, hipStream_t stream);
+
+/*
+ * lora_quantize_rows: the 8-bit form alone, scale[m] = max|x[m]| / 448 and
+ * out8[m] = x[m] / scale[m], with the rules of lora_rms_norm: base weights
+ * [N, K] at load time (one scale per output column), activations that no
+ * norm precedes.
+ */
+lora_status lora_quantize_rows(int32_t dtype, const void* x, int64_t ldx, int32_t M, int32_t K,
+                               void* out8, int64_t ldo8, float* scale, hipStream_t stream);
+
+/*
+ * lora_linear_fp8: a shared projection held in 8 bits, written together with
+ * the batch's adapter deltas (the layer output of lora_linear_fused with base
+ * operands in e4m3):
+ *     y[m, n] = x_scale[m] w_scale[n] sum_k x8[m, k] W8[n, k]
+ *             + sum_{j < rp} S[p, sl, j] B_i[n, j],    S = x A_i^T
+ * for every token m (sorted position p, adapter i, slice sl holding n); the
+ * delta is absent for tokens without an adapter and for rank-0 slots.
+ * M <= LORA_DECODE_MAX_M: one launch (S crosses it through tagged exchange
+ * slots in `workspace`, as in lora_shrink_expand_add); larger M: lora_shrink
+ * into `workspace`, then one product.
+ * W8 device e4m3 [n_total, ldw] row-major (the slices of w stacked in order),
+ *    w_scale device fp32 [n_total]; x8 device e4m3 [M, ldx8], x_scale device
+ *    fp32 [M] (lora_rms_norm's out8 and scale); ldw, ldx8 >= K, multiples of
+ *    16, 16-byte aligned pointers; K a multiple of 16 (LORA_UNSUPPORTED else).
+ * x  device bf16 [M, ldx]: what the adapters read (lora_rms_norm's out).
+ * y  device bf16 [M, ldy], overwritten (never read).
+ * seg, workspace: as lora_shrink_expand_add.  Only bf16 tables.
+ */
+lora_status lora_linear_fp8(const lora_weights_t* w, const void* W8, int64_t ldw,
+                            const float* w_scale, const void* x8, int64_t ldx8,
+                            const float* x_scale, const void* x, int64_t ldx, int32_t M,
+                            const lora_segments_t* seg, void* y, int64_t ldy, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Router and experts of one MoE layer (SGLang "LoRA + MoE" page, the base
+ * products that lora_moe_gate_up_add and lora_moe_down_add add to).
+ *   router device bf16 [E, H];
+ *   W_gu device [E, 2I, H] (gate rows first), W_d device [E, H, I]:
+ *       wdtype LORA_BF16, or LORA_E4M3 with s_gu device fp32 [E, 2I] and
+ *       s_d device fp32 [E, H], one scale per row (NULL for LORA_BF16).
+ * 1 <= topk <= 16, topk <= E <= 256; H, I multiples of 8 (16 for LORA_E4M3).
+ */
+typedef struct lora_moe_experts {
+    int32_t wdtype;          /* LORA_BF16 or LORA_E4M3 */
+    int32_t E, H, I, topk;
+    int32_t renormalize;     /* != 0: the chosen weights are divided by their sum */
+    const void* router;
+    const void* W_gu;
+    const void* W_d;
+    const float* s_gu;
+    const float* s_d;
+} lora_moe_experts_t;
+
+/*
+ * Bytes of device workspace of lora_moe_decode for M tokens (0: invalid
+ * arguments): zero it once (lora_workspace_init) before its first use, order
+ * the calls that share it on one stream.  w may be NULL.
+ */
+size_t lora_moe_decode_workspace_size(const lora_moe_weights_t* w, const lora_moe_experts_t* ex,
+                                      int32_t M);
+
+/*
+ * lora_moe_decode: a whole MoE layer for a few tokens, 0 <= M <=
+ * LORA_DECODE_MAX_M (LORA_UNSUPPORTED past it), in two launches:
+ *     logits = x router^T; the topk largest per token, ties to the lowest
+ *     expert; c = softmax(logits) of the chosen (over all E, then divided by
+ *     their sum when renormalize is set)
+ *     (g, u) = W_gu[e] x + B_gu[l, e] (A_gu[l, e] x)
+ *     h      = c silu(g) u                               rounded to bf16
+ *     out[m] = sum over the chosen e of W_d[e] h + B_d[l, e] (A_d[l, e] h)
+ * with l = ids[m]; a token whose id lies outside [0, L) or whose adapter is
+ * disabled gets no deltas.  Nothing is rounded between but h.
+ *   w NULL: no adapters (ids is not read); else bf16, of the experts' E, H, I;
+ *   ids device [M] int32; x device bf16 [M, ldx]; out device bf16 [M, ldo],
+ *   overwritten; topk_ids device int32 [M, topk] and topk_weights device fp32
+ *   [M, topk] receive the routing, largest first, when not NULL.
+ * Waits inside the launches are bounded (LORA_DEVERR_WAIT in the workspace).
+ */
+lora_status lora_moe_decode(const lora_moe_weights_t* w, const lora_moe_experts_t* ex,
+                            const int32_t* ids, const void* x, int64_t ldx, int32_t M, void* out,
+                            int64_t ldo, int32_t* topk_ids, float* topk_weights, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

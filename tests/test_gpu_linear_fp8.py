@@ -1,0 +1,180 @@
+"""lora_linear_fp8 against the 64-bit oracle, in one launch (M <= 64) and past it.
+
+Tolerance of one output: half a bf16 step, 2^-8 of it, and for the fp32 sums
+(K products in each of two serial sums, S rounded to a bf16 pair) at most
+(2 K + 256) 2^-24 + 2^-16 of the sum of the terms' magnitudes."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import decoder as O
+
+pytestmark = pytest.mark.gpu
+E4M3 = torch.float8_e4m3fn
+F64 = lambda t: t.detach().double().cpu().numpy()     # noqa: E731
+
+
+class Case:
+    def __init__(self, M, K, sizes, ranks, ids, seed=0, integers=False):
+        import adapter_lora_amd as ml
+        g = torch.Generator(device="cuda").manual_seed(seed)
+
+        def rnd(*s, std=1.0):
+            if integers:
+                return torch.randint(-1, 2, s, generator=g, device="cuda").float()
+            return torch.randn(*s, generator=g, device="cuda") * std
+
+        self.M, self.K, self.sizes, self.ranks = M, K, sizes, ranks
+        N, n_sl = sum(sizes), len(sizes)
+        self.x = rnd(M, K).bfloat16()
+        self.x8 = self.x.float().clamp(-440, 440).mul(1 if integers else 60).to(E4M3)
+        self.xs = torch.full((M,), 1.0, device="cuda") if integers else \
+            torch.rand(M, generator=g, device="cuda") * 0.02 + 0.01
+        self.W8 = rnd(N, K, std=60.0).to(E4M3)
+        self.ws = torch.full((N,), 1.0, device="cuda") if integers else \
+            torch.rand(N, generator=g, device="cuda") * 1e-3 + 1e-4
+        self.A = [rnd(n_sl * r, K, std=0.05).bfloat16() for r in ranks]
+        self.B = [rnd(N, r, std=0.05).bfloat16() for r in ranks]
+        L = len(ranks)
+        self.ids = torch.tensor(ids, dtype=torch.int32, device="cuda") if ids is not None else \
+            torch.randint(-1, L, (M,), generator=g, device="cuda").int()
+        self.table = ml.LoraTable(self.A, self.B, ranks, sizes, K, torch.bfloat16)
+        self.seg = ml.Segments(M, L)
+        ml.lora_build_segments(self.ids, self.seg)
+        self.ws_buf = ml.Workspace.for_table(self.table, M)
+        self.N = N
+
+    def run(self, y=None, x8=None, W8=None, x=None, stream=None):
+        import adapter_lora_amd as ml
+        y = torch.full((self.M, self.N), float("nan"), dtype=torch.bfloat16, device="cuda") \
+            if y is None else y
+        ml.lora_linear_fp8(self.table, self.W8 if W8 is None else W8, self.ws,
+                           self.x8 if x8 is None else x8, self.xs, self.x if x is None else x,
+                           self.seg, y, self.ws_buf, stream=stream)
+        return y
+
+    def oracle(self):
+        return O.linear_fp8_mag(F64(self.x8.float()), F64(self.xs), F64(self.W8.float()),
+                                F64(self.ws), F64(self.x), self.ids.cpu().numpy(),
+                                [F64(a) for a in self.A], [F64(b) for b in self.B], self.ranks,
+                                self.sizes)
+
+    def check(self, y):
+        import adapter_lora_amd as ml
+        want, mag = self.oracle()
+        unit = (2 * self.K + 256) * 2.0 ** -24 + 2.0 ** -16
+        got = F64(y)
+        bad = ~(np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + unit * mag)
+        assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4].tolist())
+        assert ml.lora_read_device_error(self.ws_buf.buf) == 0
+
+
+CASES = {
+    "one_token": (1, 512, [256], [16], [0]),
+    "one_token_none": (1, 512, [256], [16], [-1]),
+    "walkthrough": (3, 4096, [512, 128, 128], [16, 64, 32], [0, 2, -1]),
+    "short_k": (5, 16, [8], [8], None),
+    "ragged": (17, 1040, [40, 24, 8], [20, 0, 64, 8], None),
+    "sixteen": (16, 2048, [264], [64, 16], None),
+    "own_adapter_each": (32, 768, [96, 72], [16, 32, 64] * 11, list(range(31)) + [-1]),
+    "one_segment": (64, 1040, [160], [64], [0] * 64),
+    "no_adapter_at_all": (48, 512, [128], [16, 32], [-1] * 48),
+    "rank0_only": (9, 256, [64], [0, 0], None),
+    "ids_outside": (20, 256, [64], [16, 32], [0, 1, 2, 7, -1, -5, 1000, 0, 1, 1] * 2),
+    "full_decode": (64, 512, [200, 56], [16, 0, 64, 20] * 10, None),
+    "many_slots": (64, 256, [48], [16] * 300, None),
+    "four_slices": (33, 272, [16, 8, 24, 264], [64, 32], None),
+    "past_decode": (65, 512, [256], [16, 32], None),
+    "prefill_ragged": (300, 1040, [264, 72, 8], [20, 0, 64, 8], None),
+    "prefill_none": (130, 256, [320], [16], [-1] * 130),
+    "prefill_long_k": (129, 4112, [256], [64, 16], None),
+    "prefill_many_slots": (257, 128, [512], [16, 32] * 40, None),
+}
+
+
+@pytest.mark.parametrize("name", list(CASES))
+def test_linear_fp8_matches_oracle(name):
+    print(name, flush=True)
+    M, K, sizes, ranks, ids = CASES[name]
+    c = Case(M, K, sizes, ranks, ids)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("M", [7, 40, 200])
+def test_linear_fp8_integers_bit_exact(M):
+    """Factors in {-1, 0, 1} with unit scales: every sum is a small integer,
+    exact in fp32, and outputs up to 256 are exact in bf16."""
+    c = Case(M, 64, [64, 32], [16, 32, 0], None, seed=3, integers=True)
+    want, mag = c.oracle()
+    got = F64(c.run())
+    small = np.abs(want) <= 256
+    assert small.any() and np.array_equal(got[small], want[small])
+
+
+@pytest.mark.parametrize("M", [20, 100])
+def test_linear_fp8_strided_operands_and_neighbours(M):
+    """x, x8, W8 and y inside wider buffers whose padding is NaN or a
+    sentinel: neither is read into a result nor written."""
+    c = Case(M, 528, [120, 40], [16, 64, 0], None, seed=4)
+    nan8 = 0x7f
+
+    def wide8(t, pad):
+        buf = torch.full((t.shape[0] + 1, t.shape[1] + pad), nan8, dtype=torch.uint8, device="cuda")
+        v = buf.view(E4M3)[:t.shape[0], 16:16 + t.shape[1]]
+        buf[:t.shape[0], 16:16 + t.shape[1]] = t.view(torch.uint8)
+        return v
+
+    xw = torch.full((M, 528 + 16), float("nan"), dtype=torch.bfloat16, device="cuda")
+    xw[:, 8:536] = c.x
+    yw = torch.full((M + 1, 160 + 24), 5.0, dtype=torch.bfloat16, device="cuda")
+    y = c.run(y=yw[:M, 8:168], x8=wide8(c.x8, 48), W8=wide8(c.W8, 32), x=xw[:, 8:536])
+    c.check(y)
+    assert (yw[M] == 5).all() and (yw[:, :8] == 5).all() and (yw[:, 168:] == 5).all()
+
+
+@pytest.mark.parametrize("M", [24, 150])
+def test_linear_fp8_repeats_bit_identical(M):
+    """One workspace for many calls, on two streams in turn: the same bits."""
+    c = Case(M, 1040, [264], [16, 32, 64], None, seed=5)
+    first = c.run()
+    c.check(first)
+    side = torch.cuda.Stream()
+    for i in range(6):
+        torch.cuda.synchronize()
+        again = c.run(stream=side if i % 2 else None)
+        torch.cuda.synchronize()
+        assert torch.equal(first, again)
+
+
+def test_linear_fp8_nan_stays_in_its_row():
+    c = Case(40, 512, [64], [16, 32], None, seed=6)
+    clean = F64(c.run())
+    c.x8.view(torch.uint8)[3, 100] = 0x7f
+    y = F64(c.run())
+    assert np.isnan(y[3]).all()
+    rest = [m for m in range(40) if m != 3]
+    assert np.array_equal(y[rest], clean[rest])
+
+
+@pytest.mark.parametrize("M", [32, 200])
+def test_linear_fp8_graph_replays(M):
+    """Captured once, replayed with new inputs and eager work between."""
+    c, d = Case(M, 512, [128], [16, 32], None, seed=7), Case(M, 512, [128], [16, 32], None, seed=8)
+    y = torch.zeros(M, 128, dtype=torch.bfloat16, device="cuda")
+    c.run(y)
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        c.run(y, stream=torch.cuda.current_stream())
+    for i in range(5):
+        src = d if i % 2 else c
+        x8, xs, x = src.x8.clone(), src.xs.clone(), src.x.clone()
+        c.x8.copy_(x8), c.xs.copy_(xs), c.x.copy_(x)
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = y.clone()
+        assert torch.equal(got, c.run())
+        torch.cuda.synchronize()
+        c.check(got)
