@@ -779,7 +779,7 @@ MoeDecodeWs moe_decode_ws(const lora_moe_experts_t* ex, int r, int M) {
     l.ids = take(P * sizeof(int32_t));
     l.s_gu = take(P * r * sizeof(slot_t));
     l.s_d = take(P * r * sizeof(slot_t));
-    l.join = take((size_t)(moe_decode_splits(ex->H, ex->I) - 1) * M * ex->H * sizeof(slot_t));
+    l.join = take((size_t)(moe_decode_splits(ex->H) - 1) * M * ex->H * sizeof(slot_t));
     l.h = take(P * ex->I * sizeof(uint16_t));
     l.total = off;
     return l;
@@ -832,7 +832,7 @@ lora_status lora_moe_decode(const lora_moe_weights_t* w, const lora_moe_experts_
     p.S_d = reinterpret_cast<slot_t*>(ws + l.s_d);
     p.join = reinterpret_cast<slot_t*>(ws + l.join);
     p.h = reinterpret_cast<uint16_t*>(ws + l.h);
-    p.splits = moe_decode_splits(ex->H, ex->I);
+    p.splits = moe_decode_splits(ex->H);
     p.wc = wait_ctl();
     return from_hip(launch_moe_decode(p, stream));
 }

@@ -31,13 +31,16 @@
 
 #include "common.hpp"
 #include "kernels.hpp"
+#include "row_stage.hpp"
 
 namespace mlora {
 
-constexpr int kMdThreads = 512;
+constexpr int kMdThreads = 256;
 constexpr int kMdWaves = kMdThreads / kWave;
+constexpr int kMdResident = 3 * 256;           // workgroups: three per compute unit
 constexpr int kMdMaxE = 256;
 constexpr int kMdMaxPairs = LORA_DECODE_MAX_M * 16;
+constexpr int kMdMaxGroups = kMdMaxE + kMdMaxPairs / 33 + 1;   // a second group takes 33 tokens
 
 __device__ __forceinline__ uint32_t md_hi_lo(float f) {
     const uint32_t h = f32_to_bf16(f);
@@ -55,6 +58,28 @@ __device__ __forceinline__ uint32_t slot_wait(const slot_t* s, uint32_t want, in
     }
     *lost |= !slot_full(v, want);
     return (uint32_t)v;
+}
+
+// Eight consecutive slots, their loads in flight together; zeros unless `on`.
+__device__ __forceinline__ void slot_wait8(const slot_t* s, bool on, uint32_t want, int max_spin, bool* lost,
+                                           uint32_t* w) {
+    for (int spin = 0;; ++spin) {
+        slot_t v[8];
+        bool full = true;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = on ? slot_load(s + q) : 0ull;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            full &= slot_full(v[q], want);
+            w[q] = (uint32_t)v[q];
+        }
+        if (__ballot(on && !full) == 0ull) break;
+        if (spin >= max_spin) {
+            *lost |= on && !full;
+            break;
+        }
+        __builtin_amdgcn_s_sleep(1);
+    }
 }
 
 typedef __bf16 md_bf16x2_t __attribute__((ext_vector_type(2)));
@@ -80,6 +105,10 @@ __device__ __forceinline__ void widen16(const uint4& q, uint4& a, uint4& b) {
     a = make_uint4(o[0], o[1], o[2], o[3]);
     b = make_uint4(o[4], o[5], o[6], o[7]);
 }
+
+// S values of the gate / up products that a workgroup keeps in LDS; a call with
+// more (pairs times rank) reads the slots again for every unit.
+constexpr int kMdMaxS = 4096;
 
 // Adapter of token m, or -1 (none, disabled, or outside the table).
 __device__ __forceinline__ int md_adapter(const MoeDecodeParams& p, int m) {
@@ -156,38 +185,38 @@ __device__ __forceinline__ void md_router(const MoeDecodeParams& p, uint32_t tag
 }
 
 // ---------------------------------------------------------------- shrink of one pair
-// S[j] = A[j, :] . v over K for the rank's r rows: wave w takes rows w, w + 8, ...
-__device__ __forceinline__ void md_shrink(const uint16_t* A, const uint16_t* v, int K, int r, slot_t* S,
-                                          uint32_t tag) {
-    const int lane = lane_id(), wave = (int)threadIdx.x / kWave;
-    for (int j = wave * 2; j < r; j += 2 * kMdWaves) {         // r is a multiple of 16
-        const uint16_t* a0 = A + (int64_t)j * K;
-        const uint16_t* a1 = a0 + K;
-        float c0 = 0.f, c1 = 0.f;
+// S[j] = A[j, :] . v over K for 16 of the rank's rows, four a wavefront.
+__device__ __forceinline__ void md_shrink(const uint16_t* A, const uint16_t* v, int K, slot_t* S, uint32_t tag) {
+    const int lane = lane_id(), j = (int)threadIdx.x / kWave * 4;
+    const uint16_t* a = A + (int64_t)j * K;
+    float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-        for (int k = lane * 8; k < K; k += kWave * 8) {
-            const uint4 t = ld16(v + k);
-            c0 = md_dot8(ld16(a0 + k), t, c0);
-            c1 = md_dot8(ld16(a1 + k), t, c1);
-        }
-        c0 = wave_total(c0);
-        c1 = wave_total(c1);
-        if (lane == 0) {
-            slot_put(S + j, __uint_as_float(md_hi_lo(c0)), tag);
-            slot_put(S + j + 1, __uint_as_float(md_hi_lo(c1)), tag);
-        }
+    for (int k = lane * 8; k < K; k += kWave * 8) {
+        const uint4 t = ld16(v + k);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) c[q] = md_dot8(ld16(a + (int64_t)q * K + k), t, c[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        c[q] = wave_total(c[q]);
+        if (lane == 0) slot_put(S + j + q, __uint_as_float(md_hi_lo(c[q])), tag);
     }
 }
+static_assert(kMdWaves * 4 == 16, "a shrink workgroup takes 16 rows");
 
 // ---------------------------------------------------------------- routing tables in LDS
 struct MdRoute {
     unsigned long long mask[kMdMaxE];      // tokens of each expert
     int16_t active[kMdMaxE];               // experts with tokens, ascending
+    int16_t group[kMdMaxGroups];           // groups of up to 32 of an expert's tokens: expert, and
+                                           // 256 times the group's number within it
+    int16_t base[kMdMaxE];                 // an expert's first place in `list`
     int16_t exp_[kMdMaxPairs];             // expert of a pair, -1: none
-    int n_active;
+    int16_t list[kMdMaxPairs];             // pairs by expert, then token
+    int n_active, n_groups, n_max;         // experts with tokens; groups; most tokens of one expert
 };
 
-// After exp_ is filled: masks and the list of active experts.  Ends with a barrier.
+// After exp_ is filled: the rest.  Ends with a barrier.
 __device__ __forceinline__ void md_tables(const MoeDecodeParams& p, MdRoute& r) {
     const int tid = threadIdx.x, lane = lane_id();
     const int P = p.M * p.topk;
@@ -197,196 +226,345 @@ __device__ __forceinline__ void md_tables(const MoeDecodeParams& p, MdRoute& r) 
         if (r.exp_[f] >= 0) atomicOr(&r.mask[r.exp_[f]], 1ull << (f / p.topk));
     __syncthreads();
     if (tid < kWave) {
-        int n = 0;
+        int n = 0, pairs = 0, most = 0, groups = 0;
         for (int e0 = 0; e0 < p.E; e0 += kWave) {
-            const bool on = e0 + lane < p.E && r.mask[e0 + lane] != 0ull;
-            const unsigned long long b = __ballot(on);
-            if (on) r.active[n + __popcll(b & ((1ull << lane) - 1ull))] = (int16_t)(e0 + lane);
+            const int c = e0 + lane < p.E ? __popcll(r.mask[e0 + lane]) : 0;
+            const unsigned long long b = __ballot(c > 0);
+            const int incl = wave_incl_scan(c);
+            if (c > 0) {
+                r.active[n + __popcll(b & ((1ull << lane) - 1ull))] = (int16_t)(e0 + lane);
+                r.base[e0 + lane] = (int16_t)(pairs + incl - c);
+            }
+            // at most 64 tokens: one or two groups
+            const unsigned long long two = __ballot(c > 32);
+            const unsigned long long lt = (1ull << lane) - 1ull;
+            const int g = groups + __popcll(b & lt) + __popcll(two & lt);
+            if (c > 0) r.group[g] = (int16_t)(e0 + lane);
+            if (c > 32) r.group[g + 1] = (int16_t)(e0 + lane + kMdMaxE);
+            groups += __popcll(b) + __popcll(two);
             n += __popcll(b);
+            pairs += __builtin_amdgcn_readlane(incl, kWave - 1);
+            most = max(most, c);
         }
-        if (lane == 0) r.n_active = n;
+#pragma unroll
+        for (int o = kWave / 2; o > 0; o >>= 1) most = max(most, __shfl_xor(most, o, kWave));
+        if (lane == 0) r.n_active = n, r.n_groups = groups, r.n_max = most;
+    }
+    __syncthreads();
+    for (int f = tid; f < P; f += kMdThreads) {
+        const int e = r.exp_[f];
+        if (e >= 0) r.list[r.base[e] + __popcll(r.mask[e] & ((1ull << (f / p.topk)) - 1ull))] = (int16_t)f;
     }
     __syncthreads();
 }
 
-// 16 rows of an expert's weight, one 64-value block of K: two operands a lane
-// (values 16 lq .. 16 lq + 15 of the block).
-template <bool W8> struct MdRow;
-template <> struct MdRow<false> {
-    uint4 q[2];
-    __device__ __forceinline__ void load(const void* row, int k) {
-        q[0] = ld16(static_cast<const uint16_t*>(row) + k);
-        q[1] = ld16(static_cast<const uint16_t*>(row) + k + 8);
+// LDS values that are the same in every lane, as scalars.
+__device__ __forceinline__ int md_uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ unsigned long long md_uni(unsigned long long v) {
+    return ((unsigned long long)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32)) << 32) |
+           (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+}
+
+// ---------------------------------------------------------------- the stream
+// One block: 128 bytes of each of 32 expert rows (64 values of K in bf16, 128 in
+// 8 bits) and the same values of TB x 16 token rows, in registers from their
+// load to their turn.  A wavefront keeps U blocks in flight.
+template <bool W8, int TB> struct MdBlock {
+    static constexpr int XH = W8 ? 2 : 1;          // 64-value parts of a block
+    static constexpr int KV = 64 * XH;
+    uint4 w[4];
+    uint4 x[XH][2 * TB];
+};
+
+// Where a wavefront's loads go: lane l takes row l / 8 of each group of eight
+// and chunk l % 8 of its 128 bytes.
+template <int TB> struct MdRows {
+    uint32_t w[4];                                 // byte offsets in the expert's matrix
+    uint32_t x[2 * TB];                            // in the token matrix; kBufOff: no such row
+};
+
+template <bool W8, int TB>
+__device__ __forceinline__ void md_issue(MdBlock<W8, TB>& b, __amdgpu_buffer_rsrc_t rw, __amdgpu_buffer_rsrc_t rx,
+                                         const MdRows<TB>& r, int kb, int K) {
+    using B = MdBlock<W8, TB>;
+    const int c = lane_id() % 8;
+    // chunks past the end of the row read zeros, in both operands
+    const bool w_in = kb * B::KV + c * (W8 ? 16 : 8) < K;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b.w[i] = buf_ld16_at<true>(rw, w_in ? r.w[i] : kBufOff, (uint32_t)kb * 128u);
+#pragma unroll
+    for (int h = 0; h < B::XH; ++h) {
+        const bool x_in = kb * B::KV + h * 64 + c * 8 < K;
+#pragma unroll
+        for (int i = 0; i < 2 * TB; ++i)
+            b.x[h][i] = buf_ld16_at<false>(rx, x_in ? r.x[i] : kBufOff, (uint32_t)(kb * B::XH + h) * 128u);
     }
-    __device__ __forceinline__ void operands(uint4& a, uint4& b) const { a = q[0]; b = q[1]; }
-};
-template <> struct MdRow<true> {
-    uint4 q;
-    __device__ __forceinline__ void load(const void* row, int k) { q = ld16(static_cast<const uint8_t*>(row) + k); }
-    __device__ __forceinline__ void operands(uint4& a, uint4& b) const { widen16(q, a, b); }
-};
+}
+
+// uint4 of LDS per wavefront: 32 expert rows and 16 token rows (32 of TB = 4,
+// whose partial sums need the room at the end)
+constexpr int md_stage_words(int TB) { return 32 * 8 + (TB < 4 ? 16 : 32) * 8; }
+
+// acc[n][t] += rows 16 n .. 16 n + 15 times token block t over the block's
+// values.  `refill` issues the block's next loads once its registers are free.
+template <bool W8, int TB, typename F>
+__device__ __forceinline__ void md_consume(MdBlock<W8, TB>& b, uint4* st, const StageAt& at, f32x4_t (&acc)[2][TB],
+                                           F refill) {
+    using B = MdBlock<W8, TB>;
+    constexpr int XT = TB < 4 ? 1 : 2;            // token blocks staged at a time
+    uint4* sx = st + 32 * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) st[at.piece(i)] = b.w[i];
+#pragma unroll
+    for (int h = 0; h < B::XH; ++h)
+#pragma unroll
+        for (int t0 = 0; t0 < TB; t0 += XT) {
+#pragma unroll
+            for (int i = 0; i < 2 * XT; ++i) sx[at.piece(i)] = b.x[h][2 * t0 + i];
+            stage_order();
+            if (h == B::XH - 1 && t0 + XT >= TB) refill();
+            uint4 a[2][2];
+            if constexpr (W8) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n) widen16(st[at.half(n, h)], a[n][0], a[n][1]);
+            } else {
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) a[n][j] = st[at.half(n, j)];
+            }
+#pragma unroll
+            for (int t = 0; t < XT; ++t)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    // in 8 bits a lane's chunk is 16 values: their two halves
+                    const uint4 v = sx[W8 ? at.two(t, j) : at.half(t, j)];
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) acc[n][t0 + t] = mfma_bf16(a[n][j], v, acc[n][t0 + t]);
+                }
+            stage_order();
+        }
+}
 
 __device__ __forceinline__ uint4 md_and(const uint4& v, uint32_t m) {
     return make_uint4(v.x & m, v.y & m, v.z & m, v.w & m);
 }
 
-// Deltas of one expert added to acc: for every adapter among the expert's
-// tokens (lane t of `ad`: adapter of column t, -1 none; `pair`: its pair
-// index), B rows times the S columns of its tokens.  Groups are dealt to the
-// waves in turn, `deal` counting them across calls.
-template <int NT, int TB>
-__device__ __forceinline__ void md_delta(const MoeDecodeParams& p, const uint16_t* B, int64_t per_l,
-                                         const int64_t* row, const slot_t* S, int ad, int pair, int wave,
-                                         int& deal, uint32_t want, bool* lost, f32x4_t (&acc)[NT][TB]) {
-    const int lane = lane_id(), lr = lane % 16, lq = lane / 16;
+// Deltas of one expert, dealt to the wavefronts: step d is one 32-wide part j
+// of the rank for one adapter among the expert's tokens (`ad`: lane t holds
+// the adapter of column t, -1 for none), and wavefront d % kMdWaves takes it.
+struct MdStep {
+    int l, j;                     // adapter (-1: no such step), first rank position
+    unsigned long long cols;      // its columns
+};
+__device__ __forceinline__ MdStep md_step(int ad, int r, int d) {
+    const int per = (r + 31) / 32;
     unsigned long long rem = __ballot(ad >= 0);
-    while (rem) {
+    MdStep s{-1, 0, 0ull};
+    for (int g = d / per; rem; --g) {
         const int l = __builtin_amdgcn_readlane(ad, __ffsll((long long)rem) - 1);
         const unsigned long long same = __ballot(ad == l);
+        if (g == 0) {
+            s.l = l;
+            s.j = d % per * 32;
+            s.cols = same;
+            break;
+        }
         rem &= ~same;
-        if (deal++ % kMdWaves != wave) continue;
+    }
+    return s;
+}
+
+// A step's two operands of B rows: rows row[n] of the adapter's matrix.
+__device__ __forceinline__ void md_step_load(const MoeDecodeParams& p, const uint16_t* B, int64_t per_l,
+                                             const int64_t (&row)[2], const MdStep& s, uint4 (&b)[2]) {
+    const int j = s.j + lane_id() / 16 * 8;
+    const uint32_t mj = opaque_mask(j < p.r);
 #pragma unroll
-        for (int t = 0; t < TB; ++t) {
-            if (((same >> (16 * t)) & 0xffffull) == 0ull) continue;
-            const bool on = (same >> (16 * t + lr)) & 1ull;
-            const int f = __shfl(pair, 16 * t + lr, kWave);
-            for (int j = lq * 8; j - lq * 8 < p.r; j += 32) {
-                uint32_t w[8];
+    for (int n = 0; n < 2; ++n)
+        b[n] = md_and(ld16(B + max(s.l, 0) * per_l + row[n] * p.r + min(j, p.r - 8)), mj);
+}
+
+// acc += B S for the step's columns.  S rows by pair: from `sS` when the
+// workgroup holds them in LDS, else from their exchange slots.
+template <int TB>
+__device__ __forceinline__ void md_step_add(const MoeDecodeParams& p, const uint32_t* sS, const slot_t* S,
+                                            const MdStep& s, int pair, const uint4 (&b)[2], uint32_t want,
+                                            bool* lost, f32x4_t (&acc)[2][TB]) {
+    const int lane = lane_id(), lr = lane % 16;
+    const int j = s.j + lane / 16 * 8;
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    w[q] = on && j < p.r ? slot_wait(S + (int64_t)f * p.r + j + q, want, p.wc.max_spin, lost) : 0u;
-                uint4 h, lo;
-                h.x = (w[0] >> 16) | (w[1] & 0xffff0000u); lo.x = (w[0] & 0xffffu) | (w[1] << 16);
-                h.y = (w[2] >> 16) | (w[3] & 0xffff0000u); lo.y = (w[2] & 0xffffu) | (w[3] << 16);
-                h.z = (w[4] >> 16) | (w[5] & 0xffff0000u); lo.z = (w[4] & 0xffffu) | (w[5] << 16);
-                h.w = (w[6] >> 16) | (w[7] & 0xffff0000u); lo.w = (w[6] & 0xffffu) | (w[7] << 16);
-                const uint32_t mj = opaque_mask(j < p.r);
+    for (int t = 0; t < TB; ++t) {
+        if (((s.cols >> (16 * t)) & 0xffffull) == 0ull) continue;
+        const bool on = ((s.cols >> (16 * t + lr)) & 1ull) && j < p.r;
+        const int at = __shfl(pair, 16 * t + lr, kWave) * p.r + min(j, p.r - 8);
+        uint32_t w[8];
+        if (sS) {
+            const uint32_t m = opaque_mask(on);
+            const uint4 a = md_and(*reinterpret_cast<const uint4*>(sS + at), m);
+            const uint4 c = md_and(*reinterpret_cast<const uint4*>(sS + at + 4), m);
+            w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+            w[4] = c.x; w[5] = c.y; w[6] = c.z; w[7] = c.w;
+        } else {
+            slot_wait8(S + at, on, want, p.wc.max_spin, lost, w);
+        }
+        uint4 h, lo;
+        h.x = (w[0] >> 16) | (w[1] & 0xffff0000u); lo.x = (w[0] & 0xffffu) | (w[1] << 16);
+        h.y = (w[2] >> 16) | (w[3] & 0xffff0000u); lo.y = (w[2] & 0xffffu) | (w[3] << 16);
+        h.z = (w[4] >> 16) | (w[5] & 0xffff0000u); lo.z = (w[4] & 0xffffu) | (w[5] << 16);
+        h.w = (w[6] >> 16) | (w[7] & 0xffff0000u); lo.w = (w[6] & 0xffffu) | (w[7] << 16);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint4 b = md_and(ld16(B + l * per_l + row[n] * p.r + min(j, p.r - 8)), mj);
-                    acc[n][t] = mfma_bf16(b, h, acc[n][t]);
-                    acc[n][t] = mfma_bf16(b, lo, acc[n][t]);
-                }
-            }
+        for (int n = 0; n < 2; ++n) {
+            acc[n][t] = mfma_bf16(b[n], h, acc[n][t]);
+            acc[n][t] = mfma_bf16(b[n], lo, acc[n][t]);
         }
     }
 }
 
 // ---------------------------------------------------------------- first launch
-struct MdUnit {              // one (expert, 16 gate + 16 up rows) unit
-    int e, n0, ne;
-};
-
-template <bool W8, int TB>
-__device__ __forceinline__ void md_gate_up(const MoeDecodeParams& p, const MdUnit& u, const int16_t* s_tok,
-                                           const int16_t* s_pair, const int16_t* s_ad, const float* s_w,
-                                           float4* red, uint32_t want, bool* lost) {
+// The consumers of one launch: units u = first, first + stride, ... of
+// (up to 32 tokens of an expert, 16 gate and 16 up rows).  The wavefronts share a unit's K, block
+// by block in turn; the loads of the next unit are issued from the last blocks of the
+// one before, so the stream does not stop at its end.
+template <bool W8, int TB, int U>
+__device__ __forceinline__ void md_gate_up(const MoeDecodeParams& p, const MdRoute& rt, const float* s_w,
+                                           const int16_t* s_ad, uint32_t* s_S, uint4* smem, int first, int stride,
+                                           uint32_t want, bool* lost) {
+    using B = MdBlock<W8, TB>;
     constexpr int kBytes = W8 ? 1 : 2;
-    const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
+    constexpr int kWords = md_stage_words(TB);
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     const int lr = lane % 16, lq = lane / 16;
-    const int gi = min(u.n0 + lr, p.I - 1);
-    const int64_t row_g = (int64_t)u.e * 2 * p.I + gi, row_u = row_g + p.I;
-    const char* W = static_cast<const char*>(p.W_gu);
-    const void* rg = W + row_g * p.H * kBytes;
-    const void* ru = W + row_u * p.H * kBytes;
-    const uint16_t* xr[TB];
+    uint4* st = smem + wave * kWords;
+    const StageAt at;
+    const int tiles = (p.I + 15) / 16;
+    const int units = md_uni(rt.n_groups) * tiles;
+    const int KB = (p.H + B::KV - 1) / B::KV;
+    const int nb = ((KB + kMdWaves - 1) / kMdWaves + U - 1) / U * U;    // blocks per wavefront and unit
+    const uint32_t ebytes = (uint32_t)(2 * p.I) * (uint32_t)p.H * kBytes;
+    const __amdgpu_buffer_rsrc_t rx = uniform_rsrc(p.x, (uint32_t)(((int64_t)(p.M - 1) * p.ldx + p.H) * 2));
+
+    MdRows<TB> rows;
+    const char* wbase = nullptr;
+    int u_load = first, b_load = 0;
+    auto set_rows = [&]() {                        // the unit that loads are issued for
+        if (u_load >= units) return;
+        const int g = md_uni((int)rt.group[u_load / tiles]);
+        const int e = g % kMdMaxE, skip = g / kMdMaxE * 32;
+        const int n0 = (u_load % tiles) * 16;
+        wbase = static_cast<const char*>(p.W_gu) + (int64_t)e * 2 * p.I * p.H * kBytes;
 #pragma unroll
-    for (int t = 0; t < TB; ++t) xr[t] = p.x + (int64_t)s_tok[min(t * 16 + lr, u.ne - 1)] * p.ldx;
-    f32x4_t acc[2][TB];
+        for (int i = 0; i < 4; ++i) {
+            const int n = min(n0 + (i % 2) * 8 + lane / 8, p.I - 1) + (i / 2) * p.I;
+            rows.w[i] = (uint32_t)n * (uint32_t)p.H * kBytes + (lane % 8) * 16;
+        }
+        const int ne = __popcll(md_uni(rt.mask[e])) - skip, base = md_uni((int)rt.base[e]) + skip;
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+        for (int i = 0; i < 2 * TB; ++i) {
+            const int t = 8 * i + lane / 8;
+            rows.x[i] = t < ne ? (uint32_t)((int)rt.list[base + t] / p.topk) * (uint32_t)p.ldx * 2u + (lane % 8) * 16
+                               : kBufOff;
+        }
+    };
+    auto issue = [&](B& b) {
+        const int kb = b_load * kMdWaves + wave;
+        const bool on = u_load < units && kb < KB;
+        md_issue<W8, TB>(b, uniform_rsrc(wbase, on ? ebytes : 0u), rx, rows, on ? kb : KB, p.H);
+        if (++b_load == nb) {
+            b_load = 0;
+            u_load += stride;
+            set_rows();
+        }
+    };
+    set_rows();
+    B blk[U];
 #pragma unroll
-        for (int t = 0; t < TB; ++t) acc[n][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    constexpr int U = TB == 1 ? 4 : TB == 2 ? 3 : 2;
-    const int blocks = (p.H + 63) / 64;
-    for (int b0 = wave; b0 < blocks; b0 += U * kMdWaves) {
-        MdRow<W8> g[U], v[U];
-        uint4 xv[U][TB][2];
+    for (int q = 0; q < U; ++q) issue(blk[q]);
+
+    for (int u = first; u < units; u += stride) {
+        const int g = md_uni((int)rt.group[u / tiles]);
+        const int e = g % kMdMaxE, skip = g / kMdMaxE * 32;
+        const int n0 = (u % tiles) * 16;
+        const int ne = min(__popcll(md_uni(rt.mask[e])) - skip, 32), base = md_uni((int)rt.base[e]) + skip;
+        f32x4_t acc[2][TB];
 #pragma unroll
-        for (int q = 0; q < U; ++q) {
-            const int k = (b0 + q * kMdWaves) * 64 + lq * 16;
-            // H is a multiple of 8: a lane's second half may lie past the end
-            const int kc = min(k, p.H - (W8 ? 16 : 8)), kd = min(k + 8, p.H - 8);
-            if constexpr (W8) {
-                g[q].load(rg, kc);
-                v[q].load(ru, kc);
-            } else {
-                g[q].q[0] = ld16(static_cast<const uint16_t*>(rg) + kc);
-                g[q].q[1] = ld16(static_cast<const uint16_t*>(rg) + kd);
-                v[q].q[0] = ld16(static_cast<const uint16_t*>(ru) + kc);
-                v[q].q[1] = ld16(static_cast<const uint16_t*>(ru) + kd);
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int t = 0; t < TB; ++t) acc[n][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        // what the unit's end needs, loaded ahead of its stream: the scales and
+        // the B rows of the wavefront's first delta step
+        float sg[W8 ? 8 : 1];
+        if constexpr (W8) {
+            const float* sc = p.s_gu + (int64_t)e * 2 * p.I + min(n0 + lq * 4, p.I - 4);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) sg[q] = sc[q], sg[4 + q] = sc[p.I + q];
+        }
+        const int f = rt.list[base + min(lane, ne - 1)];
+        const int ad = p.L > 0 && lane < ne ? s_ad[f / p.topk] : -1;
+        const int64_t row_g = (int64_t)e * 2 * p.I + min(n0 + lr, p.I - 1);
+        const int64_t row[2] = {row_g, row_g + p.I};
+        MdStep step = md_step(ad, p.r, wave);
+        uint4 bop[2];
+        if (step.l >= 0) md_step_load(p, p.B_gu, (int64_t)p.E * 2 * p.I * p.r, row, step, bop);
+        for (int b = 0; b < nb; b += U)
+#pragma unroll
+            for (int q = 0; q < U; ++q) md_consume<W8, TB>(blk[q], st, at, acc, [&]() { issue(blk[q]); });
+        if constexpr (W8) {
+            // columns past I (a ragged last tile) are never stored
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int t = 0; t < TB; ++t) acc[0][t][q] *= sg[q], acc[1][t][q] *= sg[4 + q];
+        }
+        if (p.L > 0) {
+            if (u == first && s_S) {               // every unit reads S: once from the slots into LDS
+                for (int i = (int)threadIdx.x; i < p.M * p.topk * p.r; i += kMdThreads)
+                    s_S[i] = s_ad[i / (p.topk * p.r)] >= 0 ? slot_wait(p.S_gu + i, want, p.wc.max_spin, lost) : 0u;
+                __syncthreads();
             }
-            const uint32_t m0 = opaque_mask(k < p.H), m1 = opaque_mask(k + 8 < p.H);
-#pragma unroll
-            for (int t = 0; t < TB; ++t) {
-                xv[q][t][0] = md_and(ld16(xr[t] + min(k, p.H - 8)), m0);
-                xv[q][t][1] = md_and(ld16(xr[t] + kd), m1);
+            for (int d = wave; step.l >= 0;) {
+                md_step_add<TB>(p, s_S, p.S_gu, step, f, bop, want, lost, acc);
+                d += kMdWaves;
+                step = md_step(ad, p.r, d);
+                if (step.l >= 0) md_step_load(p, p.B_gu, (int64_t)p.E * 2 * p.I * p.r, row, step, bop);
             }
         }
+        // the wavefronts' partial sums join in a fixed order through the stages
+        float4* red = reinterpret_cast<float4*>(st);
 #pragma unroll
-        for (int q = 0; q < U; ++q) {
-            uint4 a, b, c, d;
-            g[q].operands(a, b);
-            v[q].operands(c, d);
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int t = 0; t < TB; ++t) {
-                acc[0][t] = mfma_bf16(a, xv[q][t][0], acc[0][t]);
-                acc[1][t] = mfma_bf16(c, xv[q][t][0], acc[1][t]);
-                acc[0][t] = mfma_bf16(b, xv[q][t][1], acc[0][t]);
-                acc[1][t] = mfma_bf16(d, xv[q][t][1], acc[1][t]);
+            for (int t = 0; t < TB; ++t)
+                red[(n * TB + t) * kWave + lane] = make_float4(acc[n][t][0], acc[n][t][1], acc[n][t][2], acc[n][t][3]);
+        __syncthreads();
+        const int pos = wave * 16 + lr, n = n0 + lq * 4;     // wave t < TB finishes token block t
+        if (wave < TB && pos < ne && n < p.I) {
+            float g[4] = {0.f, 0.f, 0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+            for (int w = 0; w < kMdWaves; ++w) {
+                const float4* src = reinterpret_cast<const float4*>(smem + w * kWords);
+                const float4 a = src[wave * kWave + lane], c = src[(TB + wave) * kWave + lane];
+                g[0] += a.x; g[1] += a.y; g[2] += a.z; g[3] += a.w;
+                v[0] += c.x; v[1] += c.y; v[2] += c.z; v[3] += c.w;
             }
+            const int f = rt.list[base + pos];
+            uint32_t o[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) o[q] = f32_to_bf16(s_w[f] * (g[q] / (1.f + expf(-g[q]))) * v[q]);
+            *reinterpret_cast<uint2*>(p.h + (int64_t)f * p.I + n) = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
         }
+        __syncthreads();
     }
-    if constexpr (W8) {
-        const float* sg = p.s_gu + (int64_t)u.e * 2 * p.I;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int n = min(u.n0 + lq * 4 + q, p.I - 1);
-            const float a = sg[n], b = sg[n + p.I];
-#pragma unroll
-            for (int t = 0; t < TB; ++t) acc[0][t][q] *= a, acc[1][t][q] *= b;
-        }
-    }
-    if (p.L > 0) {
-        const int c = min(lane, u.ne - 1);
-        const int ad = lane < u.ne ? s_ad[c] : -1;
-        int deal = 0;
-        const int64_t row[2] = {row_g, row_u};
-        md_delta<2, TB>(p, p.B_gu, (int64_t)p.E * 2 * p.I * p.r, row, p.S_gu, ad, s_pair[c], wave, deal, want,
-                        lost, acc);
-    }
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int t = 0; t < TB; ++t)
-            red[((wave * 2 + n) * TB + t) * kWave + lane] =
-                make_float4(acc[n][t][0], acc[n][t][1], acc[n][t][2], acc[n][t][3]);
-    __syncthreads();
-    const int pos = wave * 16 + lr, n = u.n0 + lq * 4;       // wave t < TB finishes token block t
-    if (wave < TB && pos < u.ne && n < p.I) {
-        float g[4] = {0.f, 0.f, 0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < kMdWaves; ++w) {
-            const float4 a = red[((w * 2) * TB + wave) * kWave + lane];
-            const float4 b = red[((w * 2 + 1) * TB + wave) * kWave + lane];
-            g[0] += a.x; g[1] += a.y; g[2] += a.z; g[3] += a.w;
-            v[0] += b.x; v[1] += b.y; v[2] += b.z; v[3] += b.w;
-        }
-        const int f = s_pair[pos];
-        uint32_t o[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = f32_to_bf16(s_w[f] * (g[q] / (1.f + expf(-g[q]))) * v[q]);
-        *reinterpret_cast<uint2*>(p.h + (int64_t)f * p.I + n) = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
-    }
-    __syncthreads();
 }
 
-template <bool W8>
-__global__ __launch_bounds__(kMdThreads) void k_moe_gate_up(MoeDecodeParams p, int shrinks) {
-    __shared__ float4 red[kMdWaves * 2 * 4 * kWave];
+// TBM: most token blocks of one group (M <= 16: one)
+template <bool W8, int TBM>
+__global__ __launch_bounds__(kMdThreads, 3) void k_moe_gate_up(MoeDecodeParams p, int shrinks) {
+    __shared__ uint4 smem[kMdWaves * md_stage_words(TBM)];
     __shared__ MdRoute rt;
     __shared__ float s_w[kMdMaxPairs];
-    __shared__ int16_t s_tok[LORA_DECODE_MAX_M], s_pair[LORA_DECODE_MAX_M], s_ad[LORA_DECODE_MAX_M];
+    __shared__ uint32_t s_S[kMdMaxS];
+    __shared__ int16_t s_ad[LORA_DECODE_MAX_M];
     const int tid = threadIdx.x;
     const uint32_t tag = launch_tag(), want = tag ^ p.wc.poll_xor;
     const int P = p.M * p.topk;
@@ -398,18 +576,20 @@ __global__ __launch_bounds__(kMdThreads) void k_moe_gate_up(MoeDecodeParams p, i
     }
     blk -= p.M;
     if (blk < shrinks) {
-        const int m = blk / p.topk, l = md_adapter(p, m);
+        const int parts = p.r / 16, f = blk / parts, j0 = blk % parts * 16;
+        const int m = f / p.topk, l = md_adapter(p, m);
         if (l < 0) return;
-        const int e = (int)slot_wait(p.route + blk, want, p.wc.max_spin, &lost);
+        const int e = (int)slot_wait(p.route + f, want, p.wc.max_spin, &lost);
         if (lost) {
             if (tid == 0) atomicOr(p.err, LORA_DEVERR_WAIT);
             return;
         }
         const int64_t slot = p.shared_outer ? l : (int64_t)l * p.E + e;
-        md_shrink(p.A_gu + slot * p.r * p.H, p.x + (int64_t)m * p.ldx, p.H, p.r, p.S_gu + (int64_t)blk * p.r, tag);
+        md_shrink(p.A_gu + (slot * p.r + j0) * p.H, p.x + (int64_t)m * p.ldx, p.H, p.S_gu + (int64_t)f * p.r + j0, tag);
         return;
     }
     blk -= shrinks;
+    if (tid < p.M) s_ad[tid] = (int16_t)md_adapter(p, tid);
     for (int f = tid; f < P; f += kMdThreads) {
         bool gone = false;
         const int e = (int)slot_wait(p.route + f, want, p.wc.max_spin, &gone);
@@ -418,153 +598,161 @@ __global__ __launch_bounds__(kMdThreads) void k_moe_gate_up(MoeDecodeParams p, i
         lost |= gone;
     }
     md_tables(p, rt);
-    const int tiles = (p.I + 15) / 16;
-    const int units = rt.n_active * tiles;
-    const int G = (int)gridDim.x - p.M - shrinks;
-    for (int u = blk; u < units; u += G) {
-        const int e = rt.active[u / tiles];
-        const unsigned long long mask = rt.mask[e];
-        if (tid < kWave && ((mask >> tid) & 1ull)) {
-            const int at = __popcll(mask & ((1ull << tid) - 1ull));
-            int f = tid * p.topk;
-            while (rt.exp_[f] != e) ++f;
-            s_tok[at] = (int16_t)tid;
-            s_pair[at] = (int16_t)f;
-            s_ad[at] = (int16_t)md_adapter(p, tid);
-        }
-        __syncthreads();
-        const MdUnit un{e, (u % tiles) * 16, (int)__popcll(mask)};
-        switch ((un.ne + 15) / 16) {
-            case 1: md_gate_up<W8, 1>(p, un, s_tok, s_pair, s_ad, s_w, red, want, &lost); break;
-            case 2: md_gate_up<W8, 2>(p, un, s_tok, s_pair, s_ad, s_w, red, want, &lost); break;
-            case 3: md_gate_up<W8, 3>(p, un, s_tok, s_pair, s_ad, s_w, red, want, &lost); break;
-            default: md_gate_up<W8, 4>(p, un, s_tok, s_pair, s_ad, s_w, red, want, &lost); break;
-        }
-    }
+    const int stride = (int)gridDim.x - p.M - shrinks;
+    uint32_t* S = P * p.r <= kMdMaxS ? s_S : nullptr;
+    if (TBM == 1 || md_uni(rt.n_max) <= 16)
+        md_gate_up<W8, 1, W8 ? 2 : 3>(p, rt, s_w, s_ad, S, smem, blk, stride, want, &lost);
+    else
+        md_gate_up<W8, TBM, W8 ? 1 : 2>(p, rt, s_w, s_ad, S, smem, blk, stride, want, &lost);
     if (lost) atomicOr(p.err, LORA_DEVERR_WAIT);
 }
 
 // ---------------------------------------------------------------- second launch
-template <bool W8, int TB>
-__global__ __launch_bounds__(kMdThreads) void k_moe_down(MoeDecodeParams p, int shrinks) {
+// A consumer: 32 output rows and one share of the blocks of all chosen
+// experts, the token's column the same for every expert (rows of tokens that
+// did not choose it read zeros), so the experts' sum needs no step of its own.
+template <bool W8, int TB, int U>
+__global__ __launch_bounds__(kMdThreads, TB > 2 ? 2 : 3) void k_moe_down(MoeDecodeParams p, int shrinks) {
+    using B = MdBlock<W8, TB>;
     constexpr int kBytes = W8 ? 1 : 2;
-    __shared__ float4 red[kMdWaves * TB * kWave];
+    constexpr int kWords = md_stage_words(TB);
+    __shared__ uint4 smem[kMdWaves * kWords];
     __shared__ MdRoute rt;
-    __shared__ int16_t fmap[kMdMaxE][TB * 16];      // pair of (active expert, token), -1: none
-    const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
+    const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int lr = lane % 16, lq = lane / 16;
     const uint32_t tag = launch_tag(), want = tag ^ p.wc.poll_xor;
     const int P = p.M * p.topk;
     bool lost = false;
-    int blk = (int)blockIdx.x;
-    if (blk < shrinks) {
-        const int m = blk / p.topk, l = md_adapter(p, m);
+    int id = (int)blockIdx.x;
+    if (id < shrinks) {
+        const int parts = p.r / 16, f = id / parts, j0 = id % parts * 16;
+        const int l = md_adapter(p, f / p.topk);
         if (l < 0) return;
-        const int e = p.route_ids[blk];
-        md_shrink(p.A_d + ((int64_t)l * p.E + e) * p.r * p.I, p.h + (int64_t)blk * p.I, p.I, p.r,
-                  p.S_d + (int64_t)blk * p.r, tag);
+        md_shrink(p.A_d + (((int64_t)l * p.E + p.route_ids[f]) * p.r + j0) * p.I, p.h + (int64_t)f * p.I, p.I,
+                  p.S_d + (int64_t)f * p.r + j0, tag);
         return;
     }
-    blk -= shrinks;
-    const int tiles = (p.H + 15) / 16;
-    const int split = blk / tiles, n0 = (blk % tiles) * 16;
+    id -= shrinks;
+    const int tiles = (p.H + 31) / 32;
+    const int split = id / tiles, n0 = (id % tiles) * 32;
     for (int f = tid; f < P; f += kMdThreads) rt.exp_[f] = (int16_t)p.route_ids[f];
     md_tables(p, rt);
-    const int na = rt.n_active;
-    for (int i = tid; i < na * TB * 16; i += kMdThreads) {
-        const int e = rt.active[i / (TB * 16)], m = i % (TB * 16);
-        int f = -1;
-        if ((rt.mask[e] >> m) & 1ull) {
-            f = m * p.topk;
-            while (rt.exp_[f] != e) ++f;
-        }
-        fmap[i / (TB * 16)][m] = (int16_t)f;
-    }
-    __syncthreads();
+    const int na = md_uni(rt.n_active);
+    const int ad0 = lane < p.M ? md_adapter(p, lane) : -1;
 
-    const int nr = min(n0 + lr, p.H - 1);
-    const char* W = static_cast<const char*>(p.W_d);
-    f32x4_t acc[1][TB], part[TB];
-#pragma unroll
-    for (int t = 0; t < TB; ++t) acc[0][t] = f32x4_t{0.f, 0.f, 0.f, 0.f}, part[t] = acc[0][t];
-    const int KB = (p.I + 63) / 64;                 // 64-value blocks of one expert
+    uint4* st = smem + wave * kWords;
+    const StageAt at;
+    const int KB = (p.I + B::KV - 1) / B::KV;               // blocks of one expert
     const int total = na * KB;
     const int t0 = (int)((int64_t)total * split / p.splits), t1 = (int)((int64_t)total * (split + 1) / p.splits);
-    constexpr int U = TB == 1 ? 4 : TB == 2 ? 3 : 2;
-    int cur = -1;
-    auto fold = [&](int ea) {                       // the scale of the expert just left
-        const float* s = p.s_d + (int64_t)rt.active[ea] * p.H;
+    const uint32_t ebytes = (uint32_t)p.H * (uint32_t)p.I * kBytes;
+    const __amdgpu_buffer_rsrc_t rh = uniform_rsrc(p.h, (uint32_t)P * (uint32_t)p.I * 2u);
+
+    MdRows<TB> rows;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const float v = s[min(n0 + lq * 4 + q, p.H - 1)];
+    for (int i = 0; i < 4; ++i)
+        rows.w[i] = (uint32_t)min(n0 + 8 * i + lane / 8, p.H - 1) * (uint32_t)p.I * kBytes + (lane % 8) * 16;
+    const char* wbase = nullptr;
+    int a_load = t0 / KB, kb_load = t0 % KB + wave;         // active expert and block of the next load
+    // a part: one expert's blocks of this share, [kb0, kb1), every kMdWaves-th of
+    // them this wavefront's, their number rounded up to U
+    auto part_end = [&](int a) { return min(KB, t1 - a * KB); };
+    auto part_beg = [&](int a) { return max(0, t0 - a * KB); };
+    auto part_blocks = [&](int a) {
+        return ((part_end(a) - part_beg(a) + kMdWaves - 1) / kMdWaves + U - 1) / U * U;
+    };
+    int left = 0, end_load = 0;
+    auto set_rows = [&]() {
+        if (a_load * KB >= t1) return;
+        const int e = md_uni((int)rt.active[a_load]);
+        wbase = static_cast<const char*>(p.W_d) + (int64_t)e * p.H * p.I * kBytes;
+        left = part_blocks(a_load);
+        end_load = part_end(a_load);
+        kb_load = part_beg(a_load) + wave;
+        const unsigned long long mask = md_uni(rt.mask[e]);
+        const int base = md_uni((int)rt.base[e]);
 #pragma unroll
-            for (int t = 0; t < TB; ++t) acc[0][t][q] += part[t][q] * v, part[t][q] = 0.f;
+        for (int i = 0; i < 2 * TB; ++i) {
+            const int m = 8 * i + lane / 8;
+            rows.x[i] = kBufOff;
+            if ((mask >> m) & 1ull) {
+                const int f = rt.list[base + __popcll(mask & ((1ull << m) - 1ull))];
+                rows.x[i] = (uint32_t)f * (uint32_t)p.I * 2u + (lane % 8) * 16;
+            }
         }
     };
-    for (int b0 = t0 + wave; b0 < t1; b0 += U * kMdWaves) {
-        MdRow<W8> w[U];
-        uint4 hv[U][TB][2];
-        int ea[U];
-#pragma unroll
-        for (int q = 0; q < U; ++q) {
-            const int b = b0 + q * kMdWaves;
-            const bool in = b < t1;
-            ea[q] = min(b, total - 1) / KB;
-            const int k = (min(b, total - 1) - ea[q] * KB) * 64 + lq * 16;
-            const char* row = W + ((int64_t)rt.active[ea[q]] * p.H + nr) * p.I * kBytes;
-            const int kc = min(k, p.I - (W8 ? 16 : 8)), kd = min(k + 8, p.I - 8);
-            if constexpr (W8) {
-                w[q].load(row, kc);
-            } else {
-                w[q].q[0] = ld16(reinterpret_cast<const uint16_t*>(row) + kc);
-                w[q].q[1] = ld16(reinterpret_cast<const uint16_t*>(row) + kd);
-            }
-#pragma unroll
-            for (int t = 0; t < TB; ++t) {
-                const int f = fmap[ea[q]][t * 16 + lr];
-                const uint16_t* hr = p.h + (int64_t)max(f, 0) * p.I;
-                hv[q][t][0] = ld16_if(hr + min(k, p.I - 8), in && f >= 0 && k < p.I, p.h);
-                hv[q][t][1] = ld16_if(hr + kd, in && f >= 0 && k + 8 < p.I, p.h);
-            }
+    auto issue = [&](B& b) {
+        const bool on = a_load * KB < t1 && kb_load < end_load;
+        md_issue<W8, TB>(b, uniform_rsrc(wbase, on ? ebytes : 0u), rh, rows, on ? kb_load : KB, p.I);
+        kb_load += kMdWaves;
+        if (--left == 0) {
+            ++a_load;
+            set_rows();
         }
+    };
+    set_rows();
+    B blk[U];
 #pragma unroll
-        for (int q = 0; q < U; ++q) {
-            if (W8 && ea[q] != cur) {
-                if (cur >= 0) fold(cur);
-                cur = ea[q];
-            }
-            uint4 a, b;
-            w[q].operands(a, b);
+    for (int q = 0; q < U; ++q) issue(blk[q]);
+
+    f32x4_t acc[2][TB], part[2][TB];
 #pragma unroll
-            for (int t = 0; t < TB; ++t) {
-                f32x4_t& c = W8 ? part[t] : acc[0][t];
-                c = mfma_bf16(a, hv[q][t][0], c);
-                c = mfma_bf16(b, hv[q][t][1], c);
-            }
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int t = 0; t < TB; ++t) acc[n][t] = f32x4_t{0.f, 0.f, 0.f, 0.f}, part[n][t] = acc[n][t];
+    for (int a = t0 / KB; a * KB < t1; ++a) {
+        const int nb = part_blocks(a);
+        for (int b = 0; b < nb; b += U)
+#pragma unroll
+            for (int q = 0; q < U; ++q) md_consume<W8, TB>(blk[q], st, at, W8 ? part : acc, [&]() { issue(blk[q]); });
+        if constexpr (W8) {                                 // the expert's scales
+            const float* s = p.s_d + (int64_t)md_uni((int)rt.active[a]) * p.H;
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float v = s[min(n0 + 16 * n + lq * 4 + q, p.H - 1)];
+#pragma unroll
+                    for (int t = 0; t < TB; ++t) acc[n][t][q] += part[n][t][q] * v, part[n][t][q] = 0.f;
+                }
         }
     }
-    if (W8 && cur >= 0) fold(cur);
     if (p.L > 0) {
-        const int ad0 = lane < p.M ? md_adapter(p, lane) : -1;
-        int deal = 0;
+        const int64_t per_l = (int64_t)(p.shared_outer ? 1 : p.E) * p.H * p.r;
+        const int64_t r0 = min(n0 + lr, p.H - 1), r1 = min(n0 + 16 + lr, p.H - 1);
+        int deal = 0;                              // goes on from expert to expert
         for (int i = split; i < na; i += p.splits) {
-            const int e = rt.active[i];
-            const int f = lane < TB * 16 ? fmap[i][lane] : -1;
-            const int64_t row[1] = {p.shared_outer ? (int64_t)nr : (int64_t)e * p.H + nr};
-            md_delta<1, TB>(p, p.B_d, (int64_t)(p.shared_outer ? 1 : p.E) * p.H * p.r, row, p.S_d,
-                            f >= 0 ? ad0 : -1, f, wave, deal, want, &lost, acc);
+            const int e = md_uni((int)rt.active[i]);
+            const unsigned long long mask = md_uni(rt.mask[e]);
+            const bool on = (mask >> lane) & 1ull;
+            const int f = on ? rt.list[rt.base[e] + __popcll(mask & ((1ull << lane) - 1ull))] : 0;
+            const int64_t eb = p.shared_outer ? 0 : (int64_t)e * p.H;
+            const int64_t row[2] = {eb + r0, eb + r1};
+            for (int d = 0;; ++d) {
+                const MdStep step = md_step(on ? ad0 : -1, p.r, d);
+                if (step.l < 0) break;
+                if (deal++ % kMdWaves != wave) continue;
+                uint4 bop[2];
+                md_step_load(p, p.B_d, per_l, row, step, bop);
+                md_step_add<TB>(p, nullptr, p.S_d, step, f, bop, want, &lost, acc);
+            }
         }
     }
+    float4* red = reinterpret_cast<float4*>(st);
 #pragma unroll
-    for (int t = 0; t < TB; ++t)
-        red[(wave * TB + t) * kWave + lane] = make_float4(acc[0][t][0], acc[0][t][1], acc[0][t][2], acc[0][t][3]);
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int t = 0; t < TB; ++t)
+            red[(n * TB + t) * kWave + lane] = make_float4(acc[n][t][0], acc[n][t][1], acc[n][t][2], acc[n][t][3]);
     __syncthreads();
-    const int m = wave * 16 + lr, n = n0 + lq * 4;
-    if (wave < TB && m < p.M && n < p.H) {
+    // part i = n * TB + t: rows 16 n of token block t
+    for (int i = wave; i < 2 * TB; i += kMdWaves) {
+        const int m = (i % TB) * 16 + lr, n = n0 + (i / TB) * 16 + lq * 4;
+        if (m >= p.M || n >= p.H) continue;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < kMdWaves; ++w) {
-            const float4 a = red[(w * TB + wave) * kWave + lane];
+            const float4 a = reinterpret_cast<const float4*>(smem + w * kWords)[i * kWave + lane];
             v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
         }
         if (split < p.splits - 1) {
@@ -585,25 +773,26 @@ __global__ __launch_bounds__(kMdThreads) void k_moe_down(MoeDecodeParams p, int 
     if (lost) atomicOr(p.err, LORA_DEVERR_WAIT);
 }
 
-int moe_decode_splits(int H, int I) {
-    const int tiles = (H + 15) / 16, blocks = (I + 63) / 64;
-    const int want = (512 + tiles - 1) / tiles;
-    return max(1, min(min(want, 16), blocks / kMdWaves));
+int moe_decode_splits(int H) {
+    // as many as keep every consumer resident at once
+    const int tiles = (H + 31) / 32;
+    return max(1, min(kMdResident / tiles, 16));
 }
 
 template <bool W8>
 hipError_t launch_moe_decode_t(const MoeDecodeParams& p, hipStream_t st) {
     const int P = p.M * p.topk;
-    const int shrinks = p.L > 0 ? P : 0;
-    const int units = min(p.E, P) * ((p.I + 15) / 16);
-    hipLaunchKernelGGL(k_moe_gate_up<W8>, dim3((unsigned)(p.M + shrinks + min(units, 512))), dim3(kMdThreads), 0, st,
-                       p, shrinks);
-    hipError_t e = hipGetLastError();
+    const int shrinks = p.L > 0 ? P * (p.r / 16) : 0;
+    const int units = min(min(p.E, P) + P / 33, kMdMaxGroups) * ((p.I + 15) / 16);
+    const dim3 g1((unsigned)(p.M + shrinks + min(units, kMdResident))), g2((unsigned)(shrinks + (p.H + 31) / 32 * p.splits));
+    const dim3 t(kMdThreads);
+    if (p.M <= 16) hipLaunchKernelGGL((k_moe_gate_up<W8, 1>), g1, t, 0, st, p, shrinks);
+    else hipLaunchKernelGGL((k_moe_gate_up<W8, 2>), g1, t, 0, st, p, shrinks);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const unsigned grid = (unsigned)(shrinks + (p.H + 15) / 16 * p.splits);
-    if (p.M <= 16) hipLaunchKernelGGL((k_moe_down<W8, 1>), dim3(grid), dim3(kMdThreads), 0, st, p, shrinks);
-    else if (p.M <= 32) hipLaunchKernelGGL((k_moe_down<W8, 2>), dim3(grid), dim3(kMdThreads), 0, st, p, shrinks);
-    else hipLaunchKernelGGL((k_moe_down<W8, 4>), dim3(grid), dim3(kMdThreads), 0, st, p, shrinks);
+    if (p.M <= 16) hipLaunchKernelGGL((k_moe_down<W8, 1, W8 ? 2 : 3>), g2, t, 0, st, p, shrinks);
+    else if (p.M <= 32) hipLaunchKernelGGL((k_moe_down<W8, 2, W8 ? 1 : 2>), g2, t, 0, st, p, shrinks);
+    else hipLaunchKernelGGL((k_moe_down<W8, 4, W8 ? 1 : 2>), g2, t, 0, st, p, shrinks);
     return hipGetLastError();
 }
 
