@@ -702,6 +702,9 @@ lora_status lora_quantize_rows(int32_t dtype, const void* x, int64_t ldx, int32_
     return from_hip(launch_rms_norm(dtype, p, stream));
 }
 
+// rows that are addressed with 32-bit byte offsets
+static bool below_2gib(int64_t rows, int64_t ld, int bytes) { return ld < (int64_t)INT32_MAX / bytes / rows; }
+
 // rows of 8-bit values read 16 bytes at a time
 static lora_status check_rows8(const void* p, int64_t ld, int64_t width) {
     if (!p || !aligned16(p) || ld < width || ld % 16 != 0) return LORA_INVALID_ARG;
@@ -731,9 +734,13 @@ lora_status lora_linear_fp8(const lora_weights_t* w, const void* W8, int64_t ldw
     if (workspace_bytes < L.total) return LORA_INVALID_ARG;
     LinearArgs a = make_args(w, seg, M);
     a.err = ws_error(workspace);
-    if (M <= LORA_DECODE_MAX_M)
+    if (M <= LORA_DECODE_MAX_M) {
+        // 32-bit offsets over the token rows and over 16 rows of W8 or A
+        if (!below_2gib(M, ldx, 2) || !below_2gib(M, ldx8, 1) || !below_2gib(16, ldw, 1))
+            return LORA_UNSUPPORTED;
         return from_hip(launch_linear_fp8(a, W8, ldw, w_scale, x8, ldx8, x_scale, x, ldx, y, ldy,
                                           workspace, stream));
+    }
     float* S = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + L.S);
     hipError_t e = launch_shrink(a, x, ldx, S, workspace, stream);
     if (e != hipSuccess) return LORA_HIP_ERROR;
@@ -752,6 +759,10 @@ static lora_status check_experts(const lora_moe_experts_t* ex, const lora_moe_we
         return LORA_INVALID_ARG;
     if ((ex->wdtype == LORA_E4M3) != (ex->s_gu != nullptr) || !ex->s_gu != !ex->s_d)
         return LORA_INVALID_ARG;
+    // 32-bit offsets within one expert's matrix and over the rows of h
+    if (!below_2gib(2 * (int64_t)ex->I, ex->H, 2) ||
+        !below_2gib((int64_t)LORA_DECODE_MAX_M * ex->topk, ex->I, 2))
+        return LORA_UNSUPPORTED;
     if (!w) return LORA_OK;
     const lora_status st = check_moe_weights(w);
     if (st != LORA_OK) return st;
@@ -805,6 +816,7 @@ lora_status lora_moe_decode(const lora_moe_weights_t* w, const lora_moe_experts_
     if (w && !ids) return LORA_INVALID_ARG;
     if ((st = check_rows(x, ldx, ex->H)) != LORA_OK) return st;
     if ((st = check_rows(out, ldo, ex->H)) != LORA_OK) return st;
+    if (!below_2gib(M, ldx, 2)) return LORA_UNSUPPORTED;
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)))
         return LORA_INVALID_ARG;
     const MoeDecodeWs l = moe_decode_ws(ex, w ? w->r : 0, M);

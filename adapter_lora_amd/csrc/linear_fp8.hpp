@@ -9,18 +9,22 @@
 // What bounds it: W8 is read once, N K bytes, and everything else is small, so
 // the launch is a stream of W8 with the rest hidden behind it.
 //   producers (first in the grid): unit = (segment, 16 S columns), the whole
-//     of K over eight waves, bf16 MFMA 16 x 16 x 32, joined through LDS.  S
-//     goes to tagged exchange slots already split into the bf16 hi / lo pair
-//     that the second product takes: one 32-bit word per value.
+//     of K over eight wavefronts, bf16 MFMA 16 x 16 x 32, joined through LDS.
+//     S goes to tagged exchange slots already split into the bf16 hi / lo pair
+//     that the second product takes: one 32-bit word per value.  (K in
+//     quarters gave the producers a shorter chain but every consumer four
+//     times the slots to read: 18.9 against 13.0 us on 32 mixed tokens.)
 //   consumers: unit = 16 NR output columns of one slice for every token, K over
-//     eight waves (v_mfma_f32_16x16x128_f8f6f4, W rows as the first operand so
-//     that a lane ends with four consecutive columns of one token).  Only after
-//     its share of W8 is read and multiplied does a workgroup look at the
-//     slots, which are full by then; each wave then adds the deltas of every
-//     eighth segment to its own partial sums, and the eight partial sums are
-//     joined through LDS in a fixed order.
-// A consumer waits for producers only, which wait for nothing and come first
-// in the grid; the waits are bounded and report LORA_DEVERR_WAIT.
+//     eight wavefronts (v_mfma_f32_16x16x128_f8f6f4, W rows as the first
+//     operand so that a lane ends with four consecutive columns of one token).
+//     Only after its share of W8 is read and multiplied does a workgroup look
+//     at the slots, which are full by then; each wavefront then adds the
+//     deltas of every eighth segment to its own partial sums, and the eight
+//     partial sums join through LDS in a fixed order.
+// Both read rows as whole 128-byte segments and change lanes through LDS
+// (row_stage.hpp).  A consumer waits for producers only, which wait for
+// nothing and come first in the grid; the waits are bounded and report
+// LORA_DEVERR_WAIT.
 //
 // Sums are fp32; S enters its product as the sum of two bf16 values (an error
 // of 2^-17 of S at most); y is rounded once.
@@ -28,6 +32,7 @@
 
 #include "common.hpp"
 #include "kernels.hpp"
+#include "row_stage.hpp"
 
 namespace mlora {
 
@@ -59,7 +64,8 @@ struct Fp8Params {
     int64_t ldx;
     uint16_t* y;
     int64_t ldy;
-    slot_t* slots;               // [64][cols]: sorted position, S column (hi / lo pair, tag)
+    slot_t* slots;               // [chunks][64][cols]: half of K, sorted position, S column
+    int chunks, chunk_kb;        // halves of K (one for short K), their blocks of 64 values
     int jb;                      // 16-column blocks of an S row
     int n_prod;                  // producer workgroups
     int tile_start[LORA_MAX_SLICES + 1];
@@ -77,206 +83,321 @@ __device__ __forceinline__ uint4 and4(const uint4& v, uint32_t m) {
     return make_uint4(v.x & m, v.y & m, v.z & m, v.w & m);
 }
 
-// S of one segment's tokens for 16 S columns: red[wave] holds the wave's
-// partial sums over its K share, joined and published by the first waves.
+// uint4 of a wavefront's stage: 16 NR rows of W (or A) and 16 token rows,
+// later its partial sums
+constexpr int fp8_stage(int TB, int NR) {
+    return (NR + 1) * 128 > NR * TB * kWave ? (NR + 1) * 128 : NR * TB * kWave;
+}
+
+// S of one segment's tokens for 16 S columns and half of K.  What names the
+// unit's rows (segment, tokens and, for tables of up to 64 slots, every slot's
+// rank and offset) is loaded in one round; then come four blocks of A a
+// wavefront at once, the whole half of K = 4096.
 template <int TB>
-__device__ __forceinline__ void fp8_producer(const Fp8Params& p, uint32_t tag, float4* red) {
+__device__ __forceinline__ void fp8_producer(const Fp8Params& p, uint32_t tag, uint4* smem, int words) {
     const LinearArgs& a = p.a;
-    const int u = (int)blockIdx.x;
+    const int c = (int)blockIdx.x % p.chunks, u = (int)blockIdx.x / p.chunks;
     const int s = u / p.jb, jb = u % p.jb;
-    if (s >= a.num_segments[0]) return;
-    const int id = a.req_to_lora[s];
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+    const int lr = lane % 16, lq = lane / 16;
+    const int slot = min(lane, a.L - 1);
+    const int rank_l = a.rank[slot];
+    const int64_t off_l = a.a_off[slot];
+    const int tok_l = a.sorted_idx[min(lane, a.M - 1)];
+    const int nseg = a.num_segments[0];
+    const int id = __builtin_amdgcn_readfirstlane(a.req_to_lora[s]);
+    const int p0 = __builtin_amdgcn_readfirstlane(a.seg_indptr[s]);
+    const int p1 = __builtin_amdgcn_readfirstlane(a.seg_indptr[s + 1]);
+    if (s >= nseg) return;
     if (id < 0 || id >= a.L) {
         table_fault(a.err, true);
         return;
     }
-    const int rp = a.rank[id];
+    const int rp = a.L <= kWave ? __builtin_amdgcn_readlane(rank_l, id) : __builtin_amdgcn_readfirstlane(a.rank[id]);
+    const int64_t off = a.L <= kWave ? readlane64(off_l, id) : a.a_off[id];
     const int per = a.r_max / 16;
     const int sl = jb / per, j0 = (jb % per) * 16;
     if (j0 >= rp) return;
-    const int p0 = a.seg_indptr[s], p1 = a.seg_indptr[s + 1];
     if (table_fault(a.err, p0 < 0 || p1 > a.M || p1 < p0)) return;
-    const int ms = p1 - p0;
-    const int lane = lane_id(), wave = (int)threadIdx.x / kWave;
-    const int lr = lane % 16, lq = lane / 16;
-    const uint16_t* A = static_cast<const uint16_t*>(a.A) + a.a_off[id] + (int64_t)(sl * rp + j0 + lr) * a.K;
-    const uint16_t* xr[TB];
+
+    const uint16_t* A = static_cast<const uint16_t*>(a.A) + off + (int64_t)(sl * rp + j0) * a.K;
+    const __amdgpu_buffer_rsrc_t ra = uniform_rsrc(A, (uint32_t)(16 * a.K * 2));
+    const __amdgpu_buffer_rsrc_t rx = uniform_rsrc(p.x, (uint32_t)(((int64_t)(a.M - 1) * p.ldx + a.K) * 2));
+    uint32_t off_a[2];
 #pragma unroll
-    for (int t = 0; t < TB; ++t) {
-        int m = a.sorted_idx[min(p0 + min(t * 16 + lr, ms - 1), a.M - 1)];
-        if (table_fault(a.err, m < 0 || m >= a.M)) m = min(max(m, 0), a.M - 1);
-        xr[t] = p.x + (int64_t)m * p.ldx;
-    }
+    for (int i = 0; i < 2; ++i) off_a[i] = (uint32_t)((8 * i + lane / 8) * a.K * 2 + (lane % 8) * 16);
+    uint4* st = smem + wave * words;
+    uint4* sx = st + 16 * 8;
+    const StageAt at;
+    constexpr int U = 4;
+    const int ms = min(p1 - p0, TB * 16);
+    const int KB = min((a.K + 63) / 64, (c + 1) * p.chunk_kb);
     f32x4_t acc[TB];
 #pragma unroll
     for (int t = 0; t < TB; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    const int steps = (a.K + 31) / 32;
-    for (int i0 = wave; i0 < steps; i0 += 4 * kFpWaves) {
-        uint4 va[4], vx[4][TB];
+    for (int b0 = c * p.chunk_kb + wave; b0 < KB; b0 += U * kFpWaves) {
+        uint4 va[U][2], vx[U][2];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int k = (i0 + q * kFpWaves) * 32 + lq * 8;
-            const int kc = min(k, a.K - 8);
-            va[q] = ld16(A + kc);
-            const uint32_t mk = opaque_mask(k < a.K);
+        for (int q = 0; q < U; ++q) {
+            const int kb = b0 + q * kFpWaves;
+            const bool in = kb < KB && kb * 64 + lane % 8 * 8 < a.K;
 #pragma unroll
-            for (int t = 0; t < TB; ++t) vx[q][t] = and4(ld16(xr[t] + kc), mk);
+            for (int i = 0; i < 2; ++i) va[q][i] = buf_ld16_at<true>(ra, in ? off_a[i] : kBufOff, (uint32_t)kb * 128u);
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int t = 0; t < TB; ++t) {               // 16 of the segment's tokens
+            if (t * 16 >= ms) break;
+            uint32_t off_x[2];
 #pragma unroll
-            for (int t = 0; t < TB; ++t)
-                if (t * 16 < ms) acc[t] = mfma_bf16(va[q], vx[q][t], acc[t]);
+            for (int i = 0; i < 2; ++i) {
+                const int k = t * 16 + 8 * i + lane / 8;
+                int m = __shfl(tok_l, min(p0 + k, a.M - 1), kWave);
+                if (table_fault(a.err, m < 0 || m >= a.M)) m = min(max(m, 0), a.M - 1);
+                off_x[i] = k < ms ? (uint32_t)m * (uint32_t)p.ldx * 2u + (lane % 8) * 16 : kBufOff;
+            }
+#pragma unroll
+            for (int q = 0; q < U; ++q) {
+                const int kb = b0 + q * kFpWaves;
+                const bool in = kb < KB && kb * 64 + lane % 8 * 8 < a.K;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    vx[q][i] = buf_ld16_at<false>(rx, in ? off_x[i] : kBufOff, (uint32_t)kb * 128u);
+            }
+#pragma unroll
+            for (int q = 0; q < U; ++q) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) st[at.piece(i)] = va[q][i], sx[at.piece(i)] = vx[q][i];
+                stage_order();
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[t] = mfma_bf16(st[at.half(0, j)], sx[at.half(0, j)], acc[t]);
+                stage_order();
+            }
+        }
     }
+    float4* red = reinterpret_cast<float4*>(st);
 #pragma unroll
-    for (int t = 0; t < TB; ++t)
-        red[(wave * TB + t) * kWave + lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+    for (int t = 0; t < TB; ++t) red[t * kWave + lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
     __syncthreads();
-    if (wave >= TB || wave * 16 >= ms) return;
+    const int pos = wave * 16 + lr;
+    if (wave >= TB || pos >= ms) return;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kFpWaves; ++w) {
-        const float4 t = red[(w * TB + wave) * kWave + lane];
-        v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
+        const float4 f = reinterpret_cast<const float4*>(smem + w * words)[wave * kWave + lane];
+        v.x += f.x; v.y += f.y; v.z += f.z; v.w += f.w;
     }
-    const int pos = wave * 16 + lr;
-    if (pos >= ms) return;
-    slot_t* d = p.slots + (int64_t)(p0 + pos) * a.cols + sl * a.r_max + j0 + lq * 4;
-    const float f[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) slot_put(d + q, __uint_as_float(hi_lo(f[q])), tag);
+    slot_t* d = p.slots + ((int64_t)c * LORA_DECODE_MAX_M + p0 + pos) * a.cols + sl * a.r_max + j0 + lq * 4;
+    slot_put(d, v.x, tag);
+    slot_put(d + 1, v.y, tag);
+    slot_put(d + 2, v.z, tag);
+    slot_put(d + 3, v.w, tag);
 }
 
 template <int TB, int NR>
-__global__ __launch_bounds__(kFpThreads) void k_linear_fp8(Fp8Params p) {
-    __shared__ float4 red[kFpWaves * TB * NR * kWave];
-    __shared__ uint16_t sHi[TB * 16 * kFpSLD], sLo[TB * 16 * kFpSLD];
+__global__ __launch_bounds__(kFpThreads, TB * NR == 8 ? 2 : 4) void k_linear_fp8(Fp8Params p) {
+    constexpr int kStage = fp8_stage(TB, NR);
+    __shared__ uint4 smem[kFpWaves * kStage];
+    __shared__ __attribute__((aligned(16))) uint16_t sHi[TB * 16 * kFpSLD], sLo[TB * 16 * kFpSLD];
     __shared__ int s_rp[TB * 16];
     const LinearArgs& a = p.a;
     const uint32_t tag = launch_tag();
     if ((int)blockIdx.x < p.n_prod) {
-        fp8_producer<TB>(p, tag, red);
+        fp8_producer<TB>(p, tag, smem, kStage);
         return;
     }
     const int ct = (int)blockIdx.x - p.n_prod;
     const int tid = threadIdx.x;
-    const int lane = lane_id(), wave = tid / kWave;
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int lr = lane % 16, lq = lane / 16;
     int sl = 0;
     while (sl + 1 < a.n_sl && ct >= p.tile_start[sl + 1]) ++sl;
     const int n0 = (int)(a.slice_off[sl] + (int64_t)(ct - p.tile_start[sl]) * (16 * NR));
     const int n1 = (int)min((int64_t)n0 + 16 * NR, a.slice_off[sl + 1]);
 
-    // ---- base product
-    const uint8_t* Wr[NR];
+    // small loads ahead of the stream (loads return in order): the tokens of
+    // the rows that this lane loads and of its column, the segments (lane s:
+    // segment s, at most 64 of them)
+    int m_row[2 * TB], tok[TB];
 #pragma unroll
-    for (int r = 0; r < NR; ++r) Wr[r] = p.W + (int64_t)min(n0 + r * 16 + lr, n1 - 1) * p.ldw;
-    const uint8_t* xr[TB];
-    float xs[TB];
-    int tok[TB];
+    for (int i = 0; i < 2 * TB; ++i) m_row[i] = a.sorted_idx[min(8 * i + lane / 8, a.M - 1)];
+#pragma unroll
+    for (int t = 0; t < TB; ++t) tok[t] = a.sorted_idx[min(t * 16 + lr, a.M - 1)];
+    const int nseg = __builtin_amdgcn_readfirstlane(a.num_segments[0]);
+    const int seg = min(lane, a.s_max - 1);
+    int q_id = a.req_to_lora[seg];
+    const int q_p0 = a.seg_indptr[seg], q_p1 = a.seg_indptr[seg + 1];
+
+    // ---- base product
+    const __amdgpu_buffer_rsrc_t rw = uniform_rsrc(p.W + (int64_t)n0 * p.ldw, (uint32_t)((n1 - n0 - 1) * p.ldw + a.K));
+    const __amdgpu_buffer_rsrc_t rx = uniform_rsrc(p.x8, (uint32_t)((int64_t)(a.M - 1) * p.ldx8 + a.K));
+    uint32_t off_w[2 * NR], off_x[2 * TB];
+#pragma unroll
+    for (int i = 0; i < 2 * NR; ++i)
+        off_w[i] = (uint32_t)(min(8 * i + lane / 8, n1 - n0 - 1) * p.ldw) + (lane % 8) * 16;
+    // blocks of 128 values in flight: W rows come from HBM, token rows from L2
+    constexpr int U = TB * NR == 8 ? 4 : 4 / NR, UX = TB * NR == 8 ? 2 : TB == 1 ? U : 4 / TB;
+    const int KB = (a.K + 127) / 128;
+    uint4 vw[U][2 * NR], vx[UX][2 * TB];
+    auto load_w = [&](int q, int kb) {
+        const bool in = kb * 128 + lane % 8 * 16 < a.K;
+#pragma unroll
+        for (int i = 0; i < 2 * NR; ++i) vw[q][i] = buf_ld16_at<true>(rw, in ? off_w[i] : kBufOff, (uint32_t)kb * 128u);
+    };
+    auto load_x = [&](int q, int kb) {
+        const bool in = kb * 128 + lane % 8 * 16 < a.K;
+#pragma unroll
+        for (int i = 0; i < 2 * TB; ++i) vx[q][i] = buf_ld16_at<false>(rx, in ? off_x[i] : kBufOff, (uint32_t)kb * 128u);
+    };
+    load_w(0, wave);
 #pragma unroll
     for (int t = 0; t < TB; ++t) {
-        int m = a.sorted_idx[min(t * 16 + lr, a.M - 1)];
-        if (table_fault(a.err, m < 0 || m >= a.M)) m = (m < 0 || m >= a.M) ? -1 : m;
-        tok[t] = t * 16 + lr < a.M ? m : -1;
-        m = max(m, 0);
-        xr[t] = p.x8 + (int64_t)m * p.ldx8;
-        xs[t] = p.x_scale[m];
+        if (table_fault(a.err, tok[t] < 0 || tok[t] >= a.M) && (tok[t] < 0 || tok[t] >= a.M)) tok[t] = -1;
+        if (t * 16 + lr >= a.M) tok[t] = -1;
     }
+#pragma unroll
+    for (int i = 0; i < 2 * TB; ++i) {
+        const int m = m_row[i];
+        const bool ok = 8 * i + lane / 8 < a.M && (!kTableChecks || (m >= 0 && m < a.M));
+        off_x[i] = ok ? (uint32_t)m * (uint32_t)p.ldx8 + (lane % 8) * 16 : kBufOff;
+    }
+#pragma unroll
+    for (int q = 0; q < UX; ++q) load_x(q, wave + q * kFpWaves);
+    // the rest of W only now, a round trip later: with all of it queued at once
+    // the producers' rows of A come behind 16 MB of W
+#pragma unroll
+    for (int q = 1; q < U; ++q) load_w(q, wave + q * kFpWaves);
+    // what the first loads name
+    const bool seg_ok = lane < nseg && q_id >= 0 && q_id < a.L;
+    const bool range_ok = q_p0 >= 0 && q_p1 >= q_p0 && q_p1 <= a.M;
+    table_fault(a.err, lane < nseg && !(seg_ok && range_ok));
+    q_id = seg_ok ? q_id : 0;
+    const int rank_l = a.rank[q_id];
+    const int64_t q_bo = a.b_off[q_id];
+    float xs[TB], ws[NR][4];
+#pragma unroll
+    for (int t = 0; t < TB; ++t) xs[t] = p.x_scale[max(tok[t], 0)];
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) ws[r][q] = p.w_scale[min(n0 + r * 16 + lq * 4 + q, n1 - 1)];
+    if (tid < TB * 16) s_rp[tid] = 0;
+
+    uint4* st = smem + wave * kStage;
+    uint4* sx = st + NR * 16 * 8;
+    const StageAt at;
     f32x4_t acc[NR][TB];
 #pragma unroll
     for (int r = 0; r < NR; ++r)
 #pragma unroll
         for (int t = 0; t < TB; ++t) acc[r][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    constexpr int U = TB * NR >= 8 ? 1 : TB >= 2 || NR >= 2 ? 2 : 4;   // K steps whose loads are in flight together
-    const int steps = (a.K + 127) / 128;
-    for (int i0 = wave; i0 < steps; i0 += U * kFpWaves) {
-        uint4 vw[U][NR][2], vx[U][TB][2];
+    for (int b0 = wave; b0 < KB; b0 += U * kFpWaves) {
 #pragma unroll
-        for (int q = 0; q < U; ++q)
+        for (int q = 0; q < U; ++q) {
+            // blocks past K read zeros (no memory is touched), and add none
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k = (i0 + q * kFpWaves) * 128 + h * 64 + lq * 16;
-                const int kc = min(k, a.K - 16);
-                const uint32_t mk = opaque_mask(k < a.K);
+            for (int i = 0; i < 2 * NR; ++i) st[at.piece(i)] = vw[q][i];
+            uint4 w[NR][2];
 #pragma unroll
-                for (int r = 0; r < NR; ++r) vw[q][r][h] = ld16(Wr[r] + kc);
+            for (int t = 0; t < TB; ++t) {
 #pragma unroll
-                for (int t = 0; t < TB; ++t) vx[q][t][h] = and4(ld16(xr[t] + kc), mk);
+                for (int i = 0; i < 2; ++i) sx[at.piece(i)] = vx[q % UX][2 * t + i];
+                stage_order();
+                if (t == 0)
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) w[r][0] = st[at.half(r, 0)], w[r][1] = st[at.half(r, 1)];
+                const uint4 x0 = sx[at.half(0, 0)], x1 = sx[at.half(0, 1)];
+#pragma unroll
+                for (int r = 0; r < NR; ++r) acc[r][t] = mfma_e4m3(w[r][0], w[r][1], x0, x1, acc[r][t]);
+                stage_order();
             }
-#pragma unroll
-        for (int q = 0; q < U; ++q)
-#pragma unroll
-            for (int r = 0; r < NR; ++r)
-#pragma unroll
-                for (int t = 0; t < TB; ++t)
-                    acc[r][t] = mfma_e4m3(vw[q][r][0], vw[q][r][1], vx[q][t][0], vx[q][t][1], acc[r][t]);
+            load_w(q, b0 + (q + U) * kFpWaves);
+            load_x(q % UX, b0 + (q + UX) * kFpWaves);
+        }
     }
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-        float ws[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) ws[q] = p.w_scale[min(n0 + r * 16 + lq * 4 + q, n1 - 1)];
+    for (int r = 0; r < NR; ++r)
 #pragma unroll
         for (int t = 0; t < TB; ++t)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) acc[r][t][q] *= xs[t] * ws[q];
-    }
+            for (int q = 0; q < 4; ++q) acc[r][t][q] *= xs[t] * ws[r][q];
 
-    // ---- deltas: lane s holds segment s (at most 64 of them)
-    const int nseg = a.num_segments[0];
-    const int seg = min(lane, a.s_max - 1);
-    int q_id = a.req_to_lora[seg];
-    const int q_p0 = a.seg_indptr[seg], q_p1 = a.seg_indptr[seg + 1];
-    const bool seg_ok = lane < nseg && q_id >= 0 && q_id < a.L;
-    const bool range_ok = q_p0 >= 0 && q_p1 >= q_p0 && q_p1 <= a.M;
-    table_fault(a.err, lane < nseg && !(seg_ok && range_ok));
-    q_id = seg_ok ? q_id : 0;
-    const int q_rp = seg_ok && (!kTableChecks || range_ok) ? a.rank[q_id] : 0;
-    const int64_t q_bo = a.b_off[q_id];
+    // ---- deltas
+    const int q_rp = seg_ok && (!kTableChecks || range_ok) ? rank_l : 0;
     if (__ballot(q_rp > 0) != 0ull) {
-        if (tid < TB * 16) s_rp[tid] = 0;
+        // B rows of the wavefront's first segments, in flight while S is read
+        constexpr int PB = TB * NR >= 4 ? 2 : 3;
+        uint4 pb[PB][NR][2];
+        auto load_b = [&](uint4 (&b)[NR][2], int s, int rp) {
+            const uint16_t* B = static_cast<const uint16_t*>(a.B) + readlane64(q_bo, s);
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    b[r][j] = ld16(B + (int64_t)min(n0 + r * 16 + lr, n1 - 1) * rp + min(j * 32 + lq * 8, rp - 8));
+        };
+#pragma unroll
+        for (int i = 0; i < PB; ++i) {
+            const int s = wave + i * kFpWaves, rp = __builtin_amdgcn_readlane(q_rp, s);
+            if (rp > 0) load_b(pb[i], s, rp);
+        }
         __syncthreads();
         if (wave == 0 && q_rp > 0)
             for (int i = max(q_p0, 0); i < min(q_p1, a.M); ++i) s_rp[i] = q_rp;
         __syncthreads();
-        // the slots of every position's own rank; the others stay zero
+        // S: the slots of every position's own rank, four a thread in flight
+        // together; positions and columns without one become zeros
+        const uint32_t want = tag ^ p.wc.poll_xor;
+        const int total = TB * 16 * a.r_max;             // a multiple of 4
         bool lost = false;
-        for (int e = tid; e < TB * 16 * a.r_max; e += kFpThreads) {
+        for (int e = tid * 4; e < total; e += kFpThreads * 4) {
             const int pos = e / a.r_max, j = e % a.r_max;
-            uint32_t w = 0;
-            if (j < s_rp[pos]) {
-                const slot_t* src = p.slots + (int64_t)pos * a.cols + sl * a.r_max + j;
-                const uint32_t want = tag ^ p.wc.poll_xor;
-                slot_t v = slot_load(src);
-                int spin = 0;
-                while (!slot_full(v, want) && spin < p.wc.max_spin) {
-                    __builtin_amdgcn_s_sleep(1);
-                    v = slot_load(src);
-                    ++spin;
-                }
-                lost |= !slot_full(v, want);
-                w = (uint32_t)v;
+            const bool on = j < s_rp[pos];               // ranks are multiples of 16
+            const slot_t* src = p.slots + (int64_t)(on ? pos : 0) * a.cols + sl * a.r_max + (on ? j : 0);
+            const int64_t second = p.chunks > 1 ? (int64_t)LORA_DECODE_MAX_M * a.cols : 0;
+            float f[4] = {0.f, 0.f, 0.f, 0.f};
+            int spin = 0;
+            // one slot is polled until it is full, then all are read: polls of
+            // all of them by every consumer slowed the producers down
+            while (on && spin < p.wc.max_spin && !slot_full(slot_load(src), want)) {
+                __builtin_amdgcn_s_sleep(2);
+                ++spin;
             }
-            sHi[pos * kFpSLD + j] = (uint16_t)(w >> 16);
-            sLo[pos * kFpSLD + j] = (uint16_t)w;
+            for (; on; ++spin) {
+                slot_t v[8];
+                bool full = true;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] = slot_load(src + q), v[4 + q] = slot_load(src + second + q);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    full &= slot_full(v[q], want) && slot_full(v[4 + q], want);
+                    f[q] = __uint_as_float((uint32_t)v[q]);
+                    if (second) f[q] += __uint_as_float((uint32_t)v[4 + q]);
+                }
+                if (full) break;
+                if (spin >= p.wc.max_spin) {
+                    lost = true;
+                    break;
+                }
+                __builtin_amdgcn_s_sleep(1);
+            }
+            const uint32_t w[4] = {hi_lo(f[0]), hi_lo(f[1]), hi_lo(f[2]), hi_lo(f[3])};
+            *reinterpret_cast<uint2*>(sHi + pos * kFpSLD + j) =
+                make_uint2((w[0] >> 16) | (w[1] & 0xffff0000u), (w[2] >> 16) | (w[3] & 0xffff0000u));
+            *reinterpret_cast<uint2*>(sLo + pos * kFpSLD + j) =
+                make_uint2((w[0] & 0xffffu) | (w[1] << 16), (w[2] & 0xffffu) | (w[3] << 16));
         }
         if (lost) atomicOr(a.err, LORA_DEVERR_WAIT);
         __syncthreads();
-        for (int s = wave; s < nseg; s += kFpWaves) {
+        auto add = [&](int s, const uint4 (&pbs)[NR][2]) {
             const int rp = __builtin_amdgcn_readlane(q_rp, s);
-            if (rp == 0) continue;
             const int p0 = __builtin_amdgcn_readlane(q_p0, s), p1 = __builtin_amdgcn_readlane(q_p1, s);
-            const uint16_t* B = static_cast<const uint16_t*>(a.B) + readlane64(q_bo, s);
 #pragma unroll
             for (int j = 0; j < LORA_MAX_RANK / 32; ++j) {
                 const int jj = j * 32 + lq * 8;
                 if (j * 32 >= rp) continue;
-                const uint32_t mj = opaque_mask(jj < rp);
                 uint4 b[NR];
 #pragma unroll
-                for (int r = 0; r < NR; ++r)
-                    b[r] = and4(ld16(B + (int64_t)min(n0 + r * 16 + lr, n1 - 1) * rp + min(jj, rp - 8)), mj);
+                for (int r = 0; r < NR; ++r) b[r] = and4(pbs[r][j], opaque_mask(jj < rp));
 #pragma unroll
                 for (int t = 0; t < TB; ++t) {
                     if (t * 16 >= p1 || t * 16 + 16 <= p0) continue;
@@ -291,34 +412,41 @@ __global__ __launch_bounds__(kFpThreads) void k_linear_fp8(Fp8Params p) {
                     }
                 }
             }
+        };
+#pragma unroll
+        for (int i = 0; i < PB; ++i)
+            if (__builtin_amdgcn_readlane(q_rp, wave + i * kFpWaves) > 0) add(wave + i * kFpWaves, pb[i]);
+        for (int s = wave + PB * kFpWaves; s < nseg; s += kFpWaves) {
+            const int rp = __builtin_amdgcn_readlane(q_rp, s);
+            if (rp == 0) continue;
+            load_b(pb[0], s, rp);
+            add(s, pb[0]);
         }
     }
 
-    // ---- join the eight partial sums; four columns of one token per thread
+    // ---- join the eight partial sums; four columns of one token per lane
+    float4* red = reinterpret_cast<float4*>(st);
 #pragma unroll
     for (int r = 0; r < NR; ++r)
 #pragma unroll
         for (int t = 0; t < TB; ++t)
-            red[(wave * NR * TB + r * TB + t) * kWave + lane] =
+            red[(r * TB + t) * kWave + lane] =
                 make_float4(acc[r][t][0], acc[r][t][1], acc[r][t][2], acc[r][t][3]);
     __syncthreads();
+    if (wave >= NR * TB) return;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int r = 0; r < NR; ++r)
+    for (int w = 0; w < kFpWaves; ++w) {
+        const float4 f = reinterpret_cast<const float4*>(smem + w * kStage)[wave * kWave + lane];
+        v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+    }
+    int m = tok[0];
 #pragma unroll
-        for (int t = 0; t < TB; ++t) {
-            if ((r * TB + t) % kFpWaves != wave) continue;
-            float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int w = 0; w < kFpWaves; ++w) {
-                const float4 f = red[(w * NR * TB + r * TB + t) * kWave + lane];
-                v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
-            }
-            const int n = n0 + r * 16 + lq * 4;          // slices are multiples of 8 wide
-            if (tok[t] >= 0 && n < n1)
-                *reinterpret_cast<uint2*>(p.y + (int64_t)tok[t] * p.ldy + n) =
-                    make_uint2(f32_to_bf16(v[0]) | (f32_to_bf16(v[1]) << 16),
-                               f32_to_bf16(v[2]) | (f32_to_bf16(v[3]) << 16));
-        }
+    for (int t = 1; t < TB; ++t) m = wave % TB == t ? tok[t] : m;
+    const int n = n0 + wave / TB * 16 + lq * 4;          // slices are multiples of 8 wide
+    if (m >= 0 && n < n1)
+        *reinterpret_cast<uint2*>(p.y + (int64_t)m * p.ldy + n) =
+            make_uint2(f32_to_bf16(v[0]) | (f32_to_bf16(v[1]) << 16), f32_to_bf16(v[2]) | (f32_to_bf16(v[3]) << 16));
 }
 
 template <int TB, int NR>
@@ -330,7 +458,9 @@ hipError_t launch_linear_fp8_as(Fp8Params& p, hipStream_t st) {
     }
     p.tile_start[p.a.n_sl] = t;
     p.jb = p.a.cols / 16;
-    p.n_prod = p.a.s_max * p.jb;
+    p.chunks = p.a.K > 1024 ? 2 : 1;
+    p.chunk_kb = ((p.a.K + 63) / 64 + p.chunks - 1) / p.chunks;
+    p.n_prod = p.a.s_max * p.jb * p.chunks;
     hipLaunchKernelGGL((k_linear_fp8<TB, NR>), dim3((unsigned)(p.n_prod + t)), dim3(kFpThreads), 0, st, p);
     return hipGetLastError();
 }
@@ -352,9 +482,12 @@ hipError_t launch_linear_fp8(const LinearArgs& a, const void* W8, int64_t ldw, c
     p.ldy = ldy;
     p.slots = reinterpret_cast<slot_t*>(static_cast<char*>(ws) + linear_ws_layout(0, a.K, a.cols).slots);
     p.wc = wait_ctl();
-    if (a.M <= 16) return launch_linear_fp8_as<1, 1>(p, st);
-    if (a.M <= 32) return launch_linear_fp8_as<2, 1>(p, st);
-    return launch_linear_fp8_as<4, 2>(p, st);
+    // a unit reads every token row once: twice the columns halve that, as long
+    // as two units are left for each compute unit
+    const bool wide = a.slice_off[a.n_sl] / 32 >= 512;
+    if (a.M <= 16) return wide ? launch_linear_fp8_as<1, 2>(p, st) : launch_linear_fp8_as<1, 1>(p, st);
+    if (a.M <= 32) return wide ? launch_linear_fp8_as<2, 2>(p, st) : launch_linear_fp8_as<2, 1>(p, st);
+    return wide ? launch_linear_fp8_as<4, 2>(p, st) : launch_linear_fp8_as<4, 1>(p, st);
 }
 
 }  // namespace mlora
