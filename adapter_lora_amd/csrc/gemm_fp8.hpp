@@ -3,11 +3,28 @@
 // S, then one product on e4m3 operands whose epilogue scales the sums by xs
 // ws, adds S B_i^T and rounds y once.
 //
-// The unit, the LDS ring, the swizzle and the epilogue are those of the bf16
-// product (gemm.hip): 128 sorted positions x 256 output columns, four waves,
-// stages of 128 bytes per row.  A stage holds 128 values of K instead of 64
-// and takes 16 v_mfma_f32_32x32x64_f8f6f4 of 64 cycles instead of 32 of 32, so
-// the same bytes through LDS carry twice the operations.
+// Work unit = (128 consecutive sorted positions, 256 output columns of one
+// slice); the rows of a unit may belong to several segments and to tokens
+// without an adapter.  Four waves, one per SIMD; wave w owns columns
+// [64 w, 64 w + 64) of the unit for all 128 rows: 4 x 2 blocks of
+// v_mfma_f32_32x32x64_f8f6f4 (64 cycles each), W rows as the first operand, so
+// that a lane holds four consecutive columns of one token, K in stages of 128.
+//
+// Both operands go through an LDS ring of three stages (48 KB each: 128 rows of
+// x8 and 256 of W8, 128 bytes).  Global loads read whole row segments (eight
+// lanes each), two stages ahead in registers; a stage is written to the ring
+// two stages before its use, so the next one is always readable and each wave
+// fetches its first operands while it multiplies the last of the current one.
+// One barrier per stage.  Chunk c of row r stands at c ^ (r / 2) % 8: operand
+// reads (32 rows, one chunk) and writes (8 rows, 8 chunks) meet distinct banks,
+// and rows 32 apart are a constant apart.  With one wave per SIMD every other
+// instruction is issued between two MFMAs, so the addresses are kept to one
+// addition per operand and stage: the ring slots are scalar offsets, W is read
+// through a buffer resource whose scalar offset is the stage, and only x rows
+// (tokens, any distance apart) have 64-bit addresses.
+//
+// The unit order gives workgroups that share an L2 (every eighth one) the same
+// columns of W for consecutive row tiles.
 #pragma once
 
 #include "common.hpp"
@@ -16,7 +33,8 @@
 
 namespace mlora {
 
-constexpr int kG8K = 128;                // K per stage
+constexpr int kG8K = 128;                          // K per stage
+constexpr int kG8Stage = (kGM + kGN) * kG8K;       // bytes of a ring slot
 
 // 32 x 32 x 64 on e4m3 operands, without block scales: lane l supplies row /
 // column l % 32 and 32 values of K (any 32, the same for both operands).
@@ -25,6 +43,15 @@ __device__ __forceinline__ f32x16_t mfma32_e4m3(const uint4& a0, const uint4& a1
     const i32x8_t a = {(int)a0.x, (int)a0.y, (int)a0.z, (int)a0.w, (int)a1.x, (int)a1.y, (int)a1.z, (int)a1.w};
     const i32x8_t b = {(int)b0.x, (int)b0.y, (int)b0.z, (int)b0.w, (int)b1.x, (int)b1.y, (int)b1.z, (int)b1.w};
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+}
+
+typedef __bf16 bf16x2_fp8_t __attribute__((ext_vector_type(2)));
+
+// Two fp32 values to a bf16 pair in one instruction, round to nearest even.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    const f2 v = {a, b};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_fp8_t));
 }
 
 struct GemmFp8Params {
@@ -38,6 +65,7 @@ struct GemmFp8Params {
     uint16_t* y;
     int64_t ldy;
     const float* S;              // fp32 [M][cols], sorted rows
+    int row_tiles;
     int col_tiles;               // 256-column tiles over all slices
     int tile_start[LORA_MAX_SLICES + 1];
     int nk2;                     // stages, rounded up to even
@@ -45,21 +73,81 @@ struct GemmFp8Params {
 };
 
 __global__ __launch_bounds__(kGThreads, 1) void k_gemm_fp8(GemmFp8Params p) {
-    __shared__ uint4 smem[kGRing * kGStage];
+    __shared__ uint4 smem[kGRing * kG8Stage / 16];
     __shared__ int s_tok[kGM];
     __shared__ float s_xs[kGM];
+    __shared__ __attribute__((aligned(16))) float s_ws[kGN];
     const LinearArgs& a = p.a;
-    const int u = (int)blockIdx.x;
-    const int rt = u / p.col_tiles;
-    const int ct = u % p.col_tiles;
+    // columns ct = 8 j + u % 8, bands of up to eight row tiles
+    const int u = (int)blockIdx.x / 8;
+    const int cts = (p.col_tiles + 7) / 8;
+    const int band = u / (8 * cts), v8 = u % (8 * cts);
+    const int in_band = min(8, p.row_tiles - band * 8);
+    const int rt = band * 8 + v8 % in_band;
+    const int ct = v8 / in_band * 8 + (int)blockIdx.x % 8;
+    if (ct >= p.col_tiles) return;
     const int tid = threadIdx.x;
     const int lane = lane_id();
-    const int wave = tid / kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int lr = lane % 32, lh = lane / 32;
     const int p0 = rt * kGM;
     const int rows = min(kGM, a.M - p0);
-    const int K = a.K;      // one byte per value: a stage is 128 of them
+    const int K = a.K;
 
+    // ---- columns of the unit (one slice)
+    int sl = 0;
+    while (sl + 1 < a.n_sl && ct >= p.tile_start[sl + 1]) ++sl;
+    const int n0 = (int)(a.slice_off[sl] + (int64_t)(ct - p.tile_start[sl]) * kGN);
+    const int n1 = (int)min((int64_t)n0 + kGN, a.slice_off[sl + 1]);
+
+    // ---- staging: thread t loads 16-byte chunk t % 8 of rows t / 8 + 32 i.
+    // The token indices are asked for first, the W rows need none of them.
+    const int tr = tid / 8, tc = tid % 8;
+    int xm[kGXL];
+#pragma unroll
+    for (int i = 0; i < kGXL; ++i) xm[i] = a.sorted_idx[p0 + min(tr + 32 * i, rows - 1)];
+    int my_tok = tid < rows ? a.sorted_idx[p0 + tid] : -1;
+    const __amdgpu_buffer_rsrc_t rw =
+        uniform_rsrc(p.W + (int64_t)n0 * p.ldw, (uint32_t)((n1 - n0 - 1) * p.ldw + K));
+    uint32_t woff[kGWL];
+#pragma unroll
+    for (int i = 0; i < kGWL; ++i)
+        woff[i] = (uint32_t)(min(tr + 32 * i, n1 - n0 - 1) * p.ldw) + tc * 16;
+    const uint8_t* xrow[kGXL];
+    uint4 rs[2][kGXL + kGWL];   // stages in flight (stage s in slot s % 2)
+    // W past K reads zeros; the x values it meets there are some of the row's own
+    auto gload_w = [&](int s, int slot, int i) {
+        rs[slot][kGXL + i] = buf_ld16_at<false>(rw, s * kG8K + tc * 16 < K ? woff[i] : kBufOff, (uint32_t)s * kG8K);
+    };
+    auto gload_x = [&](int s, int slot, int i) {
+        rs[slot][i] = ld16(xrow[i] + min(s * kG8K + tc * 16, K - 16));
+    };
+    char* const lds = reinterpret_cast<char*>(smem);
+    const int put = tr * 128 + (tc ^ (tr / 2 % 8)) * 16;
+    auto lstore = [&](int ring, int slot, int i) {
+        *reinterpret_cast<uint4*>(lds + put + ring + i * 4096) = rs[slot][i];
+    };
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < kGWL; ++i) gload_w(s, s, i);
+#pragma unroll
+    for (int i = 0; i < kGXL; ++i) {
+        const int m = (kTableChecks && (xm[i] < 0 || xm[i] >= a.M)) ? 0 : xm[i];
+        xrow[i] = p.x + (int64_t)m * p.ldx;
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < kGXL; ++i) gload_x(s, s, i);
+
+    // (checked builds) a token index outside the batch is never stored
+    if (table_fault(a.err, tid < rows && (my_tok < 0 || my_tok >= a.M))) {
+        if (tid < rows && (my_tok < 0 || my_tok >= a.M)) my_tok = -1;
+    }
+    const float my_xs = p.x_scale[max(my_tok, 0)];
+    const float my_ws = p.w_scale[min(n0 + tid, n1 - 1)];
+    static_assert(kGThreads == kGN, "one column scale per thread");
     // first round of the segment search, needed only by the epilogue:
     // lane j holds seg_indptr[j * stride] (entries past the segments hold
     // the number of tokens with an adapter)
@@ -77,83 +165,22 @@ __global__ __launch_bounds__(kGThreads, 1) void k_gemm_fp8(GemmFp8Params p) {
     const int q_rk = a.rank[lq];
     const int64_t q_bo = a.b_off[lq];
 
-    if (tid < kGM) {
-        int m = tid < rows ? a.sorted_idx[p0 + tid] : -1;
-        // (checked builds) a token index outside the batch is never stored
-        if (table_fault(a.err, tid < rows && (m < 0 || m >= a.M))) {
-            if (tid < rows && (m < 0 || m >= a.M)) m = -1;
-        }
-        s_tok[tid] = m;
-        s_xs[tid] = m >= 0 ? p.x_scale[m] : 0.f;
-    }
-
-    // ---- columns of the unit (one slice)
-    int sl = 0;
-    while (sl + 1 < a.n_sl && ct >= p.tile_start[sl + 1]) ++sl;
-    const int n0 = (int)(a.slice_off[sl] + (int64_t)(ct - p.tile_start[sl]) * kGN);
-    const int n1 = (int)min((int64_t)n0 + kGN, a.slice_off[sl + 1]);
-
-    // ---- staging: thread t loads 16-byte chunk t % 8 of rows t / 8 + 32 i
-    const int tr = tid / 8, tc = tid % 8;
-    const uint8_t* xrow[kGXL];
+    // ---- operands: K step t of a stage is chunks 4 t + 2 h + lh, h = 0, 1
+    int get[2][2];               // [t][h]: row lr
 #pragma unroll
-    for (int i = 0; i < kGXL; ++i) {
-        const int m = a.sorted_idx[p0 + min(tr + 32 * i, rows - 1)];
-        xrow[i] = p.x + (int64_t)((kTableChecks && (m < 0 || m >= a.M)) ? 0 : m) * p.ldx;
-    }
-    const uint8_t* wrow[kGWL];
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
-    for (int i = 0; i < kGWL; ++i)
-        wrow[i] = p.W + (int64_t)min(n0 + tr + 32 * i, n1 - 1) * p.ldw;
-
-    uint4 rs[2][kGXL + kGWL];   // stages in flight (stage s in slot s % 2)
-    auto kx = [&](int s) { return min(s * kG8K + tc * 16, K - 16); };
-    auto gload = [&](int s, int slot) {
-        const int k = kx(s);
-#pragma unroll
-        for (int i = 0; i < kGXL; ++i) rs[slot][i] = ld16(xrow[i] + k);
-#pragma unroll
-        for (int i = 0; i < kGWL; ++i) rs[slot][kGXL + i] = ld16(wrow[i] + k);
-    };
-    auto lstore = [&](int s, int slot) {
-        // x values past K are cleared; W there meets only those zeros
-        const uint32_t m = opaque_mask(s * kG8K + tc * 16 < K);
-        uint4* st = smem + (s % kGRing) * kGStage;
-#pragma unroll
-        for (int i = 0; i < kGXL; ++i) {
-            const uint4 v = rs[slot][i];
-            st[gsw(tr + 32 * i, tc)] = make_uint4(v.x & m, v.y & m, v.z & m, v.w & m);
-        }
-#pragma unroll
-        for (int i = 0; i < kGWL; ++i) st[kGM * 8 + gsw(tr + 32 * i, tc)] = rs[slot][kGXL + i];
-    };
-    // one load or one LDS write of the twelve per thread and stage
-    // (i < 4: x rows, else W rows); `i` is a literal at every call
-    auto gload1 = [&](int s, int slot, int i) {
-        rs[slot][i] = ld16((i < kGXL ? xrow[i] : wrow[i - kGXL]) + kx(s));
-    };
-    auto lstore1 = [&](int s, int slot, int i) {
-        uint4* st = smem + (s % kGRing) * kGStage;
-        if (i < kGXL) {
-            const uint32_t m = opaque_mask(s * kG8K + tc * 16 < K);
-            const uint4 v = rs[slot][i];
-            st[gsw(tr + 32 * i, tc)] = make_uint4(v.x & m, v.y & m, v.z & m, v.w & m);
-        } else {
-            st[kGM * 8 + gsw(tr + 32 * (i - kGXL), tc)] = rs[slot][i];
-        }
-    };
-    // MFMA operands of K step t (64 values) of stage s: two 16-byte chunks a lane
+        for (int h = 0; h < 2; ++h) get[t][h] = lr * 128 + ((4 * t + 2 * h + lh) ^ (lr / 2 % 8)) * 16;
+    const int wpart = kGM * 128 + wave * 64 * 128;
     struct Ops {
-        uint4 a[kGRB][2];
-        uint4 b[kGCB][2];
+        uint4 x[kGRB][2];
+        uint4 w[kGCB][2];
     };
     // one of the twelve operand reads of K step t (j < 8: x rows, else W rows)
-    auto oread1 = [&](Ops& o, int s, int t, int j) {
-        const uint4* st = smem + (s % kGRing) * kGStage;
+    auto oread1 = [&](Ops& o, int ring, int t, int j) {
         const int blk = j / 2, h = j % 2;
-        const int c = 4 * t + 2 * h + lh;
-        if (blk < kGRB) o.a[blk][h] = st[gsw(blk * 32 + lr, c)];
-        else o.b[blk - kGRB][h] = st[kGM * 8 + gsw(wave * 64 + (blk - kGRB) * 32 + lr, c)];
+        if (blk < kGRB) o.x[blk][h] = *reinterpret_cast<const uint4*>(lds + (get[t][h] + ring) + blk * 4096);
+        else o.w[blk - kGRB][h] = *reinterpret_cast<const uint4*>(lds + (get[t][h] + ring + wpart) + (blk - kGRB) * 4096);
     };
 
     f32x16_t acc[kGRB][kGCB];
@@ -165,46 +192,85 @@ __global__ __launch_bounds__(kGThreads, 1) void k_gemm_fp8(GemmFp8Params p) {
             for (int q = 0; q < 16; ++q) acc[rb][cb][q] = 0.f;
     auto mfma1 = [&](const Ops& o, int i) {
         const int rb = i / kGCB, cb = i % kGCB;
-        acc[rb][cb] = mfma32_e4m3(o.a[rb][0], o.a[rb][1], o.b[cb][0], o.b[cb][1], acc[rb][cb]);
+        acc[rb][cb] = mfma32_e4m3(o.w[cb][0], o.w[cb][1], o.x[rb][0], o.x[rb][1], acc[rb][cb]);
     };
 
     // prologue: stages 0 and 1 in LDS, stages 2 and 3 in flight, the first
     // operands of stage 0 read
-    gload(0, 0);
-    gload(1, 1);
-    lstore(0, 0);
-    gload(2, 0);
-    lstore(1, 1);
-    gload(3, 1);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+        for (int i = 0; i < kGXL + kGWL; ++i) lstore(s * kG8Stage, s, i);
+#pragma unroll
+        for (int i = 0; i < kGWL; ++i) gload_w(s + 2, s, i);
+#pragma unroll
+        for (int i = 0; i < kGXL; ++i) gload_x(s + 2, s, i);
+    }
+    if (tid < kGM) {
+        s_tok[tid] = my_tok;
+        s_xs[tid] = my_xs;
+    }
+    s_ws[tid] = my_ws;
     __syncthreads();
     Ops o0;
 #pragma unroll
     for (int j = 0; j < 12; ++j) oread1(o0, 0, 0, j);
 
-    // the unit's first two segments (start, end, rank, B offset; rank 0:
-    // none), for the B operands loaded during the last two stages
-    int sfirst = 0;
-    int pk_beg[2] = {0, 0}, pk_end[2] = {0, 0}, pk_rp[2] = {0, 0};
-    int64_t pk_bo[2] = {0, 0};
-    if (quick && p0 < m_valid) {
-        sfirst = 63 - __clzll((long long)__ballot(lane <= L && srch1 <= p0));
+    // segment s of the unit: rows [beg, end) of the sorted order, the adapter's
+    // rank (0: none) and B offset; beg past the unit: no more segments
+    struct Seg {
+        int beg, end, rp;
+        int64_t bo;
+    };
+    auto segment = [&](int s) {
+        Seg g{INT32_MAX, 0, 0, 0};
+        if (s >= nseg) return g;
+        int id;
+        if (quick) {
+            g.beg = __builtin_amdgcn_readlane(srch1, s);
+            g.end = __builtin_amdgcn_readlane(srch1, s + 1);
+            id = __builtin_amdgcn_readlane(q_id, s);
+        } else {
+            g.beg = __builtin_amdgcn_readfirstlane(a.seg_indptr[s]);
+            g.end = __builtin_amdgcn_readfirstlane(a.seg_indptr[s + 1]);
+            id = __builtin_amdgcn_readfirstlane(a.req_to_lora[s]);
+        }
+        if (g.beg >= p0 + rows) return g;
+        const bool id_ok = id >= 0 && id < L;   // never index past the table
+        table_fault(a.err, !id_ok);
+        if (!id_ok) return g;
+        g.rp = quick ? __builtin_amdgcn_readlane(q_rk, id) : __builtin_amdgcn_readfirstlane(a.rank[id]);
+        g.bo = quick ? readlane64(q_bo, id) : readlane64(a.b_off[id], 0);
+        return g;
+    };
+    auto load_b = [&](uint4 (&b)[kGCB][4], const Seg& g) {
+        if (g.rp == 0) return;
+        const uint16_t* Bt = reinterpret_cast<const uint16_t*>(a.B) + g.bo;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int sj = sfirst + j;
-            if (sj >= nseg) break;
-            pk_beg[j] = __builtin_amdgcn_readlane(srch1, sj);
-            pk_end[j] = __builtin_amdgcn_readlane(srch1, sj + 1);
-            const int id = __builtin_amdgcn_readlane(q_id, sj);
-            if (pk_beg[j] < p0 + rows && id >= 0 && id < L) {
-                pk_rp[j] = __builtin_amdgcn_readlane(q_rk, id);
-                pk_bo[j] = readlane64(q_bo, id);
-            }
+        for (int cb = 0; cb < kGCB; ++cb) {
+            const int n = min(n0 + wave * 64 + cb * 32 + lr, n1 - 1);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                b[cb][t] = ld16(Bt + (int64_t)n * g.rp + min(t * 16, g.rp - 16) + lh * 8);
+        }
+    };
+    // the segment that holds sorted position p0: the last s with seg_indptr[s] <= p0
+    const bool lora = p0 < m_valid && a.r_max > 0;
+    int s0 = 0;
+    if (lora) {
+        const uint64_t b1 = __ballot(lane * p.seg_stride <= L && srch1 <= p0);
+        s0 = (63 - __clzll((long long)b1)) * p.seg_stride;
+        if (!quick) {
+            const int v2 = a.seg_indptr[min(s0 + lane, L)];
+            const uint64_t b2 = __ballot(lane < p.seg_stride && s0 + lane <= L && v2 <= p0);
+            s0 += 63 - __clzll((long long)b2);
         }
     }
 
-    // stage ks; `slot` (ks & 1) is a literal at every call.  The ring slot of
-    // stage ks + 2 was last read (stage ks - 1) before the previous barrier;
-    // stage ks + 1 was written a stage ago, before that barrier.  Each MFMA (64
+    // stage ks; `slot` (ks & 1) is a literal at every call; r0, r1, r2 are the
+    // ring offsets of stages ks, ks + 1 and ks + 2.  The ring slot of stage
+    // ks + 2 was last read (stage ks - 1) before the previous barrier; stage
+    // ks + 1 was written a stage ago, before that barrier.  Each MFMA (64
     // cycles) is followed by its share of the stage's other work in a fixed
     // order: operand reads for the next K step throughout, the writes of
     // stage ks + 2 during the first K step, the loads of stage ks + 4 (into the
@@ -214,29 +280,32 @@ __global__ __launch_bounds__(kGThreads, 1) void k_gemm_fp8(GemmFp8Params p) {
     // (stages ks + 4 do not exist); 2 = MFMAs and operand reads only (the
     // last two stages: nothing left to write, no barrier); 3 = the same
     // without the reads for a next stage.
+    int r0 = 0, r1 = kG8Stage, r2 = 2 * kG8Stage;
     auto step = [&](int ks, int slot, int mode) {
         Ops o1;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             mfma1(o0, i);
-            if (i < 6) oread1(o1, ks, 1, 2 * i), oread1(o1, ks, 1, 2 * i + 1);
+            if (i < 6) oread1(o1, r0, 1, 2 * i), oread1(o1, r0, 1, 2 * i + 1);
             if (mode < 2) {
-                lstore1(ks + 2, slot, i);
-                if (i >= 4) lstore1(ks + 2, slot, 4 + i);
+                lstore(r2, slot, i);
+                if (i >= 4) lstore(r2, slot, 4 + i);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             mfma1(o1, i);
-            if (i < 6 && mode < 3) oread1(o0, ks + 1, 0, 2 * i), oread1(o0, ks + 1, 0, 2 * i + 1);
+            if (i < 6 && mode < 3) oread1(o0, r1, 0, 2 * i), oread1(o0, r1, 0, 2 * i + 1);
             if (mode == 0) {
-                gload1(ks + 4, slot, i);
-                if (i >= 4) gload1(ks + 4, slot, 4 + i);
+                gload_w(ks + 4, slot, i);
+                if (i >= 4) gload_x(ks + 4, slot, i - 4);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
         if (mode < 2) __syncthreads();
+        const int t = r0;
+        r0 = r1; r1 = r2; r2 = t;
     };
     int ks = 0;
     for (; ks + 4 < p.nk2; ks += 2) {
@@ -253,42 +322,38 @@ __global__ __launch_bounds__(kGThreads, 1) void k_gemm_fp8(GemmFp8Params p) {
     // values for this slice, the same for every segment (thread t: row t / 2,
     // rank positions 32 (t % 2) + 4 e, clamped into the row; positions past a
     // segment's rank are never multiplied), and the B operands of the first
-    // two segments (rank steps t < rp / 16, as below)
-    const bool lora = p0 < m_valid && a.r_max > 0;
+    // segment (rank steps t < rp / 16, as below)
     float4 sv[8];
     uint4 pb[2][kGCB][4];
+    Seg sg[2] = {{INT32_MAX, 0, 0, 0}, {INT32_MAX, 0, 0, 0}};
     if (lora) {
         const int srow = min(p0 + tid / 2, a.M - 1);
         const float* sp = p.S + (int64_t)srow * a.cols + sl * a.r_max;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             sv[e] = *reinterpret_cast<const float4*>(sp + min((tid % 2) * 32 + 4 * e, a.r_max - 4));
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if (pk_rp[j] == 0) continue;
-            const int rp = pk_rp[j];
-            const uint16_t* Bt = reinterpret_cast<const uint16_t*>(a.B) + pk_bo[j];
-#pragma unroll
-            for (int cb = 0; cb < kGCB; ++cb) {
-                const int n = min(n0 + wave * 64 + cb * 32 + lr, n1 - 1);
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    pb[j][cb][t] = ld16(Bt + (int64_t)n * rp + min(t * 16, rp - 16) + lh * 8);
-            }
-        }
+        sg[0] = segment(s0);
+        load_b(pb[0], sg[0]);
     }
     step(ks, 0, 2);
     step(ks + 1, 1, 3);
-    // ---- dequantization: row 8 (q / 4) + 4 lh + q % 4 of block rb, column lr of block cb
+    // ---- dequantization: row lr of block rb, columns 8 (q / 4) + 4 lh + q % 4 of block cb
+    float xs[kGRB];
 #pragma unroll
-    for (int cb = 0; cb < kGCB; ++cb) {
-        const float ws = p.w_scale[min(n0 + wave * 64 + cb * 32 + lr, n1 - 1)];
+    for (int rb = 0; rb < kGRB; ++rb) xs[rb] = s_xs[rb * 32 + lr];
 #pragma unroll
-        for (int rb = 0; rb < kGRB; ++rb)
+    for (int cb = 0; cb < kGCB; ++cb)
 #pragma unroll
-            for (int q = 0; q < 16; ++q)
-                acc[rb][cb][q] *= s_xs[rb * 32 + (q / 4) * 8 + lh * 4 + q % 4] * ws;
-    }
+        for (int g = 0; g < 4; ++g) {
+            const float4 ws = *reinterpret_cast<const float4*>(s_ws + wave * 64 + cb * 32 + 8 * g + 4 * lh);
+#pragma unroll
+            for (int rb = 0; rb < kGRB; ++rb) {
+                acc[rb][cb][4 * g] *= xs[rb] * ws.x;
+                acc[rb][cb][4 * g + 1] *= xs[rb] * ws.y;
+                acc[rb][cb][4 * g + 2] *= xs[rb] * ws.z;
+                acc[rb][cb][4 * g + 3] *= xs[rb] * ws.w;
+            }
+        }
     __syncthreads();     // every wave is done with the ring
 
     // ---- LoRA epilogue: the unit's S values as a bf16 hi / lo pair in LDS,
@@ -301,99 +366,51 @@ __global__ __launch_bounds__(kGThreads, 1) void k_gemm_fp8(GemmFp8Params p) {
             const int row = tid / 2, j0 = (tid % 2) * 32;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float f[4] = {sv[e].x, sv[e].y, sv[e].z, sv[e].w};
-                uint32_t h[4], l[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    h[q] = f32_to_bf16(f[q]);
-                    l[q] = f32_to_bf16(f[q] - bf16_to_f32(h[q]));
-                }
-                *reinterpret_cast<uint2*>(sHi + row * kSLD + j0 + 4 * e) =
-                    make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-                *reinterpret_cast<uint2*>(sLo + row * kSLD + j0 + 4 * e) =
-                    make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
+                const uint32_t h0 = pack_bf16(sv[e].x, sv[e].y), h1 = pack_bf16(sv[e].z, sv[e].w);
+                const uint32_t l0 = pack_bf16(sv[e].x - __uint_as_float(h0 << 16), sv[e].y - __uint_as_float(h0 & 0xffff0000u));
+                const uint32_t l1 = pack_bf16(sv[e].z - __uint_as_float(h1 << 16), sv[e].w - __uint_as_float(h1 & 0xffff0000u));
+                *reinterpret_cast<uint2*>(sHi + row * kSLD + j0 + 4 * e) = make_uint2(h0, h1);
+                *reinterpret_cast<uint2*>(sLo + row * kSLD + j0 + 4 * e) = make_uint2(l0, l1);
             }
         }
         __syncthreads();
-        // segment of sorted position p0: the last s with seg_indptr[s] <= p0
-        int s0 = sfirst;
-        if (!quick) {
-            const uint64_t b1 = __ballot(lane * p.seg_stride <= L && srch1 <= p0);
-            const int lo = (63 - __clzll((long long)b1)) * p.seg_stride;
-            const int v2 = a.seg_indptr[min(lo + lane, L)];
-            const uint64_t b2 = __ballot(lane < p.seg_stride && lo + lane <= L && v2 <= p0);
-            s0 = lo + 63 - __clzll((long long)b2);
-        }
-        for (int s = s0; s < nseg; ++s) {
-            const int k = quick ? s - s0 : 2;       // 0, 1: the prefetched segments
-            int beg, end, rp;
-            int64_t bo = 0;
-            uint4 bop[kGCB][4];
-            if (k == 0) {
-                beg = pk_beg[0]; end = pk_end[0]; rp = pk_rp[0];
-            } else if (k == 1) {
-                beg = pk_beg[1]; end = pk_end[1]; rp = pk_rp[1];
-            } else {
-                beg = a.seg_indptr[s];
-                end = a.seg_indptr[s + 1];
-                const int id = a.req_to_lora[s];
-                const bool id_ok = id >= 0 && id < L;   // never index past the table
-                table_fault(a.err, beg < p0 + rows && !id_ok);
-                rp = (beg < p0 + rows && id_ok) ? a.rank[id] : 0;
-                bo = id_ok ? a.b_off[id] : 0;
-            }
-            if (beg >= p0 + rows) break;
-            if (rp == 0) continue;
-            if (k == 0) {
-#pragma unroll
-                for (int cb = 0; cb < kGCB; ++cb)
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) bop[cb][t] = pb[0][cb][t];
-            } else if (k == 1) {
-#pragma unroll
-                for (int cb = 0; cb < kGCB; ++cb)
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) bop[cb][t] = pb[1][cb][t];
-            } else {
-                const uint16_t* Bt = reinterpret_cast<const uint16_t*>(a.B) + bo;
-#pragma unroll
-                for (int cb = 0; cb < kGCB; ++cb) {
-                    const int n = min(n0 + wave * 64 + cb * 32 + lr, n1 - 1);
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        bop[cb][t] = ld16(Bt + (int64_t)n * rp + min(t * 16, rp - 16) + lh * 8);
-                }
-            }
-            const int r0 = max(beg - p0, 0), r1 = min(end - p0, rows);
+        auto add = [&](int beg, int end, int rp, const uint4 (&bop)[kGCB][4]) {
+            const int b0 = max(beg - p0, 0), b1 = min(end - p0, rows);
 #pragma unroll
             for (int rb = 0; rb < kGRB; ++rb) {
-                if (rb * 32 + 32 <= r0 || rb * 32 >= r1) continue;
+                if (rb * 32 + 32 <= b0 || rb * 32 >= b1) continue;
                 const int row = rb * 32 + lr;
-                const uint32_t m = opaque_mask(row >= r0 && row < r1);
+                const uint32_t m = opaque_mask(row >= b0 && row < b1);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     if (t * 16 >= rp) continue;
                     const int o = row * kSLD + t * 16 + lh * 8;
-                    const uint4 h0 = *reinterpret_cast<const uint4*>(sHi + o);
-                    const uint4 l0 = *reinterpret_cast<const uint4*>(sLo + o);
-                    const uint4 h = make_uint4(h0.x & m, h0.y & m, h0.z & m, h0.w & m);
-                    const uint4 l = make_uint4(l0.x & m, l0.y & m, l0.z & m, l0.w & m);
+                    const uint4 h = and4(*reinterpret_cast<const uint4*>(sHi + o), m);
+                    const uint4 l = and4(*reinterpret_cast<const uint4*>(sLo + o), m);
 #pragma unroll
                     for (int cb = 0; cb < kGCB; ++cb) {
-                        acc[rb][cb] = mfma32_bf16(h, bop[cb][t], acc[rb][cb]);
-                        acc[rb][cb] = mfma32_bf16(l, bop[cb][t], acc[rb][cb]);
+                        acc[rb][cb] = mfma32_bf16(bop[cb][t], h, acc[rb][cb]);
+                        acc[rb][cb] = mfma32_bf16(bop[cb][t], l, acc[rb][cb]);
                     }
                 }
             }
+        };
+        // the next segment's B rows are in flight while one is added
+        for (int s = s0; sg[0].beg < p0 + rows; s += 2) {
+            sg[1] = segment(s + 1);
+            load_b(pb[1], sg[1]);
+            if (sg[0].rp > 0) add(sg[0].beg, sg[0].end, sg[0].rp, pb[0]);
+            sg[0] = segment(s + 2);
+            load_b(pb[0], sg[0]);
+            if (sg[1].beg < p0 + rows && sg[1].rp > 0) add(sg[1].beg, sg[1].end, sg[1].rp, pb[1]);
         }
         __syncthreads();     // the output staging below reuses the S rows' LDS
     }
 
     // ---- store through LDS (the ring is free: every wave has passed the last
     // barrier): each wave stages its 128 x 64 block as bf16, rows of 72
-    // values, then writes whole 16-byte row pieces.  acc[rb][cb][q] is row
-    // 32 rb + 8 (q / 4) + 4 lh + q % 4, column 64 w + 32 cb + lr.  A wave reads
-    // back only what it wrote itself, so no barrier is needed.
+    // values, then writes whole 128-byte row pieces.  A wave reads back only
+    // what it wrote itself, so no barrier is needed.
     {
         constexpr int OLD = 72;
         uint16_t* so = reinterpret_cast<uint16_t*>(smem) + wave * kGM * OLD;
@@ -402,9 +419,11 @@ __global__ __launch_bounds__(kGThreads, 1) void k_gemm_fp8(GemmFp8Params p) {
 #pragma unroll
             for (int cb = 0; cb < kGCB; ++cb)
 #pragma unroll
-                for (int q = 0; q < 16; ++q)
-                    so[(rb * 32 + (q / 4) * 8 + lh * 4 + q % 4) * OLD + cb * 32 + lr] =
-                        (uint16_t)f32_to_bf16(acc[rb][cb][q]);
+                for (int g = 0; g < 4; ++g)
+                    *reinterpret_cast<uint2*>(so + (rb * 32 + lr) * OLD + cb * 32 + 8 * g + 4 * lh) =
+                        make_uint2(pack_bf16(acc[rb][cb][4 * g], acc[rb][cb][4 * g + 1]),
+                                   pack_bf16(acc[rb][cb][4 * g + 2], acc[rb][cb][4 * g + 3]));
+        stage_order();
         const int c = lane % 8;
         const int n = n0 + wave * 64 + c * 8;       // slices are multiples of 8 wide
 #pragma unroll
@@ -441,8 +460,8 @@ hipError_t launch_gemm_fp8(const LinearArgs& a, const void* x8, int64_t ldx8, co
     const int nk = (a.K + kG8K - 1) / kG8K;
     p.nk2 = (nk + 1) / 2 * 2;
     p.seg_stride = (a.L + 1 + kWave - 1) / kWave;
-    const int row_units = (a.M + kGM - 1) / kGM;
-    const unsigned grid = (unsigned)(row_units * p.col_tiles);
+    p.row_tiles = (a.M + kGM - 1) / kGM;
+    const unsigned grid = (unsigned)(p.row_tiles * ((p.col_tiles + 7) / 8 * 8));
     hipLaunchKernelGGL(k_gemm_fp8, dim3(grid), dim3(kGThreads), 0, st, p);
     return hipGetLastError();
 }
