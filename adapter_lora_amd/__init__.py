@@ -561,15 +561,17 @@ def _matrix(t: Optional[torch.Tensor], name: str, shape, dtype):
     exactly this shape and dtype; zeros for None."""
     if t is None:
         return 0, 0
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise LoraError(f"{name} is {t.dtype} but must be {dtype}")
     if t.shape != shape:
         raise LoraError(f"{name} must be a tensor of shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise LoraError(f"{name} must live on the GPU")
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1]
     ld, unit = t.stride()
     if unit != 1 and t.numel() > 0:
         raise LoraError(f"{name} must have unit column stride")
-    if not t.is_cuda:
-        raise LoraError(f"{name} must live on the GPU")
     return t.data_ptr(), max(ld, shape[1])
 
 

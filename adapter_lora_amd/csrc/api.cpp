@@ -742,9 +742,9 @@ lora_status lora_linear_fp8(const lora_weights_t* w, const void* W8, int64_t ldw
                                           workspace, stream));
     }
     float* S = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + L.S);
-    hipError_t e = launch_shrink(a, x, ldx, S, workspace, stream);
-    if (e != hipSuccess) return LORA_HIP_ERROR;
-    return from_hip(launch_gemm_fp8(a, x8, ldx8, x_scale, W8, ldw, w_scale, S, y, ldy, stream));
+    if (!below_2gib(256, ldw, 1)) return LORA_UNSUPPORTED;
+    return from_hip(launch_linear_fp8_many(a, W8, ldw, w_scale, x8, ldx8, x_scale, x, ldx, S, y, ldy, workspace,
+                                           stream));
 }
 
 static lora_status check_experts(const lora_moe_experts_t* ex, const lora_moe_weights_t* w) {

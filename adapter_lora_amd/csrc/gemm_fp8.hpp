@@ -3,15 +3,23 @@
 // S, then one product on e4m3 operands whose epilogue scales the sums by xs
 // ws, adds S B_i^T and rounds y once.
 //
-// Work unit = (128 consecutive sorted positions, 256 output columns of one
+// Work unit = (32 RB consecutive sorted positions, 128 CB output columns of one
 // slice); the rows of a unit may belong to several segments and to tokens
-// without an adapter.  Four waves, one per SIMD; wave w owns columns
-// [64 w, 64 w + 64) of the unit for all 128 rows: 4 x 2 blocks of
-// v_mfma_f32_32x32x64_f8f6f4 (64 cycles each), W rows as the first operand, so
-// that a lane holds four consecutive columns of one token, K in stages of 128.
+// without an adapter.  Four waves, one per SIMD, side by side; each owns all
+// rows of 32 CB columns: RB x CB blocks of v_mfma_f32_32x32x64_f8f6f4 (64 cycles
+// each), W rows as the first operand, so that a lane holds four consecutive
+// columns of one token, K in stages of 128.
+//   128 x 256 (RB 4, CB 2): a stage takes 0.85 us on every compute unit, 2.5
+//     PFLOP/s; a large library product of this type reaches 2.6 on the same
+//     card.  With the LDS writes left out a stage took 0.62 us, with the loads
+//     left out 0.74; a third stage of loads in flight changed nothing, and
+//     256 x 256 units (fewer LDS accesses per MFMA, all 512 registers) ran at
+//     the same rate.
+//   64 x 128 (RB 2, CB 1): two to a compute unit, for batches with too few large
+//     units to fill the chip.
 //
-// Both operands go through an LDS ring of three stages (48 KB each: 128 rows of
-// x8 and 256 of W8, 128 bytes).  Global loads read whole row segments (eight
+// Both operands go through an LDS ring of three stages (rows of 128 bytes, 48 KB
+// or 24 KB a stage).  Global loads read whole row segments (eight
 // lanes each), two stages ahead in registers; a stage is written to the ring
 // two stages before its use, so the next one is always readable and each wave
 // fetches its first operands while it multiplies the last of the current one.
@@ -34,7 +42,15 @@
 namespace mlora {
 
 constexpr int kG8K = 128;                          // K per stage
-constexpr int kG8Stage = (kGM + kGN) * kG8K;       // bytes of a ring slot
+
+// Shape of a unit: 32 RB rows, 128 CB columns; four waves side by side.
+template <int RB_, int CB_> struct G8Shape {
+    static constexpr int RB = RB_, CB = CB_;
+    static constexpr int M = 32 * RB, N = 128 * CB;
+    static constexpr int Stage = (M + N) * kG8K;         // bytes of a ring slot
+    static constexpr int XL = M / 32, WL = N / 32;       // rows loaded per thread and stage
+    static constexpr int Waves = RB * CB >= 8 ? 1 : 2;   // per SIMD
+};
 
 // 32 x 32 x 64 on e4m3 operands, without block scales: lane l supplies row /
 // column l % 32 and 32 values of K (any 32, the same for both operands).
@@ -72,7 +88,10 @@ struct GemmFp8Params {
     int seg_stride;              // ceil((L + 1) / 64): first-round search stride
 };
 
-__global__ __launch_bounds__(kGThreads, 1) void k_gemm_fp8(GemmFp8Params p) {
+template <typename G>
+__global__ __launch_bounds__(kGThreads, G::Waves) void k_gemm_fp8(GemmFp8Params p) {
+    constexpr int kGM = G::M, kGN = G::N, kGXL = G::XL, kGWL = G::WL, kGRB = G::RB, kGCB = G::CB;
+    constexpr int kG8Stage = G::Stage, kWN = 32 * kGCB;          // columns of a wave
     __shared__ uint4 smem[kGRing * kG8Stage / 16];
     __shared__ int s_tok[kGM];
     __shared__ float s_xs[kGM];
@@ -147,7 +166,7 @@ __global__ __launch_bounds__(kGThreads, 1) void k_gemm_fp8(GemmFp8Params p) {
     }
     const float my_xs = p.x_scale[max(my_tok, 0)];
     const float my_ws = p.w_scale[min(n0 + tid, n1 - 1)];
-    static_assert(kGThreads == kGN, "one column scale per thread");
+    static_assert(kGThreads >= kGN && kGThreads >= kGM, "one row, one column scale per thread");
     // first round of the segment search, needed only by the epilogue:
     // lane j holds seg_indptr[j * stride] (entries past the segments hold
     // the number of tokens with an adapter)
@@ -171,12 +190,12 @@ __global__ __launch_bounds__(kGThreads, 1) void k_gemm_fp8(GemmFp8Params p) {
     for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int h = 0; h < 2; ++h) get[t][h] = lr * 128 + ((4 * t + 2 * h + lh) ^ (lr / 2 % 8)) * 16;
-    const int wpart = kGM * 128 + wave * 64 * 128;
+    const int wpart = (kGM + wave * kWN) * 128;
     struct Ops {
         uint4 x[kGRB][2];
         uint4 w[kGCB][2];
     };
-    // one of the twelve operand reads of K step t (j < 8: x rows, else W rows)
+    // one of the operand reads of K step t (x rows first)
     auto oread1 = [&](Ops& o, int ring, int t, int j) {
         const int blk = j / 2, h = j % 2;
         if (blk < kGRB) o.x[blk][h] = *reinterpret_cast<const uint4*>(lds + (get[t][h] + ring) + blk * 4096);
@@ -210,11 +229,12 @@ __global__ __launch_bounds__(kGThreads, 1) void k_gemm_fp8(GemmFp8Params p) {
         s_tok[tid] = my_tok;
         s_xs[tid] = my_xs;
     }
-    s_ws[tid] = my_ws;
+    if (tid < kGN) s_ws[tid] = my_ws;
     __syncthreads();
     Ops o0;
+    constexpr int kReads = 2 * (kGRB + kGCB), kMf = kGRB * kGCB, kLd = kGXL + kGWL;
 #pragma unroll
-    for (int j = 0; j < 12; ++j) oread1(o0, 0, 0, j);
+    for (int j = 0; j < kReads; ++j) oread1(o0, 0, 0, j);
 
     // segment s of the unit: rows [beg, end) of the sorted order, the adapter's
     // rank (0: none) and B offset; beg past the unit: no more segments
@@ -248,7 +268,7 @@ __global__ __launch_bounds__(kGThreads, 1) void k_gemm_fp8(GemmFp8Params p) {
         const uint16_t* Bt = reinterpret_cast<const uint16_t*>(a.B) + g.bo;
 #pragma unroll
         for (int cb = 0; cb < kGCB; ++cb) {
-            const int n = min(n0 + wave * 64 + cb * 32 + lr, n1 - 1);
+            const int n = min(n0 + wave * kWN + cb * 32 + lr, n1 - 1);
 #pragma unroll
             for (int t = 0; t < 4; ++t)
                 b[cb][t] = ld16(Bt + (int64_t)n * g.rp + min(t * 16, g.rp - 16) + lh * 8);
@@ -284,23 +304,27 @@ __global__ __launch_bounds__(kGThreads, 1) void k_gemm_fp8(GemmFp8Params p) {
     auto step = [&](int ks, int slot, int mode) {
         Ops o1;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kMf; ++i) {
             mfma1(o0, i);
-            if (i < 6) oread1(o1, r0, 1, 2 * i), oread1(o1, r0, 1, 2 * i + 1);
-            if (mode < 2) {
-                lstore(r2, slot, i);
-                if (i >= 4) lstore(r2, slot, 4 + i);
-            }
+#pragma unroll
+            for (int j = i * kReads / kMf; j < (i + 1) * kReads / kMf; ++j) oread1(o1, r0, 1, j);
+            if (mode < 2)
+#pragma unroll
+                for (int j = i * kLd / kMf; j < (i + 1) * kLd / kMf; ++j) lstore(r2, slot, j);
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kMf; ++i) {
             mfma1(o1, i);
-            if (i < 6 && mode < 3) oread1(o0, r1, 0, 2 * i), oread1(o0, r1, 0, 2 * i + 1);
-            if (mode == 0) {
-                gload_w(ks + 4, slot, i);
-                if (i >= 4) gload_x(ks + 4, slot, i - 4);
-            }
+            if (mode < 3)
+#pragma unroll
+                for (int j = i * kReads / kMf; j < (i + 1) * kReads / kMf; ++j) oread1(o0, r1, 0, j);
+            if (mode == 0)
+#pragma unroll
+                for (int j = i * kLd / kMf; j < (i + 1) * kLd / kMf; ++j) {
+                    if (j < kGWL) gload_w(ks + 4, slot, j);
+                    else gload_x(ks + 4, slot, j - kGWL);
+                }
             __builtin_amdgcn_sched_barrier(0);
         }
         if (mode < 2) __syncthreads();
@@ -319,19 +343,20 @@ __global__ __launch_bounds__(kGThreads, 1) void k_gemm_fp8(GemmFp8Params p) {
     }
 
     // ---- LoRA operands, loaded during the last two stages: the unit's S
-    // values for this slice, the same for every segment (thread t: row t / 2,
-    // rank positions 32 (t % 2) + 4 e, clamped into the row; positions past a
-    // segment's rank are never multiplied), and the B operands of the first
-    // segment (rank steps t < rp / 16, as below)
-    float4 sv[8];
+    // values for this slice, the same for every segment (kSV of a row per
+    // thread, clamped into the row; positions past a segment's rank are never
+    // multiplied), and the B operands of the first segment (rank steps
+    // t < rp / 16, as below)
+    constexpr int kSV = kGM * LORA_MAX_RANK / kGThreads, kSVT = LORA_MAX_RANK / kSV;
+    float4 sv[kSV / 4];
     uint4 pb[2][kGCB][4];
     Seg sg[2] = {{INT32_MAX, 0, 0, 0}, {INT32_MAX, 0, 0, 0}};
     if (lora) {
-        const int srow = min(p0 + tid / 2, a.M - 1);
+        const int srow = min(p0 + tid / kSVT, a.M - 1);
         const float* sp = p.S + (int64_t)srow * a.cols + sl * a.r_max;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            sv[e] = *reinterpret_cast<const float4*>(sp + min((tid % 2) * 32 + 4 * e, a.r_max - 4));
+        for (int e = 0; e < kSV / 4; ++e)
+            sv[e] = *reinterpret_cast<const float4*>(sp + min((tid % kSVT) * kSV + 4 * e, a.r_max - 4));
         sg[0] = segment(s0);
         load_b(pb[0], sg[0]);
     }
@@ -345,7 +370,7 @@ __global__ __launch_bounds__(kGThreads, 1) void k_gemm_fp8(GemmFp8Params p) {
     for (int cb = 0; cb < kGCB; ++cb)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            const float4 ws = *reinterpret_cast<const float4*>(s_ws + wave * 64 + cb * 32 + 8 * g + 4 * lh);
+            const float4 ws = *reinterpret_cast<const float4*>(s_ws + wave * kWN + cb * 32 + 8 * g + 4 * lh);
 #pragma unroll
             for (int rb = 0; rb < kGRB; ++rb) {
                 acc[rb][cb][4 * g] *= xs[rb] * ws.x;
@@ -363,9 +388,9 @@ __global__ __launch_bounds__(kGThreads, 1) void k_gemm_fp8(GemmFp8Params p) {
         uint16_t* sHi = reinterpret_cast<uint16_t*>(smem);   // the ring is free now
         uint16_t* sLo = sHi + kGM * kSLD;
         {
-            const int row = tid / 2, j0 = (tid % 2) * 32;
+            const int row = tid / kSVT, j0 = (tid % kSVT) * kSV;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < kSV / 4; ++e) {
                 const uint32_t h0 = pack_bf16(sv[e].x, sv[e].y), h1 = pack_bf16(sv[e].z, sv[e].w);
                 const uint32_t l0 = pack_bf16(sv[e].x - __uint_as_float(h0 << 16), sv[e].y - __uint_as_float(h0 & 0xffff0000u));
                 const uint32_t l1 = pack_bf16(sv[e].z - __uint_as_float(h1 << 16), sv[e].w - __uint_as_float(h1 & 0xffff0000u));
@@ -408,32 +433,48 @@ __global__ __launch_bounds__(kGThreads, 1) void k_gemm_fp8(GemmFp8Params p) {
     }
 
     // ---- store through LDS (the ring is free: every wave has passed the last
-    // barrier): each wave stages its 128 x 64 block as bf16, rows of 72
-    // values, then writes whole 128-byte row pieces.  A wave reads back only
-    // what it wrote itself, so no barrier is needed.
-    {
-        constexpr int OLD = 72;
-        uint16_t* so = reinterpret_cast<uint16_t*>(smem) + wave * kGM * OLD;
+    // barrier): each wave stages its part as bf16, rows of 8 values more than
+    // its columns, then writes whole row pieces.  A wave reads back only what
+    // it wrote itself, so no barrier is needed.
+    constexpr int OLD = kWN + 8, kCh = kWN / 8;     // 16-byte chunks of a row
+    uint16_t* so = reinterpret_cast<uint16_t*>(smem) + wave * kGM * OLD;
+    static_assert(4 * kGM * OLD * 2 <= kGRing * kG8Stage && 2 * kGM * kSLD * 2 <= kGRing * kG8Stage,
+                  "staged output and S must fit the ring");
 #pragma unroll
-        for (int rb = 0; rb < kGRB; ++rb)
+    for (int rb = 0; rb < kGRB; ++rb)
 #pragma unroll
-            for (int cb = 0; cb < kGCB; ++cb)
+        for (int cb = 0; cb < kGCB; ++cb)
 #pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    *reinterpret_cast<uint2*>(so + (rb * 32 + lr) * OLD + cb * 32 + 8 * g + 4 * lh) =
-                        make_uint2(pack_bf16(acc[rb][cb][4 * g], acc[rb][cb][4 * g + 1]),
-                                   pack_bf16(acc[rb][cb][4 * g + 2], acc[rb][cb][4 * g + 3]));
-        stage_order();
-        const int c = lane % 8;
-        const int n = n0 + wave * 64 + c * 8;       // slices are multiples of 8 wide
+            for (int g = 0; g < 4; ++g)
+                *reinterpret_cast<uint2*>(so + (rb * 32 + lr) * OLD + cb * 32 + 8 * g + 4 * lh) =
+                    make_uint2(pack_bf16(acc[rb][cb][4 * g], acc[rb][cb][4 * g + 1]),
+                               pack_bf16(acc[rb][cb][4 * g + 2], acc[rb][cb][4 * g + 3]));
+    stage_order();
+    const int c = lane % kCh;
+    const int n = n0 + wave * kWN + c * 8;          // slices are multiples of 8 wide
 #pragma unroll
-        for (int j = 0; j < kGM / 8; ++j) {
-            const int row = j * 8 + lane / 8;
-            const int m = s_tok[row];
-            const uint4 v = *reinterpret_cast<const uint4*>(so + row * OLD + c * 8);
-            if (m >= 0 && n < n1) *reinterpret_cast<uint4*>(p.y + (int64_t)m * p.ldy + n) = v;
-        }
+    for (int j = 0; j < kGM * kCh / kWave; ++j) {
+        const int row = j * (kWave / kCh) + lane / kCh;
+        const int m = s_tok[row];
+        const uint4 v = *reinterpret_cast<const uint4*>(so + row * OLD + c * 8);
+        if (m >= 0 && n < n1) *reinterpret_cast<uint4*>(p.y + (int64_t)m * p.ldy + n) = v;
     }
+}
+
+template <typename G>
+hipError_t launch_gemm_fp8_as(GemmFp8Params& p, hipStream_t st) {
+    const LinearArgs& a = p.a;
+    int t = 0;
+    for (int s = 0; s < a.n_sl; ++s) {
+        p.tile_start[s] = t;
+        t += (int)((a.slice_off[s + 1] - a.slice_off[s] + G::N - 1) / G::N);
+    }
+    p.tile_start[a.n_sl] = t;
+    p.col_tiles = t;
+    p.row_tiles = (a.M + G::M - 1) / G::M;
+    const unsigned grid = (unsigned)(p.row_tiles * ((p.col_tiles + 7) / 8 * 8));
+    hipLaunchKernelGGL((k_gemm_fp8<G>), dim3(grid), dim3(kGThreads), 0, st, p);
+    return hipGetLastError();
 }
 
 hipError_t launch_gemm_fp8(const LinearArgs& a, const void* x8, int64_t ldx8, const float* x_scale,
@@ -450,20 +491,46 @@ hipError_t launch_gemm_fp8(const LinearArgs& a, const void* x8, int64_t ldx8, co
     p.y = static_cast<uint16_t*>(y);
     p.ldy = ldy;
     p.S = S;
-    int t = 0;
-    for (int s = 0; s < a.n_sl; ++s) {
-        p.tile_start[s] = t;
-        t += (int)((a.slice_off[s + 1] - a.slice_off[s] + kGN - 1) / kGN);
-    }
-    p.tile_start[a.n_sl] = t;
-    p.col_tiles = t;
+    auto columns = [&](int width) {              // column tiles of that width
+        int64_t t = 0;
+        for (int i = 0; i < a.n_sl; ++i) t += (a.slice_off[i + 1] - a.slice_off[i] + width - 1) / width;
+        return t;
+    };
     const int nk = (a.K + kG8K - 1) / kG8K;
     p.nk2 = (nk + 1) / 2 * 2;
     p.seg_stride = (a.L + 1 + kWave - 1) / kWave;
-    p.row_tiles = (a.M + kGM - 1) / kGM;
-    const unsigned grid = (unsigned)(p.row_tiles * ((p.col_tiles + 7) / 8 * 8));
-    hipLaunchKernelGGL(k_gemm_fp8, dim3(grid), dim3(kGThreads), 0, st, p);
-    return hipGetLastError();
+    // Small units finish sooner while they fit the chip in few rounds: with K =
+    // 4096 a round of 256 small ones (two share a compute unit) takes 12 us, a
+    // round of 256 large ones 38, the rest of the call 12 and 6.  Measured, small
+    // against large: 256 x 4096 24.5 / 42.8 us, 768 x 4096 33.6 / 44.5, 768 x 8192
+    // 45.9 / 43.2, 2048 x 4096 54.8 / 47.7, 512 x 28672 112 / 96.
+    const int64_t ns = columns(128), nl = columns(256);
+    const int64_t small = ((a.M + 63) / 64 * ns + 255) / 256, large = ((a.M + 127) / 128 * nl + 255) / 256;
+    if (6 + 12 * small < 38 * large) return launch_gemm_fp8_as<G8Shape<2, 1>>(p, st);
+    return launch_gemm_fp8_as<G8Shape<4, 2>>(p, st);
+}
+
+// Any number of tokens, S by way of memory: shrink, then one of the products.
+hipError_t launch_linear_fp8_many(const LinearArgs& a, const void* W8, int64_t ldw, const float* w_scale,
+                                  const void* x8, int64_t ldx8, const float* x_scale, const void* x,
+                                  int64_t ldx, float* S, void* y, int64_t ldy, void* ws, hipStream_t st) {
+    // One launch over all of K reads the rows of x again for every 16 columns of
+    // S; partial sums over K (two launches) read them once.  Measured, the call
+    // with one and the other, 4096 wide: 512 tokens of 64 columns 41.5 / 45.8 us,
+    // 1024 44.3 / 45.4, 2048 57.1 / 55.5; 1024 tokens of 192 columns 55.0 / 52.6;
+    // 16384 tokens of 16 columns 195 / 203.
+    const bool rows = a.cols == 16 || (int64_t)a.M * a.cols <= 65536;
+    const hipError_t e = rows ? launch_shrink_rows(a, static_cast<const uint16_t*>(x), ldx, S, st)
+                              : launch_shrink(a, x, ldx, S, ws, st);
+    if (e != hipSuccess) return e;
+    // The decode kernel over groups of 64 tokens while one round of its units
+    // (32 columns a group) is enough and K is long enough for eight wavefronts
+    // to share: 65 tokens, 4096 x 4096 22.0 against 24.9 us with small units, K =
+    // 8192 and 512 tokens to 1024 columns 30.9 / 36.9; K = 1024 16.5 / 13.5.
+    const int64_t units = (a.M + 63) / 64 * ((a.slice_off[a.n_sl] + 31) / 32);
+    if (units <= 256 && a.K >= 2048 && ldx8 < INT32_MAX / (int64_t)a.M)
+        return launch_linear_fp8_groups(a, W8, ldw, w_scale, x8, ldx8, x_scale, S, y, ldy, st);
+    return launch_gemm_fp8(a, x8, ldx8, x_scale, W8, ldw, w_scale, S, y, ldy, st);
 }
 
 }  // namespace mlora

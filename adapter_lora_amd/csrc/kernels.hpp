@@ -226,15 +226,15 @@ struct NormParams {
 
 hipError_t launch_rms_norm(int dtype, const NormParams& p, hipStream_t st);
 
-// y = xs ws (x8 W8^T) + S B_i^T on e4m3 operands.  M <= LORA_DECODE_MAX_M in
-// one launch (linear_fp8.hpp); any M from S (fp32 [M][cols], sorted rows) with
-// launch_gemm_fp8 (gemm_fp8.hpp).
+// y = xs ws (x8 W8^T) + S B_i^T on e4m3 operands: M <= LORA_DECODE_MAX_M in one
+// launch (linear_fp8.hpp; `ws` holds the exchange slots), any M by way of S in
+// memory (gemm_fp8.hpp; fp32 [M][cols], sorted rows, `ws` the partial sums).
 hipError_t launch_linear_fp8(const LinearArgs& a, const void* W8, int64_t ldw, const float* w_scale,
                              const void* x8, int64_t ldx8, const float* x_scale, const void* x,
                              int64_t ldx, void* y, int64_t ldy, void* ws, hipStream_t st);
-hipError_t launch_gemm_fp8(const LinearArgs& a, const void* x8, int64_t ldx8, const float* x_scale,
-                           const void* W8, int64_t ldw, const float* w_scale, const float* S, void* y,
-                           int64_t ldy, hipStream_t st);
+hipError_t launch_linear_fp8_many(const LinearArgs& a, const void* W8, int64_t ldw, const float* w_scale,
+                                  const void* x8, int64_t ldx8, const float* x_scale, const void* x,
+                                  int64_t ldx, float* S, void* y, int64_t ldy, void* ws, hipStream_t st);
 
 // A whole MoE layer for few tokens (moe_decode.hpp).
 struct MoeDecodeParams {

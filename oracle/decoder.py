@@ -30,11 +30,13 @@ def row_scale(v) -> np.ndarray:
 
 def linear_fp8_mag(x8, x_scale, W8, w_scale, x, ids, A: Sequence[np.ndarray],
                    B: Sequence[np.ndarray], ranks: Sequence[int],
-                   slice_sizes: Sequence[int]) -> Tuple[np.ndarray, np.ndarray]:
-    """y = (x8 xs)(W8 ws)^T + the adapter's delta per token; A[i] [n_sl * r, K]
+                   slice_sizes: Sequence[int]) -> Tuple[np.ndarray, np.ndarray, np.ndarray]:
+    """y = (x8 xs)(W8 ws)^T + the adapter's delta per token, with the term
+    magnitudes of the base product and of the delta; A[i] [n_sl * r, K]
     slice-major, B[i] [N, r]."""
     xd, Wd = x8 * x_scale[:, None], W8 * w_scale[:, None]
     y, mag = xd @ Wd.T, np.abs(xd) @ np.abs(Wd).T
+    dmag = np.zeros_like(y)
     for m in range(x.shape[0]):
         i = int(ids[m])
         if i < 0 or i >= len(ranks) or ranks[i] == 0:
@@ -43,9 +45,9 @@ def linear_fp8_mag(x8, x_scale, W8, w_scale, x, ids, A: Sequence[np.ndarray],
         for s, n in enumerate(slice_sizes):
             a, b = A[i][s * r:(s + 1) * r], B[i][n0:n0 + n]
             y[m, n0:n0 + n] += b @ (a @ x[m])
-            mag[m, n0:n0 + n] += np.abs(b) @ (np.abs(a) @ np.abs(x[m]))
+            dmag[m, n0:n0 + n] += np.abs(b) @ (np.abs(a) @ np.abs(x[m]))
             n0 += n
-    return y, mag
+    return y, mag, dmag
 
 
 def route(x, router, topk: int, renormalize: bool) -> Tuple[np.ndarray, np.ndarray]:

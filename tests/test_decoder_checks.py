@@ -210,8 +210,9 @@ def test_oracle_linear_agrees_with_the_dense_oracle():
     ids = np.array([0, 2, -1, 1, 0, 2, 2, -1, 0])
     base = (x8 * xs[:, None]) @ (W8 * ws[:, None]).T
     want = L.lora_linear(x, ids, A, B, ranks, sizes, base)
-    got, mag = D.linear_fp8_mag(x8, xs, W8, ws, x, ids, A, B, ranks, sizes)
-    assert np.allclose(got, want, rtol=0, atol=1e-12) and (mag >= np.abs(got) - 1e-12).all()
+    got, mag, dmag = D.linear_fp8_mag(x8, xs, W8, ws, x, ids, A, B, ranks, sizes)
+    assert np.allclose(got, want, rtol=0, atol=1e-12) and (mag + dmag >= np.abs(got) - 1e-12).all()
+    assert not dmag[[2, 3, 7]].any()                             # no adapter, an empty slot
 
 
 @pytest.mark.parametrize("shared", [False, True])
