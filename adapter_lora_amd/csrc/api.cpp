@@ -790,7 +790,7 @@ MoeDecodeWs moe_decode_ws(const lora_moe_experts_t* ex, int r, int M) {
     l.ids = take(P * sizeof(int32_t));
     l.s_gu = take(P * r * sizeof(slot_t));
     l.s_d = take(P * r * sizeof(slot_t));
-    l.join = take((size_t)(moe_decode_splits(ex->H) - 1) * M * ex->H * sizeof(slot_t));
+    l.join = take((size_t)(moe_decode_splits(ex->H, M) - 1) * M * ex->H * sizeof(slot_t));
     l.h = take(P * ex->I * sizeof(uint16_t));
     l.total = off;
     return l;
@@ -800,7 +800,9 @@ MoeDecodeWs moe_decode_ws(const lora_moe_experts_t* ex, int r, int M) {
 size_t lora_moe_decode_workspace_size(const lora_moe_weights_t* w, const lora_moe_experts_t* ex,
                                       int32_t M) {
     if (check_experts(ex, w) != LORA_OK || M < 0 || M > LORA_DECODE_MAX_M) return 0;
-    return moe_decode_ws(ex, w ? w->r : 0, M).total;
+    // enough for fewer tokens too (up to 32 take more splits)
+    const int r = w ? w->r : 0;
+    return std::max(moe_decode_ws(ex, r, M).total, moe_decode_ws(ex, r, std::min(M, 32)).total);
 }
 
 lora_status lora_moe_decode(const lora_moe_weights_t* w, const lora_moe_experts_t* ex,
@@ -844,7 +846,7 @@ lora_status lora_moe_decode(const lora_moe_weights_t* w, const lora_moe_experts_
     p.S_d = reinterpret_cast<slot_t*>(ws + l.s_d);
     p.join = reinterpret_cast<slot_t*>(ws + l.join);
     p.h = reinterpret_cast<uint16_t*>(ws + l.h);
-    p.splits = moe_decode_splits(ex->H);
+    p.splits = moe_decode_splits(ex->H, M);
     p.wc = wait_ctl();
     return from_hip(launch_moe_decode(p, stream));
 }

@@ -269,7 +269,7 @@ struct MoeDecodeParams {
 };
 
 // Workgroups that share one tile of 16 output columns of the second launch.
-int moe_decode_splits(int H);
+int moe_decode_splits(int H, int M);
 
 hipError_t launch_moe_decode(const MoeDecodeParams& p, hipStream_t st);
 

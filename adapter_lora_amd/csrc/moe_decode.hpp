@@ -82,6 +82,27 @@ __device__ __forceinline__ void slot_wait8(const slot_t* s, bool on, uint32_t wa
     }
 }
 
+// Twice four consecutive slots, in flight together.
+__device__ __forceinline__ void slot_wait4x2(const slot_t* a, const slot_t* b, uint32_t want, int max_spin, bool* lost,
+                                             float* f) {
+    for (int spin = 0;; ++spin) {
+        slot_t v[8];
+        bool full = true;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = slot_load(a + q), v[4 + q] = slot_load(b + q);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            full &= slot_full(v[q], want);
+            f[q] = __uint_as_float((uint32_t)v[q]);
+        }
+        if (full || spin >= max_spin) {
+            *lost |= !full;
+            return;
+        }
+        __builtin_amdgcn_s_sleep(1);
+    }
+}
+
 typedef __bf16 md_bf16x2_t __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ float md_dot8(const uint4& a, const uint4& b, float c) {
     const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
@@ -119,17 +140,40 @@ __device__ __forceinline__ int md_adapter(const MoeDecodeParams& p, int m) {
 }
 
 // ---------------------------------------------------------------- router
+// Logits of one token: AT experts of a wavefront together, UN chunks of 512
+// values of each in flight.
+template <int AT, int UN>
+__device__ __forceinline__ void md_logits(const MoeDecodeParams& p, const uint16_t* x, float* s_logit) {
+    const int lane = lane_id(), wave = (int)threadIdx.x / kWave;
+    for (int e0 = wave; e0 < p.E; e0 += AT * kMdWaves) {
+        const uint16_t* w[AT];
+        float c[AT];
+#pragma unroll
+        for (int i = 0; i < AT; ++i) {
+            w[i] = p.router + (int64_t)min(e0 + i * kMdWaves, p.E - 1) * p.H;
+            c[i] = 0.f;
+        }
+#pragma unroll UN
+        for (int k = lane * 8; k < p.H; k += kWave * 8) {
+            const uint4 v = ld16(x + k);
+#pragma unroll
+            for (int i = 0; i < AT; ++i) c[i] = md_dot8(ld16(w[i] + k), v, c[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < AT; ++i) {
+            c[i] = wave_total(c[i]);
+            if (lane == 0 && e0 + i * kMdWaves < p.E) s_logit[e0 + i * kMdWaves] = c[i];
+        }
+    }
+}
+
 __device__ __forceinline__ void md_router(const MoeDecodeParams& p, uint32_t tag, int m, float* s_logit) {
     const int lane = lane_id(), wave = (int)threadIdx.x / kWave;
     const uint16_t* x = p.x + (int64_t)m * p.ldx;
-    for (int e = wave; e < p.E; e += kMdWaves) {
-        const uint16_t* w = p.router + (int64_t)e * p.H;
-        float c = 0.f;
-#pragma unroll 4
-        for (int k = lane * 8; k < p.H; k += kWave * 8) c = md_dot8(ld16(x + k), ld16(w + k), c);
-        c = wave_total(c);
-        if (lane == 0) s_logit[e] = c;
-    }
+    // an expert's row is a chain of loads: several experts at a time
+    if (p.E <= 2 * kMdWaves) md_logits<2, 8>(p, x, s_logit);
+    else if (p.E <= 16 * kMdWaves) md_logits<8, 2>(p, x, s_logit);
+    else md_logits<16, 1>(p, x, s_logit);
     __syncthreads();
     if (wave != 0) return;
     // four experts a lane; a logit as an ordered integer, so that the largest
@@ -267,26 +311,28 @@ __device__ __forceinline__ unsigned long long md_uni(unsigned long long v) {
 
 // ---------------------------------------------------------------- the stream
 // One block: 128 bytes of each of 32 expert rows (64 values of K in bf16, 128 in
-// 8 bits) and the same values of TB x 16 token rows, in registers from their
-// load to their turn.  A wavefront keeps U blocks in flight.
-template <bool W8, int TB> struct MdBlock {
+// 8 bits) and the same values of 8 XP token rows, in registers from their load
+// to their turn.  A wavefront keeps U blocks in flight.
+constexpr int md_blocks_of(int XP) { return (XP + 1) / 2; }      // 16-column token blocks
+
+template <bool W8, int XP> struct MdBlock {
     static constexpr int XH = W8 ? 2 : 1;          // 64-value parts of a block
     static constexpr int KV = 64 * XH;
     uint4 w[4];
-    uint4 x[XH][2 * TB];
+    uint4 x[XH][XP];
 };
 
 // Where a wavefront's loads go: lane l takes row l / 8 of each group of eight
 // and chunk l % 8 of its 128 bytes.
-template <int TB> struct MdRows {
+template <int XP> struct MdRows {
     uint32_t w[4];                                 // byte offsets in the expert's matrix
-    uint32_t x[2 * TB];                            // in the token matrix; kBufOff: no such row
+    uint32_t x[XP];                                // in the token matrix; kBufOff: no such row
 };
 
-template <bool W8, int TB>
-__device__ __forceinline__ void md_issue(MdBlock<W8, TB>& b, __amdgpu_buffer_rsrc_t rw, __amdgpu_buffer_rsrc_t rx,
-                                         const MdRows<TB>& r, int kb, int K) {
-    using B = MdBlock<W8, TB>;
+template <bool W8, int XP>
+__device__ __forceinline__ void md_issue(MdBlock<W8, XP>& b, __amdgpu_buffer_rsrc_t rw, __amdgpu_buffer_rsrc_t rx,
+                                         const MdRows<XP>& r, int kb, int K) {
+    using B = MdBlock<W8, XP>;
     const int c = lane_id() % 8;
     // chunks past the end of the row read zeros, in both operands
     const bool w_in = kb * B::KV + c * (W8 ? 16 : 8) < K;
@@ -296,22 +342,26 @@ __device__ __forceinline__ void md_issue(MdBlock<W8, TB>& b, __amdgpu_buffer_rsr
     for (int h = 0; h < B::XH; ++h) {
         const bool x_in = kb * B::KV + h * 64 + c * 8 < K;
 #pragma unroll
-        for (int i = 0; i < 2 * TB; ++i)
+        for (int i = 0; i < XP; ++i)
             b.x[h][i] = buf_ld16_at<false>(rx, x_in ? r.x[i] : kBufOff, (uint32_t)(kb * B::XH + h) * 128u);
     }
 }
 
-// uint4 of LDS per wavefront: 32 expert rows and 16 token rows (32 of TB = 4,
+// uint4 of LDS per wavefront: 32 expert rows and 16 token rows (32 of XP = 8,
 // whose partial sums need the room at the end)
-constexpr int md_stage_words(int TB) { return 32 * 8 + (TB < 4 ? 16 : 32) * 8; }
+constexpr int md_stage_words(int XP) { return 32 * 8 + (XP < 8 ? 16 : 32) * 8; }
 
 // acc[n][t] += rows 16 n .. 16 n + 15 times token block t over the block's
 // values.  `refill` issues the block's next loads once its registers are free.
-template <bool W8, int TB, typename F>
-__device__ __forceinline__ void md_consume(MdBlock<W8, TB>& b, uint4* st, const StageAt& at, f32x4_t (&acc)[2][TB],
-                                           F refill) {
-    using B = MdBlock<W8, TB>;
-    constexpr int XT = TB < 4 ? 1 : 2;            // token blocks staged at a time
+// With XP = 1 the operand's columns 8 to 15 are whatever LDS holds: they only
+// reach sums that nobody reads.
+template <bool W8, int XP, typename F>
+__device__ __forceinline__ void md_consume(MdBlock<W8, XP>& b, uint4* st, const StageAt& at,
+                                           f32x4_t (&acc)[2][md_blocks_of(XP)], F refill) {
+    using B = MdBlock<W8, XP>;
+    constexpr int TB = md_blocks_of(XP);
+    constexpr int XT = XP < 8 ? 1 : 2;             // token blocks staged at a time
+    constexpr int PT = XP == 1 ? 1 : 2 * XT;       // their pieces
     uint4* sx = st + 32 * 8;
 #pragma unroll
     for (int i = 0; i < 4; ++i) st[at.piece(i)] = b.w[i];
@@ -320,7 +370,7 @@ __device__ __forceinline__ void md_consume(MdBlock<W8, TB>& b, uint4* st, const 
 #pragma unroll
         for (int t0 = 0; t0 < TB; t0 += XT) {
 #pragma unroll
-            for (int i = 0; i < 2 * XT; ++i) sx[at.piece(i)] = b.x[h][2 * t0 + i];
+            for (int i = 0; i < PT; ++i) sx[at.piece(i)] = b.x[h][2 * t0 + i];
             stage_order();
             if (h == B::XH - 1 && t0 + XT >= TB) refill();
             uint4 a[2][2];
@@ -426,13 +476,14 @@ __device__ __forceinline__ void md_step_add(const MoeDecodeParams& p, const uint
 // (up to 32 tokens of an expert, 16 gate and 16 up rows).  The wavefronts share a unit's K, block
 // by block in turn; the loads of the next unit are issued from the last blocks of the
 // one before, so the stream does not stop at its end.
-template <bool W8, int TB, int U>
+template <bool W8, int XP, int U>
 __device__ __forceinline__ void md_gate_up(const MoeDecodeParams& p, const MdRoute& rt, const float* s_w,
                                            const int16_t* s_ad, uint32_t* s_S, uint4* smem, int first, int stride,
                                            uint32_t want, bool* lost) {
-    using B = MdBlock<W8, TB>;
+    using B = MdBlock<W8, XP>;
+    constexpr int TB = md_blocks_of(XP);
     constexpr int kBytes = W8 ? 1 : 2;
-    constexpr int kWords = md_stage_words(TB);
+    constexpr int kWords = md_stage_words(XP);
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     const int lr = lane % 16, lq = lane / 16;
     uint4* st = smem + wave * kWords;
@@ -444,7 +495,7 @@ __device__ __forceinline__ void md_gate_up(const MoeDecodeParams& p, const MdRou
     const uint32_t ebytes = (uint32_t)(2 * p.I) * (uint32_t)p.H * kBytes;
     const __amdgpu_buffer_rsrc_t rx = uniform_rsrc(p.x, (uint32_t)(((int64_t)(p.M - 1) * p.ldx + p.H) * 2));
 
-    MdRows<TB> rows;
+    MdRows<XP> rows;
     const char* wbase = nullptr;
     int u_load = first, b_load = 0;
     auto set_rows = [&]() {                        // the unit that loads are issued for
@@ -460,7 +511,7 @@ __device__ __forceinline__ void md_gate_up(const MoeDecodeParams& p, const MdRou
         }
         const int ne = __popcll(md_uni(rt.mask[e])) - skip, base = md_uni((int)rt.base[e]) + skip;
 #pragma unroll
-        for (int i = 0; i < 2 * TB; ++i) {
+        for (int i = 0; i < XP; ++i) {
             const int t = 8 * i + lane / 8;
             rows.x[i] = t < ne ? (uint32_t)((int)rt.list[base + t] / p.topk) * (uint32_t)p.ldx * 2u + (lane % 8) * 16
                                : kBufOff;
@@ -469,7 +520,7 @@ __device__ __forceinline__ void md_gate_up(const MoeDecodeParams& p, const MdRou
     auto issue = [&](B& b) {
         const int kb = b_load * kMdWaves + wave;
         const bool on = u_load < units && kb < KB;
-        md_issue<W8, TB>(b, uniform_rsrc(wbase, on ? ebytes : 0u), rx, rows, on ? kb : KB, p.H);
+        md_issue<W8, XP>(b, uniform_rsrc(wbase, on ? ebytes : 0u), rx, rows, on ? kb : KB, p.H);
         if (++b_load == nb) {
             b_load = 0;
             u_load += stride;
@@ -508,7 +559,7 @@ __device__ __forceinline__ void md_gate_up(const MoeDecodeParams& p, const MdRou
         if (step.l >= 0) md_step_load(p, p.B_gu, (int64_t)p.E * 2 * p.I * p.r, row, step, bop);
         for (int b = 0; b < nb; b += U)
 #pragma unroll
-            for (int q = 0; q < U; ++q) md_consume<W8, TB>(blk[q], st, at, acc, [&]() { issue(blk[q]); });
+            for (int q = 0; q < U; ++q) md_consume<W8, XP>(blk[q], st, at, acc, [&]() { issue(blk[q]); });
         if constexpr (W8) {
             // columns past I (a ragged last tile) are never stored
 #pragma unroll
@@ -518,8 +569,12 @@ __device__ __forceinline__ void md_gate_up(const MoeDecodeParams& p, const MdRou
         }
         if (p.L > 0) {
             if (u == first && s_S) {               // every unit reads S: once from the slots into LDS
-                for (int i = (int)threadIdx.x; i < p.M * p.topk * p.r; i += kMdThreads)
-                    s_S[i] = s_ad[i / (p.topk * p.r)] >= 0 ? slot_wait(p.S_gu + i, want, p.wc.max_spin, lost) : 0u;
+                for (int i = (int)threadIdx.x * 8; i < p.M * p.topk * p.r; i += kMdThreads * 8) {
+                    uint32_t w[8];
+                    slot_wait8(p.S_gu + i, s_ad[i / (p.topk * p.r)] >= 0, want, p.wc.max_spin, lost, w);
+                    *reinterpret_cast<uint4*>(s_S + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4*>(s_S + i + 4) = make_uint4(w[4], w[5], w[6], w[7]);
+                }
                 __syncthreads();
             }
             for (int d = wave; step.l >= 0;) {
@@ -557,13 +612,15 @@ __device__ __forceinline__ void md_gate_up(const MoeDecodeParams& p, const MdRou
     }
 }
 
-// TBM: most token blocks of one group (M <= 16: one)
-template <bool W8, int TBM>
+// XPM: most pieces of eight tokens of one group, by M: 1, 2 or 4.  The variant
+// taken is the one of the batch's busiest expert: fewer token registers leave
+// more for blocks of the expert in flight.
+template <bool W8, int XPM>
 __global__ __launch_bounds__(kMdThreads, 3) void k_moe_gate_up(MoeDecodeParams p, int shrinks) {
-    __shared__ uint4 smem[kMdWaves * md_stage_words(TBM)];
+    __shared__ uint4 smem[kMdWaves * md_stage_words(XPM)];
     __shared__ MdRoute rt;
     __shared__ float s_w[kMdMaxPairs];
-    __shared__ uint32_t s_S[kMdMaxS];
+    __shared__ __attribute__((aligned(16))) uint32_t s_S[kMdMaxS];
     __shared__ int16_t s_ad[LORA_DECODE_MAX_M];
     const int tid = threadIdx.x;
     const uint32_t tag = launch_tag(), want = tag ^ p.wc.poll_xor;
@@ -600,10 +657,13 @@ __global__ __launch_bounds__(kMdThreads, 3) void k_moe_gate_up(MoeDecodeParams p
     md_tables(p, rt);
     const int stride = (int)gridDim.x - p.M - shrinks;
     uint32_t* S = P * p.r <= kMdMaxS ? s_S : nullptr;
-    if (TBM == 1 || md_uni(rt.n_max) <= 16)
-        md_gate_up<W8, 1, W8 ? 2 : 3>(p, rt, s_w, s_ad, S, smem, blk, stride, want, &lost);
+    const int most = md_uni(rt.n_max);
+    if (XPM == 1 || most <= 8)
+        md_gate_up<W8, 1, W8 ? 2 : 4>(p, rt, s_w, s_ad, S, smem, blk, stride, want, &lost);
+    else if (XPM == 2 || most <= 16)
+        md_gate_up<W8, 2, W8 ? 2 : 3>(p, rt, s_w, s_ad, S, smem, blk, stride, want, &lost);
     else
-        md_gate_up<W8, TBM, W8 ? 1 : 2>(p, rt, s_w, s_ad, S, smem, blk, stride, want, &lost);
+        md_gate_up<W8, XPM, W8 ? 1 : 2>(p, rt, s_w, s_ad, S, smem, blk, stride, want, &lost);
     if (lost) atomicOr(p.err, LORA_DEVERR_WAIT);
 }
 
@@ -611,11 +671,12 @@ __global__ __launch_bounds__(kMdThreads, 3) void k_moe_gate_up(MoeDecodeParams p
 // A consumer: 32 output rows and one share of the blocks of all chosen
 // experts, the token's column the same for every expert (rows of tokens that
 // did not choose it read zeros), so the experts' sum needs no step of its own.
-template <bool W8, int TB, int U>
-__global__ __launch_bounds__(kMdThreads, TB > 2 ? 2 : 3) void k_moe_down(MoeDecodeParams p, int shrinks) {
-    using B = MdBlock<W8, TB>;
+template <bool W8, int XP, int U>
+__global__ __launch_bounds__(kMdThreads, XP > 4 ? 2 : 3) void k_moe_down(MoeDecodeParams p, int shrinks) {
+    using B = MdBlock<W8, XP>;
+    constexpr int TB = md_blocks_of(XP);
     constexpr int kBytes = W8 ? 1 : 2;
-    constexpr int kWords = md_stage_words(TB);
+    constexpr int kWords = md_stage_words(XP);
     __shared__ uint4 smem[kMdWaves * kWords];
     __shared__ MdRoute rt;
     const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -648,7 +709,7 @@ __global__ __launch_bounds__(kMdThreads, TB > 2 ? 2 : 3) void k_moe_down(MoeDeco
     const uint32_t ebytes = (uint32_t)p.H * (uint32_t)p.I * kBytes;
     const __amdgpu_buffer_rsrc_t rh = uniform_rsrc(p.h, (uint32_t)P * (uint32_t)p.I * 2u);
 
-    MdRows<TB> rows;
+    MdRows<XP> rows;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         rows.w[i] = (uint32_t)min(n0 + 8 * i + lane / 8, p.H - 1) * (uint32_t)p.I * kBytes + (lane % 8) * 16;
@@ -672,7 +733,7 @@ __global__ __launch_bounds__(kMdThreads, TB > 2 ? 2 : 3) void k_moe_down(MoeDeco
         const unsigned long long mask = md_uni(rt.mask[e]);
         const int base = md_uni((int)rt.base[e]);
 #pragma unroll
-        for (int i = 0; i < 2 * TB; ++i) {
+        for (int i = 0; i < XP; ++i) {
             const int m = 8 * i + lane / 8;
             rows.x[i] = kBufOff;
             if ((mask >> m) & 1ull) {
@@ -683,7 +744,7 @@ __global__ __launch_bounds__(kMdThreads, TB > 2 ? 2 : 3) void k_moe_down(MoeDeco
     };
     auto issue = [&](B& b) {
         const bool on = a_load * KB < t1 && kb_load < end_load;
-        md_issue<W8, TB>(b, uniform_rsrc(wbase, on ? ebytes : 0u), rh, rows, on ? kb_load : KB, p.I);
+        md_issue<W8, XP>(b, uniform_rsrc(wbase, on ? ebytes : 0u), rh, rows, on ? kb_load : KB, p.I);
         kb_load += kMdWaves;
         if (--left == 0) {
             ++a_load;
@@ -704,7 +765,7 @@ __global__ __launch_bounds__(kMdThreads, TB > 2 ? 2 : 3) void k_moe_down(MoeDeco
         const int nb = part_blocks(a);
         for (int b = 0; b < nb; b += U)
 #pragma unroll
-            for (int q = 0; q < U; ++q) md_consume<W8, TB>(blk[q], st, at, W8 ? part : acc, [&]() { issue(blk[q]); });
+            for (int q = 0; q < U; ++q) md_consume<W8, XP>(blk[q], st, at, W8 ? part : acc, [&]() { issue(blk[q]); });
         if constexpr (W8) {                                 // the expert's scales
             const float* s = p.s_d + (int64_t)md_uni((int)rt.active[a]) * p.H;
 #pragma unroll
@@ -720,22 +781,37 @@ __global__ __launch_bounds__(kMdThreads, TB > 2 ? 2 : 3) void k_moe_down(MoeDeco
     if (p.L > 0) {
         const int64_t per_l = (int64_t)(p.shared_outer ? 1 : p.E) * p.H * p.r;
         const int64_t r0 = min(n0 + lr, p.H - 1), r1 = min(n0 + 16 + lr, p.H - 1);
-        int deal = 0;                              // goes on from expert to expert
-        for (int i = split; i < na; i += p.splits) {
-            const int e = md_uni((int)rt.active[i]);
-            const unsigned long long mask = md_uni(rt.mask[e]);
-            const bool on = (mask >> lane) & 1ull;
-            const int f = on ? rt.list[rt.base[e] + __popcll(mask & ((1ull << lane) - 1ull))] : 0;
-            const int64_t eb = p.shared_outer ? 0 : (int64_t)e * p.H;
-            const int64_t row[2] = {eb + r0, eb + r1};
-            for (int d = 0;; ++d) {
-                const MdStep step = md_step(on ? ad0 : -1, p.r, d);
-                if (step.l < 0) break;
-                if (deal++ % kMdWaves != wave) continue;
-                uint4 bop[2];
-                md_step_load(p, p.B_d, per_l, row, step, bop);
-                md_step_add<TB>(p, nullptr, p.S_d, step, f, bop, want, &lost, acc);
+        // the wavefront's steps over the split's experts, dealt in turn; the B
+        // rows of one are in flight while the one before is added
+        int deal = 0, i = split, d = -1, pair = 0;
+        auto next = [&](uint4 (&b)[2]) {
+            for (; i < na; i += p.splits, d = -1) {
+                const int e = md_uni((int)rt.active[i]);
+                const unsigned long long mask = md_uni(rt.mask[e]);
+                const bool on = (mask >> lane) & 1ull;
+                for (++d;; ++d) {
+                    const MdStep s = md_step(on ? ad0 : -1, p.r, d);
+                    if (s.l < 0) break;
+                    if (deal++ % kMdWaves != wave) continue;
+                    pair = on ? rt.list[rt.base[e] + __popcll(mask & ((1ull << lane) - 1ull))] : 0;
+                    const int64_t eb = p.shared_outer ? 0 : (int64_t)e * p.H;
+                    const int64_t row[2] = {eb + r0, eb + r1};
+                    md_step_load(p, p.B_d, per_l, row, s, b);
+                    return s;
+                }
             }
+            return MdStep{-1, 0, 0ull};
+        };
+        uint4 b0[2], b1[2];
+        MdStep s0 = next(b0);
+        while (s0.l >= 0) {
+            const int f0 = pair;
+            const MdStep s1 = next(b1);
+            md_step_add<TB>(p, nullptr, p.S_d, s0, f0, b0, want, &lost, acc);
+            if (s1.l < 0) break;
+            const int f1 = pair;
+            s0 = next(b0);
+            md_step_add<TB>(p, nullptr, p.S_d, s1, f1, b1, want, &lost, acc);
         }
     }
     float4* red = reinterpret_cast<float4*>(st);
@@ -760,11 +836,18 @@ __global__ __launch_bounds__(kMdThreads, TB > 2 ? 2 : 3) void k_moe_down(MoeDeco
 #pragma unroll
             for (int q = 0; q < 4; ++q) slot_put(d + q, v[q], tag);
         } else {
-            // the last split of a tile adds the others, in split order
-            for (int s = 0; s < p.splits - 1; ++s) {
-                const slot_t* d = p.join + ((int64_t)s * p.M + m) * p.H + n;
+            // the last split of a tile adds the others, in split order, two at a time
+            const slot_t* d = p.join + (int64_t)m * p.H + n;
+            const int64_t per = (int64_t)p.M * p.H;
+            for (int s = 0; s < p.splits - 1; s += 2) {
+                const bool two = s + 1 < p.splits - 1;
+                float f[8];
+                slot_wait4x2(d + s * per, d + (two ? s + 1 : s) * per, want, p.wc.max_spin, &lost, f);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] += __uint_as_float(slot_wait(d + q, want, p.wc.max_spin, &lost));
+                for (int q = 0; q < 4; ++q) v[q] += f[q];
+                if (two)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[q] += f[4 + q];
             }
             *reinterpret_cast<uint2*>(p.out + (int64_t)m * p.ldo + n) =
                 make_uint2(f32_to_bf16(v[0]) | (f32_to_bf16(v[1]) << 16), f32_to_bf16(v[2]) | (f32_to_bf16(v[3]) << 16));
@@ -773,10 +856,11 @@ __global__ __launch_bounds__(kMdThreads, TB > 2 ? 2 : 3) void k_moe_down(MoeDeco
     if (lost) atomicOr(p.err, LORA_DEVERR_WAIT);
 }
 
-int moe_decode_splits(int H) {
-    // as many as keep every consumer resident at once
+int moe_decode_splits(int H, int M) {
+    // as many as keep every consumer resident at once (with more than 32
+    // tokens a consumer has the registers of two workgroups a compute unit)
     const int tiles = (H + 31) / 32;
-    return max(1, min(kMdResident / tiles, 16));
+    return max(1, min((M > 32 ? kMdResident / 3 * 2 : kMdResident) / tiles, 16));
 }
 
 template <bool W8>
@@ -786,13 +870,15 @@ hipError_t launch_moe_decode_t(const MoeDecodeParams& p, hipStream_t st) {
     const int units = min(min(p.E, P) + P / 33, kMdMaxGroups) * ((p.I + 15) / 16);
     const dim3 g1((unsigned)(p.M + shrinks + min(units, kMdResident))), g2((unsigned)(shrinks + (p.H + 31) / 32 * p.splits));
     const dim3 t(kMdThreads);
-    if (p.M <= 16) hipLaunchKernelGGL((k_moe_gate_up<W8, 1>), g1, t, 0, st, p, shrinks);
-    else hipLaunchKernelGGL((k_moe_gate_up<W8, 2>), g1, t, 0, st, p, shrinks);
+    if (p.M <= 8) hipLaunchKernelGGL((k_moe_gate_up<W8, 1>), g1, t, 0, st, p, shrinks);
+    else if (p.M <= 16) hipLaunchKernelGGL((k_moe_gate_up<W8, 2>), g1, t, 0, st, p, shrinks);
+    else hipLaunchKernelGGL((k_moe_gate_up<W8, 4>), g1, t, 0, st, p, shrinks);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (p.M <= 16) hipLaunchKernelGGL((k_moe_down<W8, 1, W8 ? 2 : 3>), g2, t, 0, st, p, shrinks);
-    else if (p.M <= 32) hipLaunchKernelGGL((k_moe_down<W8, 2, W8 ? 1 : 2>), g2, t, 0, st, p, shrinks);
-    else hipLaunchKernelGGL((k_moe_down<W8, 4, W8 ? 1 : 2>), g2, t, 0, st, p, shrinks);
+    if (p.M <= 8) hipLaunchKernelGGL((k_moe_down<W8, 1, W8 ? 3 : 4>), g2, t, 0, st, p, shrinks);
+    else if (p.M <= 16) hipLaunchKernelGGL((k_moe_down<W8, 2, W8 ? 2 : 3>), g2, t, 0, st, p, shrinks);
+    else if (p.M <= 32) hipLaunchKernelGGL((k_moe_down<W8, 4, W8 ? 1 : 2>), g2, t, 0, st, p, shrinks);
+    else hipLaunchKernelGGL((k_moe_down<W8, 8, W8 ? 1 : 2>), g2, t, 0, st, p, shrinks);
     return hipGetLastError();
 }
 

@@ -619,7 +619,7 @@ typedef struct lora_moe_experts {
 } lora_moe_experts_t;
 
 /*
- * Bytes of device workspace of lora_moe_decode for M tokens (0: invalid
+ * Bytes of device workspace of lora_moe_decode for up to M tokens (0: invalid
  * arguments): zero it once (lora_workspace_init) before its first use, order
  * the calls that share it on one stream.  w may be NULL.
  */
