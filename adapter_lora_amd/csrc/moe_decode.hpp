@@ -251,13 +251,12 @@ static_assert(kMdWaves * 4 == 16, "a shrink workgroup takes 16 rows");
 // ---------------------------------------------------------------- routing tables in LDS
 struct MdRoute {
     unsigned long long mask[kMdMaxE];      // tokens of each expert
-    int16_t active[kMdMaxE];               // experts with tokens, ascending
     int16_t group[kMdMaxGroups];           // groups of up to 32 of an expert's tokens: expert, and
                                            // 256 times the group's number within it
     int16_t base[kMdMaxE];                 // an expert's first place in `list`
     int16_t exp_[kMdMaxPairs];             // expert of a pair, -1: none
     int16_t list[kMdMaxPairs];             // pairs by expert, then token
-    int n_active, n_groups, n_max;         // experts with tokens; groups; most tokens of one expert
+    int n_groups, n_max;                   // groups; most tokens of one expert
 };
 
 // After exp_ is filled: the rest.  Ends with a barrier.
@@ -270,15 +269,12 @@ __device__ __forceinline__ void md_tables(const MoeDecodeParams& p, MdRoute& r) 
         if (r.exp_[f] >= 0) atomicOr(&r.mask[r.exp_[f]], 1ull << (f / p.topk));
     __syncthreads();
     if (tid < kWave) {
-        int n = 0, pairs = 0, most = 0, groups = 0;
+        int pairs = 0, most = 0, groups = 0;
         for (int e0 = 0; e0 < p.E; e0 += kWave) {
             const int c = e0 + lane < p.E ? __popcll(r.mask[e0 + lane]) : 0;
             const unsigned long long b = __ballot(c > 0);
             const int incl = wave_incl_scan(c);
-            if (c > 0) {
-                r.active[n + __popcll(b & ((1ull << lane) - 1ull))] = (int16_t)(e0 + lane);
-                r.base[e0 + lane] = (int16_t)(pairs + incl - c);
-            }
+            if (c > 0) r.base[e0 + lane] = (int16_t)(pairs + incl - c);
             // at most 64 tokens: one or two groups
             const unsigned long long two = __ballot(c > 32);
             const unsigned long long lt = (1ull << lane) - 1ull;
@@ -286,13 +282,12 @@ __device__ __forceinline__ void md_tables(const MoeDecodeParams& p, MdRoute& r) 
             if (c > 0) r.group[g] = (int16_t)(e0 + lane);
             if (c > 32) r.group[g + 1] = (int16_t)(e0 + lane + kMdMaxE);
             groups += __popcll(b) + __popcll(two);
-            n += __popcll(b);
             pairs += __builtin_amdgcn_readlane(incl, kWave - 1);
             most = max(most, c);
         }
 #pragma unroll
         for (int o = kWave / 2; o > 0; o >>= 1) most = max(most, __shfl_xor(most, o, kWave));
-        if (lane == 0) r.n_active = n, r.n_groups = groups, r.n_max = most;
+        if (lane == 0) r.n_groups = groups, r.n_max = most;
     }
     __syncthreads();
     for (int f = tid; f < P; f += kMdThreads) {
@@ -446,7 +441,7 @@ __device__ __forceinline__ void md_step_add(const MoeDecodeParams& p, const uint
 #pragma unroll
     for (int t = 0; t < TB; ++t) {
         if (((s.cols >> (16 * t)) & 0xffffull) == 0ull) continue;
-        const bool on = ((s.cols >> (16 * t + lr)) & 1ull) && j < p.r;
+        const bool col = (s.cols >> (16 * t + lr)) & 1ull, on = col && j < p.r;
         const int at = __shfl(pair, 16 * t + lr, kWave) * p.r + min(j, p.r - 8);
         uint32_t w[8];
         if (sS) {
@@ -463,10 +458,13 @@ __device__ __forceinline__ void md_step_add(const MoeDecodeParams& p, const uint
         h.y = (w[2] >> 16) | (w[3] & 0xffff0000u); lo.y = (w[2] & 0xffffu) | (w[3] << 16);
         h.z = (w[4] >> 16) | (w[5] & 0xffff0000u); lo.z = (w[4] & 0xffffu) | (w[5] << 16);
         h.w = (w[6] >> 16) | (w[7] & 0xffff0000u); lo.w = (w[6] & 0xffffu) | (w[7] << 16);
+        // other columns keep their sums: their zeros times an adapter's
+        // infinities would not be zero
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-            acc[n][t] = mfma_bf16(b[n], h, acc[n][t]);
-            acc[n][t] = mfma_bf16(b[n], lo, acc[n][t]);
+            const f32x4_t v = mfma_bf16(b[n], lo, mfma_bf16(b[n], h, acc[n][t]));
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[n][t][q] = col ? v[q] : acc[n][t][q];
         }
     }
 }
@@ -668,19 +666,183 @@ __global__ __launch_bounds__(kMdThreads, 3) void k_moe_gate_up(MoeDecodeParams p
 }
 
 // ---------------------------------------------------------------- second launch
-// A consumer: 32 output rows and one share of the blocks of all chosen
-// experts, the token's column the same for every expert (rows of tokens that
-// did not choose it read zeros), so the experts' sum needs no step of its own.
+// The consumers of the second launch: 32 output rows and one share of the blocks
+// of all groups (up to 32 tokens of an expert).  A group's sums have its own
+// tokens as columns; they are added to the workgroup's output, one fp32 value a
+// row and token, which each wavefront holds for itself in LDS (`out`).  So an
+// expert's values, infinities among them, reach the tokens that chose it and no
+// others, and columns do not grow with the batch.
+constexpr int kMdOut = 36;                         // floats of a token's 32 rows, spread over banks
+
 template <bool W8, int XP, int U>
-__global__ __launch_bounds__(kMdThreads, XP > 4 ? 2 : 3) void k_moe_down(MoeDecodeParams p, int shrinks) {
+__device__ __forceinline__ void md_down(const MoeDecodeParams& p, const MdRoute& rt, const int16_t* s_ad, float* out,
+                                        uint4* st, int n0, int split, uint32_t want, bool* lost) {
     using B = MdBlock<W8, XP>;
     constexpr int TB = md_blocks_of(XP);
     constexpr int kBytes = W8 ? 1 : 2;
-    constexpr int kWords = md_stage_words(XP);
-    __shared__ uint4 smem[kMdWaves * kWords];
-    __shared__ MdRoute rt;
-    const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     const int lr = lane % 16, lq = lane / 16;
+    const StageAt at;
+    const int ng = md_uni(rt.n_groups);
+    const int KB = (p.I + B::KV - 1) / B::KV;               // blocks of one group
+    const int total = ng * KB;
+    const int t0 = (int)((int64_t)total * split / p.splits), t1 = (int)((int64_t)total * (split + 1) / p.splits);
+    const uint32_t ebytes = (uint32_t)p.H * (uint32_t)p.I * kBytes;
+    const __amdgpu_buffer_rsrc_t rh = uniform_rsrc(p.h, (uint32_t)(p.M * p.topk) * (uint32_t)p.I * 2u);
+    struct Group {
+        int e, base, ne;
+    };
+    auto group = [&](int g) {
+        const int v = md_uni((int)rt.group[g]), e = v % kMdMaxE, skip = v / kMdMaxE * 32;
+        return Group{e, md_uni((int)rt.base[e]) + skip, min((int)__popcll(md_uni(rt.mask[e])) - skip, 32)};
+    };
+
+    MdRows<XP> rows;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        rows.w[i] = (uint32_t)min(n0 + 8 * i + lane / 8, p.H - 1) * (uint32_t)p.I * kBytes + (lane % 8) * 16;
+    const char* wbase = nullptr;
+    int g_load = t0 / KB, kb_load = 0;                      // group and block of the next load
+    // a part: one group's blocks of this share, [beg, end), every kMdWaves-th of
+    // them this wavefront's, their number rounded up to U
+    auto part_end = [&](int g) { return min(KB, t1 - g * KB); };
+    auto part_beg = [&](int g) { return max(0, t0 - g * KB); };
+    auto part_blocks = [&](int g) {
+        return ((part_end(g) - part_beg(g) + kMdWaves - 1) / kMdWaves + U - 1) / U * U;
+    };
+    int left = 0, end_load = 0;
+    auto set_rows = [&]() {
+        if (g_load * KB >= t1) return;
+        const Group g = group(g_load);
+        wbase = static_cast<const char*>(p.W_d) + (int64_t)g.e * p.H * p.I * kBytes;
+        left = part_blocks(g_load);
+        end_load = part_end(g_load);
+        kb_load = part_beg(g_load) + wave;
+#pragma unroll
+        for (int i = 0; i < XP; ++i) {
+            const int t = 8 * i + lane / 8;
+            rows.x[i] = t < g.ne ? (uint32_t)rt.list[g.base + t] * (uint32_t)p.I * 2u + (lane % 8) * 16 : kBufOff;
+        }
+    };
+    auto issue = [&](B& b) {
+        const bool on = g_load * KB < t1 && kb_load < end_load;
+        md_issue<W8, XP>(b, uniform_rsrc(wbase, on ? ebytes : 0u), rh, rows, on ? kb_load : KB, p.I);
+        kb_load += kMdWaves;
+        if (--left == 0) {
+            ++g_load;
+            set_rows();
+        }
+    };
+    set_rows();
+    B blk[U];
+#pragma unroll
+    for (int q = 0; q < U; ++q) issue(blk[q]);
+
+    f32x4_t part[2][TB];
+    auto clear = [&]() {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int t = 0; t < TB; ++t) part[n][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    };
+    // the group's sums, times the rows' scales, to its tokens' rows
+    auto add = [&](const Group& g, const float (&s)[2][4]) {
+        stage_order();
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+            if (16 * t + lr >= g.ne) continue;
+            float* d = out + (int)rt.list[g.base + 16 * t + lr] / p.topk * kMdOut + lq * 4;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                float4* o = reinterpret_cast<float4*>(d + 16 * n);
+                float4 v = *o;
+                v.x += part[n][t][0] * s[n][0];
+                v.y += part[n][t][1] * s[n][1];
+                v.z += part[n][t][2] * s[n][2];
+                v.w += part[n][t][3] * s[n][3];
+                *o = v;
+            }
+        }
+    };
+    float one[2][4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) one[n][q] = 1.f;
+    for (int a = t0 / KB; a * KB < t1; ++a) {
+        const Group g = group(a);
+        const int nb = part_blocks(a);
+        float s[2][4];
+        if constexpr (W8) {                                 // loaded ahead of the part's stream
+            const float* sc = p.s_d + (int64_t)g.e * p.H;
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) s[n][q] = sc[min(n0 + 16 * n + lq * 4 + q, p.H - 1)];
+        }
+        clear();
+        for (int b = 0; b < nb; b += U)
+#pragma unroll
+            for (int q = 0; q < U; ++q) md_consume<W8, XP>(blk[q], st, at, part, [&]() { issue(blk[q]); });
+        add(g, W8 ? s : one);
+    }
+    if (p.L > 0) {
+        const int64_t per_l = (int64_t)(p.shared_outer ? 1 : p.E) * p.H * p.r;
+        const int64_t r0 = min(n0 + lr, p.H - 1), r1 = min(n0 + 16 + lr, p.H - 1);
+        // the wavefront's steps over the split's groups, dealt in turn; the B
+        // rows of one are in flight while the one before is added
+        struct Task {
+            MdStep s;
+            int pair;
+            Group g;
+        };
+        int deal = 0, i = split, d = -1;
+        auto next = [&](uint4 (&b)[2]) {
+            for (; i < ng; i += p.splits, d = -1) {
+                const Group g = group(i);
+                const int f = lane < g.ne ? rt.list[g.base + lane] : 0;
+                const int ad = lane < g.ne ? s_ad[f / p.topk] : -1;
+                for (++d;; ++d) {
+                    const MdStep s = md_step(ad, p.r, d);
+                    if (s.l < 0) break;
+                    if (deal++ % kMdWaves != wave) continue;
+                    const int64_t eb = p.shared_outer ? 0 : (int64_t)g.e * p.H;
+                    const int64_t row[2] = {eb + r0, eb + r1};
+                    md_step_load(p, p.B_d, per_l, row, s, b);
+                    return Task{s, f, g};
+                }
+            }
+            return Task{MdStep{-1, 0, 0ull}, 0, Group{0, 0, 0}};
+        };
+        auto delta = [&](const Task& k, const uint4 (&b)[2]) {
+            clear();
+            md_step_add<TB>(p, nullptr, p.S_d, k.s, k.pair, b, want, lost, part);
+            add(k.g, one);
+        };
+        uint4 b0[2], b1[2];
+        Task k0 = next(b0);
+        while (k0.s.l >= 0) {
+            const Task k1 = next(b1);
+            delta(k0, b0);
+            if (k1.s.l < 0) break;
+            k0 = next(b0);
+            delta(k1, b1);
+        }
+    }
+}
+
+// MT: most tokens.  With more than 32 the outputs of a workgroup leave room for
+// two of them in a compute unit's LDS, and those have registers for more blocks
+// in flight.  XPM, and the choice by the busiest expert: as in the first launch.
+template <bool W8, int XPM, int MT>
+__global__ __launch_bounds__(kMdThreads, MT > 32 ? 2 : 3) void k_moe_down(MoeDecodeParams p, int shrinks) {
+    constexpr int kWords = md_stage_words(XPM);
+    constexpr int kMore = MT > 32 ? 1 : 0;
+    __shared__ uint4 smem[kMdWaves * kWords];
+    __shared__ __attribute__((aligned(16))) float s_out[kMdWaves][MT * kMdOut];
+    __shared__ MdRoute rt;
+    __shared__ int16_t s_ad[LORA_DECODE_MAX_M];
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const uint32_t tag = launch_tag(), want = tag ^ p.wc.poll_xor;
     const int P = p.M * p.topk;
     bool lost = false;
@@ -697,138 +859,27 @@ __global__ __launch_bounds__(kMdThreads, XP > 4 ? 2 : 3) void k_moe_down(MoeDeco
     const int tiles = (p.H + 31) / 32;
     const int split = id / tiles, n0 = (id % tiles) * 32;
     for (int f = tid; f < P; f += kMdThreads) rt.exp_[f] = (int16_t)p.route_ids[f];
+    if (tid < p.M) s_ad[tid] = (int16_t)md_adapter(p, tid);
+    for (int i = tid % kWave; i < p.M * kMdOut / 4; i += kWave)
+        reinterpret_cast<float4*>(s_out[wave])[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     md_tables(p, rt);
-    const int na = md_uni(rt.n_active);
-    const int ad0 = lane < p.M ? md_adapter(p, lane) : -1;
-
+    const int most = md_uni(rt.n_max);
     uint4* st = smem + wave * kWords;
-    const StageAt at;
-    const int KB = (p.I + B::KV - 1) / B::KV;               // blocks of one expert
-    const int total = na * KB;
-    const int t0 = (int)((int64_t)total * split / p.splits), t1 = (int)((int64_t)total * (split + 1) / p.splits);
-    const uint32_t ebytes = (uint32_t)p.H * (uint32_t)p.I * kBytes;
-    const __amdgpu_buffer_rsrc_t rh = uniform_rsrc(p.h, (uint32_t)P * (uint32_t)p.I * 2u);
-
-    MdRows<XP> rows;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        rows.w[i] = (uint32_t)min(n0 + 8 * i + lane / 8, p.H - 1) * (uint32_t)p.I * kBytes + (lane % 8) * 16;
-    const char* wbase = nullptr;
-    int a_load = t0 / KB, kb_load = t0 % KB + wave;         // active expert and block of the next load
-    // a part: one expert's blocks of this share, [kb0, kb1), every kMdWaves-th of
-    // them this wavefront's, their number rounded up to U
-    auto part_end = [&](int a) { return min(KB, t1 - a * KB); };
-    auto part_beg = [&](int a) { return max(0, t0 - a * KB); };
-    auto part_blocks = [&](int a) {
-        return ((part_end(a) - part_beg(a) + kMdWaves - 1) / kMdWaves + U - 1) / U * U;
-    };
-    int left = 0, end_load = 0;
-    auto set_rows = [&]() {
-        if (a_load * KB >= t1) return;
-        const int e = md_uni((int)rt.active[a_load]);
-        wbase = static_cast<const char*>(p.W_d) + (int64_t)e * p.H * p.I * kBytes;
-        left = part_blocks(a_load);
-        end_load = part_end(a_load);
-        kb_load = part_beg(a_load) + wave;
-        const unsigned long long mask = md_uni(rt.mask[e]);
-        const int base = md_uni((int)rt.base[e]);
-#pragma unroll
-        for (int i = 0; i < XP; ++i) {
-            const int m = 8 * i + lane / 8;
-            rows.x[i] = kBufOff;
-            if ((mask >> m) & 1ull) {
-                const int f = rt.list[base + __popcll(mask & ((1ull << m) - 1ull))];
-                rows.x[i] = (uint32_t)f * (uint32_t)p.I * 2u + (lane % 8) * 16;
-            }
-        }
-    };
-    auto issue = [&](B& b) {
-        const bool on = a_load * KB < t1 && kb_load < end_load;
-        md_issue<W8, XP>(b, uniform_rsrc(wbase, on ? ebytes : 0u), rh, rows, on ? kb_load : KB, p.I);
-        kb_load += kMdWaves;
-        if (--left == 0) {
-            ++a_load;
-            set_rows();
-        }
-    };
-    set_rows();
-    B blk[U];
-#pragma unroll
-    for (int q = 0; q < U; ++q) issue(blk[q]);
-
-    f32x4_t acc[2][TB], part[2][TB];
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int t = 0; t < TB; ++t) acc[n][t] = f32x4_t{0.f, 0.f, 0.f, 0.f}, part[n][t] = acc[n][t];
-    for (int a = t0 / KB; a * KB < t1; ++a) {
-        const int nb = part_blocks(a);
-        for (int b = 0; b < nb; b += U)
-#pragma unroll
-            for (int q = 0; q < U; ++q) md_consume<W8, XP>(blk[q], st, at, W8 ? part : acc, [&]() { issue(blk[q]); });
-        if constexpr (W8) {                                 // the expert's scales
-            const float* s = p.s_d + (int64_t)md_uni((int)rt.active[a]) * p.H;
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float v = s[min(n0 + 16 * n + lq * 4 + q, p.H - 1)];
-#pragma unroll
-                    for (int t = 0; t < TB; ++t) acc[n][t][q] += part[n][t][q] * v, part[n][t][q] = 0.f;
-                }
-        }
-    }
-    if (p.L > 0) {
-        const int64_t per_l = (int64_t)(p.shared_outer ? 1 : p.E) * p.H * p.r;
-        const int64_t r0 = min(n0 + lr, p.H - 1), r1 = min(n0 + 16 + lr, p.H - 1);
-        // the wavefront's steps over the split's experts, dealt in turn; the B
-        // rows of one are in flight while the one before is added
-        int deal = 0, i = split, d = -1, pair = 0;
-        auto next = [&](uint4 (&b)[2]) {
-            for (; i < na; i += p.splits, d = -1) {
-                const int e = md_uni((int)rt.active[i]);
-                const unsigned long long mask = md_uni(rt.mask[e]);
-                const bool on = (mask >> lane) & 1ull;
-                for (++d;; ++d) {
-                    const MdStep s = md_step(on ? ad0 : -1, p.r, d);
-                    if (s.l < 0) break;
-                    if (deal++ % kMdWaves != wave) continue;
-                    pair = on ? rt.list[rt.base[e] + __popcll(mask & ((1ull << lane) - 1ull))] : 0;
-                    const int64_t eb = p.shared_outer ? 0 : (int64_t)e * p.H;
-                    const int64_t row[2] = {eb + r0, eb + r1};
-                    md_step_load(p, p.B_d, per_l, row, s, b);
-                    return s;
-                }
-            }
-            return MdStep{-1, 0, 0ull};
-        };
-        uint4 b0[2], b1[2];
-        MdStep s0 = next(b0);
-        while (s0.l >= 0) {
-            const int f0 = pair;
-            const MdStep s1 = next(b1);
-            md_step_add<TB>(p, nullptr, p.S_d, s0, f0, b0, want, &lost, acc);
-            if (s1.l < 0) break;
-            const int f1 = pair;
-            s0 = next(b0);
-            md_step_add<TB>(p, nullptr, p.S_d, s1, f1, b1, want, &lost, acc);
-        }
-    }
-    float4* red = reinterpret_cast<float4*>(st);
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int t = 0; t < TB; ++t)
-            red[(n * TB + t) * kWave + lane] = make_float4(acc[n][t][0], acc[n][t][1], acc[n][t][2], acc[n][t][3]);
+    if (XPM == 1 || most <= 8)
+        md_down<W8, 1, (W8 ? 3 : 4) + kMore>(p, rt, s_ad, s_out[wave], st, n0, split, want, &lost);
+    else if (XPM == 2 || most <= 16)
+        md_down<W8, 2, (W8 ? 2 : 3) + kMore>(p, rt, s_ad, s_out[wave], st, n0, split, want, &lost);
+    else
+        md_down<W8, 4, (W8 ? 1 : 2) + kMore>(p, rt, s_ad, s_out[wave], st, n0, split, want, &lost);
     __syncthreads();
-    // part i = n * TB + t: rows 16 n of token block t
-    for (int i = wave; i < 2 * TB; i += kMdWaves) {
-        const int m = (i % TB) * 16 + lr, n = n0 + (i / TB) * 16 + lq * 4;
-        if (m >= p.M || n >= p.H) continue;
+    // the wavefronts' sums in a fixed order, then the splits'
+    for (int i = tid; i < p.M * 8; i += kMdThreads) {
+        const int m = i / 8, c = i % 8 * 4, n = n0 + c;
+        if (n >= p.H) continue;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < kMdWaves; ++w) {
-            const float4 a = reinterpret_cast<const float4*>(smem + w * kWords)[i * kWave + lane];
+            const float4 a = *reinterpret_cast<const float4*>(s_out[w] + m * kMdOut + c);
             v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
         }
         if (split < p.splits - 1) {
@@ -875,10 +926,10 @@ hipError_t launch_moe_decode_t(const MoeDecodeParams& p, hipStream_t st) {
     else hipLaunchKernelGGL((k_moe_gate_up<W8, 4>), g1, t, 0, st, p, shrinks);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (p.M <= 8) hipLaunchKernelGGL((k_moe_down<W8, 1, W8 ? 3 : 4>), g2, t, 0, st, p, shrinks);
-    else if (p.M <= 16) hipLaunchKernelGGL((k_moe_down<W8, 2, W8 ? 2 : 3>), g2, t, 0, st, p, shrinks);
-    else if (p.M <= 32) hipLaunchKernelGGL((k_moe_down<W8, 4, W8 ? 1 : 2>), g2, t, 0, st, p, shrinks);
-    else hipLaunchKernelGGL((k_moe_down<W8, 8, W8 ? 1 : 2>), g2, t, 0, st, p, shrinks);
+    if (p.M <= 8) hipLaunchKernelGGL((k_moe_down<W8, 1, 32>), g2, t, 0, st, p, shrinks);
+    else if (p.M <= 16) hipLaunchKernelGGL((k_moe_down<W8, 2, 32>), g2, t, 0, st, p, shrinks);
+    else if (p.M <= 32) hipLaunchKernelGGL((k_moe_down<W8, 4, 32>), g2, t, 0, st, p, shrinks);
+    else hipLaunchKernelGGL((k_moe_down<W8, 4, LORA_DECODE_MAX_M>), g2, t, 0, st, p, shrinks);
     return hipGetLastError();
 }
 
