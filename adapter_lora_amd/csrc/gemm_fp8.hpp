@@ -405,7 +405,8 @@ __global__ __launch_bounds__(kGThreads, G::Waves) void k_gemm_fp8(GemmFp8Params 
             for (int rb = 0; rb < kGRB; ++rb) {
                 if (rb * 32 + 32 <= b0 || rb * 32 >= b1) continue;
                 const int row = rb * 32 + lr;
-                const uint32_t m = opaque_mask(row >= b0 && row < b1);
+                const bool mine = row >= b0 && row < b1, whole = b0 <= rb * 32 && rb * 32 + 32 <= b1;
+                const uint32_t m = opaque_mask(mine);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     if (t * 16 >= rp) continue;
@@ -414,8 +415,15 @@ __global__ __launch_bounds__(kGThreads, G::Waves) void k_gemm_fp8(GemmFp8Params 
                     const uint4 l = and4(*reinterpret_cast<const uint4*>(sLo + o), m);
 #pragma unroll
                     for (int cb = 0; cb < kGCB; ++cb) {
-                        acc[rb][cb] = mfma32_bf16(bop[cb][t], h, acc[rb][cb]);
-                        acc[rb][cb] = mfma32_bf16(bop[cb][t], l, acc[rb][cb]);
+                        const f32x16_t v = mfma32_bf16(bop[cb][t], l, mfma32_bf16(bop[cb][t], h, acc[rb][cb]));
+                        if (whole) {
+                            acc[rb][cb] = v;
+                        } else {
+                            // other tokens keep their sums: their zeros times an
+                            // adapter's infinities would not be zero
+#pragma unroll
+                            for (int q = 0; q < 16; ++q) acc[rb][cb][q] = mine ? v[q] : acc[rb][cb][q];
+                        }
                     }
                 }
             }

@@ -398,9 +398,9 @@ __global__ __launch_bounds__(kFpThreads, TB * NR == 8 ? 2 : 4) void k_linear_fp8
                 for (; on; ++spin) {
                     slot_t v[8];
                     bool full = true;
-    #pragma unroll
+#pragma unroll
                     for (int q = 0; q < 4; ++q) v[q] = slot_load(src + q), v[4 + q] = slot_load(src + second + q);
-    #pragma unroll
+#pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         full &= slot_full(v[q], want) && slot_full(v[4 + q], want);
                         f[q] = __uint_as_float((uint32_t)v[q]);
@@ -439,13 +439,17 @@ __global__ __launch_bounds__(kFpThreads, TB * NR == 8 ? 2 : 4) void k_linear_fp8
                 for (int t = 0; t < TB; ++t) {
                     if (t * 16 >= p1 || t * 16 + 16 <= p0) continue;
                     const int pos = t * 16 + lr;
-                    const uint32_t mp = opaque_mask(pos >= p0 && pos < p1 && jj < rp);
+                    const bool mine = pos >= p0 && pos < p1;
+                    const uint32_t mp = opaque_mask(mine && jj < rp);
                     const uint4 h = and4(*reinterpret_cast<const uint4*>(sHi + pos * kFpSLD + jj), mp);
                     const uint4 l = and4(*reinterpret_cast<const uint4*>(sLo + pos * kFpSLD + jj), mp);
 #pragma unroll
                     for (int r = 0; r < NR; ++r) {
-                        acc[r][t] = mfma_bf16(b[r], h, acc[r][t]);
-                        acc[r][t] = mfma_bf16(b[r], l, acc[r][t]);
+                        // other tokens keep their sums: their zeros times an
+                        // adapter's infinities would not be zero
+                        const f32x4_t v = mfma_bf16(b[r], l, mfma_bf16(b[r], h, acc[r][t]));
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) acc[r][t][q] = mine ? v[q] : acc[r][t][q];
                     }
                 }
             }
