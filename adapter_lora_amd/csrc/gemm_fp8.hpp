@@ -70,6 +70,25 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_fp8_t));
 }
 
+// Running maximum of bf16 values without their signs, two by two: an infinity or
+// NaN is 0x7f80 or more.
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u16x2_t max_magnitude(const uint4& v, u16x2_t m) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, w[i] & 0x7fff7fffu));
+    return m;
+}
+
+// bf16 values, infinities and NaN as zeros
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t w) {
+    return ((w & 0x7f80u) == 0x7f80u ? 0u : w & 0xffffu) | ((w & 0x7f800000u) == 0x7f800000u ? 0u : w & 0xffff0000u);
+}
+__device__ __forceinline__ uint4 finite_or_zero(const uint4& v) {
+    return make_uint4(finite_or_zero(v.x), finite_or_zero(v.y), finite_or_zero(v.z), finite_or_zero(v.w));
+}
+
 struct GemmFp8Params {
     LinearArgs a;
     const uint8_t* x;
@@ -384,6 +403,7 @@ __global__ __launch_bounds__(kGThreads, G::Waves) void k_gemm_fp8(GemmFp8Params 
     // ---- LoRA epilogue: the unit's S values as a bf16 hi / lo pair in LDS,
     // then one pass per segment that meets the unit's rows, its S rows picked
     // by a row mask on the operand
+    bool special = false;        // B rows of this wave's columns with an infinity or NaN
     if (lora) {
         uint16_t* sHi = reinterpret_cast<uint16_t*>(smem);   // the ring is free now
         uint16_t* sLo = sHi + kGM * kSLD;
@@ -399,14 +419,32 @@ __global__ __launch_bounds__(kGThreads, G::Waves) void k_gemm_fp8(GemmFp8Params 
             }
         }
         __syncthreads();
-        auto add = [&](int beg, int end, int rp, const uint4 (&bop)[kGCB][4]) {
+        // A block of 32 rows that a segment covers in part has zeros for its
+        // other tokens, and zeros times an infinity are not zero: infinities and
+        // NaN of B stay out of this product and join the segment's own tokens
+        // at the end.  (A select for every partly covered sum, which the AGPRs
+        // that hold them cannot take, cost 93 -> 105 us at 512 x 28672.)
+        auto add = [&](int beg, int end, int rp, uint4 (&bop)[kGCB][4]) {
             const int b0 = max(beg - p0, 0), b1 = min(end - p0, rows);
+            u16x2_t top = {0, 0};
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                if (t * 16 >= rp) continue;
+#pragma unroll
+                for (int cb = 0; cb < kGCB; ++cb) top = max_magnitude(bop[cb][t], top);
+            }
+            if (__ballot(top[0] >= 0x7f80 || top[1] >= 0x7f80) != 0ull) {
+                special = true;
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int cb = 0; cb < kGCB; ++cb) bop[cb][t] = finite_or_zero(bop[cb][t]);
+            }
 #pragma unroll
             for (int rb = 0; rb < kGRB; ++rb) {
                 if (rb * 32 + 32 <= b0 || rb * 32 >= b1) continue;
                 const int row = rb * 32 + lr;
-                const bool mine = row >= b0 && row < b1, whole = b0 <= rb * 32 && rb * 32 + 32 <= b1;
-                const uint32_t m = opaque_mask(mine);
+                const uint32_t m = opaque_mask(row >= b0 && row < b1);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     if (t * 16 >= rp) continue;
@@ -415,15 +453,8 @@ __global__ __launch_bounds__(kGThreads, G::Waves) void k_gemm_fp8(GemmFp8Params 
                     const uint4 l = and4(*reinterpret_cast<const uint4*>(sLo + o), m);
 #pragma unroll
                     for (int cb = 0; cb < kGCB; ++cb) {
-                        const f32x16_t v = mfma32_bf16(bop[cb][t], l, mfma32_bf16(bop[cb][t], h, acc[rb][cb]));
-                        if (whole) {
-                            acc[rb][cb] = v;
-                        } else {
-                            // other tokens keep their sums: their zeros times an
-                            // adapter's infinities would not be zero
-#pragma unroll
-                            for (int q = 0; q < 16; ++q) acc[rb][cb][q] = mine ? v[q] : acc[rb][cb][q];
-                        }
+                        acc[rb][cb] = mfma32_bf16(bop[cb][t], h, acc[rb][cb]);
+                        acc[rb][cb] = mfma32_bf16(bop[cb][t], l, acc[rb][cb]);
                     }
                 }
             }
@@ -458,6 +489,25 @@ __global__ __launch_bounds__(kGThreads, G::Waves) void k_gemm_fp8(GemmFp8Params 
                     make_uint2(pack_bf16(acc[rb][cb][4 * g], acc[rb][cb][4 * g + 1]),
                                pack_bf16(acc[rb][cb][4 * g + 2], acc[rb][cb][4 * g + 3]));
     stage_order();
+    if (special && lane < kWN) {
+        // what the product left out, one column a lane: an infinity or NaN
+        // whatever the finite terms are, so it may be added to the rounded sum
+        const int n = n0 + wave * kWN + lane;
+        for (int s = s0;; ++s) {
+            const Seg g = segment(s);
+            if (g.beg >= p0 + rows) break;
+            const uint16_t* B = reinterpret_cast<const uint16_t*>(a.B) + g.bo + (int64_t)min(n, n1 - 1) * g.rp;
+            for (int j = 0; j < g.rp; ++j) {
+                if ((B[j] & 0x7f80u) != 0x7f80u) continue;
+                const float b = bf16_to_f32(B[j]);
+                for (int row = max(g.beg - p0, 0); row < min(g.end - p0, rows); ++row) {
+                    uint16_t& o = so[row * OLD + lane];
+                    o = (uint16_t)f32_to_bf16(bf16_to_f32(o) + b * p.S[(int64_t)(p0 + row) * a.cols + sl * a.r_max + j]);
+                }
+            }
+        }
+        stage_order();
+    }
     const int c = lane % kCh;
     const int n = n0 + wave * kWN + c * 8;          // slices are multiples of 8 wide
 #pragma unroll

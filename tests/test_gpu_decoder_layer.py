@@ -136,21 +136,31 @@ def test_two_graphs_share_a_workspace():
 @pytest.mark.parametrize("M,K,sizes", [(40, 512, [72]), (64, 4096, [16]), (200, 2064, [264, 40]),
                                        (300, 1040, [264, 72]), (300, 144, [13320])])
 def test_adapters_infinities_stay_with_its_tokens(M, K, sizes):
-    """Infinite and NaN values in one adapter's A and B: tokens of other
-    adapters, and without one, keep their bits."""
+    """Infinite and NaN values in one adapter's B make its own tokens' columns
+    infinite or NaN, a NaN in its A all its outputs; everything else keeps its
+    bits."""
     import adapter_lora_amd as ml
     c = Case(M, K, sizes, [16, 32, 64], None, seed=5)
     clean = c.run()
     c.check(clean)
     c.B[1][3, 1] = float("inf")
     c.B[1][5, 0] = float("nan")
-    c.A[1][2, 7] = float("nan")
+    c.B[1][6, 31] = float("-inf")
     c.table = ml.LoraTable(c.A, c.B, c.ranks, sizes, K, torch.bfloat16)
     y = c.run()
     other = c.ids != 1
     assert other.any() and (~other).any()
     assert torch.equal(y[other], clean[other])
-    assert torch.isnan(y[~other][:, 5]).all()
+    # S enters as hi + lo: inf * hi + inf * lo is NaN where their signs differ,
+    # so an infinite column is promised to be infinite or NaN, no more
+    assert not torch.isfinite(y[~other][:, [3, 5, 6]]).any()
+    rest = [n for n in range(c.N) if n not in (3, 5, 6)]
+    assert torch.equal(y[~other][:, rest], clean[~other][:, rest])
+    c.A[1][2, 7] = float("nan")
+    c.table = ml.LoraTable(c.A, c.B, c.ranks, sizes, K, torch.bfloat16)
+    y = c.run()
+    assert torch.equal(y[other], clean[other])
+    assert torch.isnan(y[~other][:, :sizes[0]]).all()
 
 
 @pytest.mark.parametrize("M,w8", [(6, False), (14, True), (30, False), (30, True), (60, False)])
