@@ -515,20 +515,24 @@ __device__ __forceinline__ void md_gate_up(const MoeDecodeParams& p, const MdRou
                                : kBufOff;
         }
     };
-    auto issue = [&](B& b) {
-        const int kb = b_load * kMdWaves + wave;
+    // U blocks are issued at a time, one after the other
+    auto issue = [&](B& b, int q) {
+        const int kb = (b_load + q) * kMdWaves + wave;
         const bool on = u_load < units && kb < KB;
         md_issue<W8, XP>(b, uniform_rsrc(wbase, on ? ebytes : 0u), rx, rows, on ? kb : KB, p.H);
-        if (++b_load == nb) {
-            b_load = 0;
-            u_load += stride;
-            set_rows();
-        }
+    };
+    auto issued = [&]() {
+        b_load += U;
+        if (b_load < nb) return;
+        b_load = 0;
+        u_load += stride;
+        set_rows();
     };
     set_rows();
     B blk[U];
 #pragma unroll
-    for (int q = 0; q < U; ++q) issue(blk[q]);
+    for (int q = 0; q < U; ++q) issue(blk[q], q);
+    issued();
 
     for (int u = first; u < units; u += stride) {
         const int g = md_uni((int)rt.group[u / tiles]);
@@ -555,9 +559,11 @@ __device__ __forceinline__ void md_gate_up(const MoeDecodeParams& p, const MdRou
         MdStep step = md_step(ad, p.r, wave);
         uint4 bop[2];
         if (step.l >= 0) md_step_load(p, p.B_gu, (int64_t)p.E * 2 * p.I * p.r, row, step, bop);
-        for (int b = 0; b < nb; b += U)
+        for (int b = 0; b < nb; b += U) {
 #pragma unroll
-            for (int q = 0; q < U; ++q) md_consume<W8, XP>(blk[q], st, at, acc, [&]() { issue(blk[q]); });
+            for (int q = 0; q < U; ++q) md_consume<W8, XP>(blk[q], st, at, acc, [&]() { issue(blk[q], q); });
+            issued();
+        }
         if constexpr (W8) {
             // columns past I (a ragged last tile) are never stored
 #pragma unroll
@@ -724,19 +730,23 @@ __device__ __forceinline__ void md_down(const MoeDecodeParams& p, const MdRoute&
             rows.x[i] = t < g.ne ? (uint32_t)rt.list[g.base + t] * (uint32_t)p.I * 2u + (lane % 8) * 16 : kBufOff;
         }
     };
-    auto issue = [&](B& b) {
-        const bool on = g_load * KB < t1 && kb_load < end_load;
-        md_issue<W8, XP>(b, uniform_rsrc(wbase, on ? ebytes : 0u), rh, rows, on ? kb_load : KB, p.I);
-        kb_load += kMdWaves;
-        if (--left == 0) {
-            ++g_load;
-            set_rows();
-        }
+    auto issue = [&](B& b, int q) {
+        const int kb = kb_load + q * kMdWaves;
+        const bool on = g_load * KB < t1 && kb < end_load;
+        md_issue<W8, XP>(b, uniform_rsrc(wbase, on ? ebytes : 0u), rh, rows, on ? kb : KB, p.I);
+    };
+    auto issued = [&]() {
+        kb_load += U * kMdWaves;
+        left -= U;
+        if (left > 0) return;
+        ++g_load;
+        set_rows();
     };
     set_rows();
     B blk[U];
 #pragma unroll
-    for (int q = 0; q < U; ++q) issue(blk[q]);
+    for (int q = 0; q < U; ++q) issue(blk[q], q);
+    issued();
 
     f32x4_t part[2][TB];
     auto clear = [&]() {
@@ -781,9 +791,11 @@ __device__ __forceinline__ void md_down(const MoeDecodeParams& p, const MdRoute&
                 for (int q = 0; q < 4; ++q) s[n][q] = sc[min(n0 + 16 * n + lq * 4 + q, p.H - 1)];
         }
         clear();
-        for (int b = 0; b < nb; b += U)
+        for (int b = 0; b < nb; b += U) {
 #pragma unroll
-            for (int q = 0; q < U; ++q) md_consume<W8, XP>(blk[q], st, at, part, [&]() { issue(blk[q]); });
+            for (int q = 0; q < U; ++q) md_consume<W8, XP>(blk[q], st, at, part, [&]() { issue(blk[q], q); });
+            issued();
+        }
         add(g, W8 ? s : one);
     }
     if (p.L > 0) {
