@@ -307,7 +307,15 @@ __device__ __forceinline__ unsigned long long md_uni(unsigned long long v) {
 // ---------------------------------------------------------------- the stream
 // One block: 128 bytes of each of 32 expert rows (64 values of K in bf16, 128 in
 // 8 bits) and the same values of 8 XP token rows, in registers from their load
-// to their turn.  A wavefront keeps U blocks in flight.
+// to their turn.  A wavefront keeps U = md_flight blocks in flight and works in
+// rounds of U.  Twelve wavefronts of a compute unit have 50 KB or more of expert
+// rows on their way with one each, which is what latency times bandwidth asks
+// for; more of them pays where the next block's address waits for nothing (one
+// token of two bf16 experts: 1 block 127 us a call, 2 124, 4 122) and costs where
+// rounds end ragged (12 tokens of H = 4096 in rounds of 3: 234, of 2 222; 27
+// tokens of 40 experts in 8 bits, rounds of 2: 123, of 1 114).
+constexpr int md_flight(bool w8) { return w8 ? 1 : 2; }
+
 constexpr int md_blocks_of(int XP) { return (XP + 1) / 2; }      // 16-column token blocks
 
 template <bool W8, int XP> struct MdBlock {
@@ -474,13 +482,13 @@ __device__ __forceinline__ void md_step_add(const MoeDecodeParams& p, const uint
 // (up to 32 tokens of an expert, 16 gate and 16 up rows).  The wavefronts share a unit's K, block
 // by block in turn; the loads of the next unit are issued from the last blocks of the
 // one before, so the stream does not stop at its end.
-template <bool W8, int XP, int U>
+template <bool W8, int XP>
 __device__ __forceinline__ void md_gate_up(const MoeDecodeParams& p, const MdRoute& rt, const float* s_w,
                                            const int16_t* s_ad, uint32_t* s_S, uint4* smem, int first, int stride,
                                            uint32_t want, bool* lost) {
     using B = MdBlock<W8, XP>;
     constexpr int TB = md_blocks_of(XP);
-    constexpr int kBytes = W8 ? 1 : 2;
+    constexpr int kBytes = W8 ? 1 : 2, U = md_flight(W8);
     constexpr int kWords = md_stage_words(XP);
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     const int lr = lane % 16, lq = lane / 16;
@@ -663,11 +671,11 @@ __global__ __launch_bounds__(kMdThreads, 3) void k_moe_gate_up(MoeDecodeParams p
     uint32_t* S = P * p.r <= kMdMaxS ? s_S : nullptr;
     const int most = md_uni(rt.n_max);
     if (XPM == 1 || most <= 8)
-        md_gate_up<W8, 1, W8 ? 2 : 4>(p, rt, s_w, s_ad, S, smem, blk, stride, want, &lost);
+        md_gate_up<W8, 1>(p, rt, s_w, s_ad, S, smem, blk, stride, want, &lost);
     else if (XPM == 2 || most <= 16)
-        md_gate_up<W8, 2, W8 ? 2 : 3>(p, rt, s_w, s_ad, S, smem, blk, stride, want, &lost);
+        md_gate_up<W8, 2>(p, rt, s_w, s_ad, S, smem, blk, stride, want, &lost);
     else
-        md_gate_up<W8, XPM, W8 ? 1 : 2>(p, rt, s_w, s_ad, S, smem, blk, stride, want, &lost);
+        md_gate_up<W8, XPM>(p, rt, s_w, s_ad, S, smem, blk, stride, want, &lost);
     if (lost) atomicOr(p.err, LORA_DEVERR_WAIT);
 }
 
@@ -680,12 +688,12 @@ __global__ __launch_bounds__(kMdThreads, 3) void k_moe_gate_up(MoeDecodeParams p
 // others, and columns do not grow with the batch.
 constexpr int kMdOut = 36;                         // floats of a token's 32 rows, spread over banks
 
-template <bool W8, int XP, int U>
+template <bool W8, int XP>
 __device__ __forceinline__ void md_down(const MoeDecodeParams& p, const MdRoute& rt, const int16_t* s_ad, float* out,
                                         uint4* st, int n0, int split, uint32_t want, bool* lost) {
     using B = MdBlock<W8, XP>;
     constexpr int TB = md_blocks_of(XP);
-    constexpr int kBytes = W8 ? 1 : 2;
+    constexpr int kBytes = W8 ? 1 : 2, U = md_flight(W8);
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     const int lr = lane % 16, lq = lane / 16;
     const StageAt at;
@@ -849,7 +857,6 @@ __device__ __forceinline__ void md_down(const MoeDecodeParams& p, const MdRoute&
 template <bool W8, int XPM, int MT>
 __global__ __launch_bounds__(kMdThreads, MT > 32 ? 2 : 3) void k_moe_down(MoeDecodeParams p, int shrinks) {
     constexpr int kWords = md_stage_words(XPM);
-    constexpr int kMore = MT > 32 ? 1 : 0;
     __shared__ uint4 smem[kMdWaves * kWords];
     __shared__ __attribute__((aligned(16))) float s_out[kMdWaves][MT * kMdOut];
     __shared__ MdRoute rt;
@@ -878,11 +885,11 @@ __global__ __launch_bounds__(kMdThreads, MT > 32 ? 2 : 3) void k_moe_down(MoeDec
     const int most = md_uni(rt.n_max);
     uint4* st = smem + wave * kWords;
     if (XPM == 1 || most <= 8)
-        md_down<W8, 1, (W8 ? 3 : 4) + kMore>(p, rt, s_ad, s_out[wave], st, n0, split, want, &lost);
+        md_down<W8, 1>(p, rt, s_ad, s_out[wave], st, n0, split, want, &lost);
     else if (XPM == 2 || most <= 16)
-        md_down<W8, 2, (W8 ? 2 : 3) + kMore>(p, rt, s_ad, s_out[wave], st, n0, split, want, &lost);
+        md_down<W8, 2>(p, rt, s_ad, s_out[wave], st, n0, split, want, &lost);
     else
-        md_down<W8, 4, (W8 ? 1 : 2) + kMore>(p, rt, s_ad, s_out[wave], st, n0, split, want, &lost);
+        md_down<W8, 4>(p, rt, s_ad, s_out[wave], st, n0, split, want, &lost);
     __syncthreads();
     // the wavefronts' sums in a fixed order, then the splits'
     for (int i = tid; i < p.M * 8; i += kMdThreads) {
