@@ -8,12 +8,11 @@
 //
 // What bounds it: W8 is read once, N K bytes, and everything else is small, so
 // the launch is a stream of W8 with the rest hidden behind it.
-//   producers (first in the grid): unit = (segment, 16 S columns), the whole
-//     of K over eight wavefronts, bf16 MFMA 16 x 16 x 32, joined through LDS.
-//     S goes to tagged exchange slots already split into the bf16 hi / lo pair
-//     that the second product takes: one 32-bit word per value.  (K in
-//     quarters gave the producers a shorter chain but every consumer four
-//     times the slots to read: 18.9 against 13.0 us on 32 mixed tokens.)
+//   producers (first in the grid): unit = (segment, 16 S columns, half of K or
+//     all of it) over eight wavefronts, bf16 MFMA 16 x 16 x 32, joined through
+//     LDS.  S goes to tagged exchange slots in fp32, one a value and half; the
+//     consumers add the halves and split the sum into the bf16 hi / lo pair of
+//     their product.
 //   consumers: unit = 16 NR output columns of one slice for every token, K over
 //     eight wavefronts (v_mfma_f32_16x16x128_f8f6f4, W rows as the first
 //     operand so that a lane ends with four consecutive columns of one token).
@@ -31,8 +30,14 @@
 // lies below 2^-13 of it (seen with single products; every e4m3 form does), then
 // adds the eights in fp32.  That is some 2^-14 of a sum's magnitudes, far below
 // the 2^-4 to which the operands were rounded; widening both to bf16 would avoid
-// it at half the matrix rate.  Everything else is fp32; S enters its product as the sum of two bf16 values (an error
-// of 2^-17 of S at most); y is rounded once.
+// it at half the matrix rate.  Everything else is fp32; S enters its product as
+// the sum of two bf16 values (an error of 2^-17 of S at most); y is rounded once.
+//
+// Measured (kernel alone): one token to 4096 + 1024 + 1024 columns, K = 4096, rank
+// 64 11.3 us, without an adapter 9.6; 32 tokens of 32 mixed adapters to 4096
+// columns 12.2, without adapters 8.8.  W8's 25 and 17 MB would take 4.9 and 3.3
+// at the rate of a large copy: what is left is the launch, the first loads' round
+// trips (index, rows, S, join) and the producers' chain.
 #pragma once
 
 #include "common.hpp"
@@ -601,7 +606,11 @@ hipError_t launch_linear_fp8_as(Fp8Params& p, hipStream_t st) {
     unsigned grid;
     if (SLOTS) {
         p.jb = p.a.cols / 16;
-        p.chunks = p.a.K > 1024 ? 2 : 1;
+        // K in halves shortens the chain that the consumers wait for, as long
+        // as both halves' workgroups fit the chip in one round (in one and in
+        // two, 32 adapters: 4096 x 4096 with 32 tokens 14.3 / 12.9 us, 64 tokens
+        // 18.1 / 16.9; three slices, 768 halves, 64 tokens 26.6 / 28.5)
+        p.chunks = p.a.K > 1024 && 2 * p.a.s_max * p.jb <= 256 ? 2 : 1;
         p.chunk_kb = ((p.a.K + 63) / 64 + p.chunks - 1) / p.chunks;
         p.n_prod = p.a.s_max * p.jb * p.chunks;
         grid = (unsigned)(p.n_prod + t);
@@ -635,9 +644,13 @@ hipError_t launch_linear_fp8(const LinearArgs& a, const void* W8, int64_t ldw, c
     Fp8Params p = fp8_params(a, W8, ldw, w_scale, x8, ldx8, x_scale, x, ldx, y, ldy);
     p.slots = reinterpret_cast<slot_t*>(static_cast<char*>(ws) + linear_ws_layout(0, a.K, a.cols).slots);
     p.wc = wait_ctl();
-    // a unit reads every token row once: twice the columns halve that, as long
-    // as two units are left for each compute unit
-    const bool wide = a.slice_off[a.n_sl] / 32 >= 512;
+    // A unit reads every token row once: twice the columns halve that and the
+    // units.  Measured, 16 against 32 columns, K = 4096: N = 8192 1 token 12.0 /
+    // 10.6 us, 32 tokens 18.9 / 16.5, 64 25.3 / 23.6; N = 28672 32.8 / 27.7, 53.0 /
+    // 41.8, 73.3 / 72.0; N = 6144 10.4 / 9.2, 20.6 / 24.2, 28.6 / 28.3; N = 4096
+    // 8.0 / 8.4, 12.9 / 14.5, 16.9 / 21.6.
+    const int64_t units = a.slice_off[a.n_sl] / 32;
+    const bool wide = units >= (a.M <= 16 ? 192 : 256);
     if (a.M <= 16) return wide ? launch_linear_fp8_as<1, 2>(p, st) : launch_linear_fp8_as<1, 1>(p, st);
     if (a.M <= 32) return wide ? launch_linear_fp8_as<2, 2>(p, st) : launch_linear_fp8_as<2, 1>(p, st);
     return wide ? launch_linear_fp8_as<4, 2>(p, st) : launch_linear_fp8_as<4, 1>(p, st);
@@ -649,7 +662,9 @@ hipError_t launch_linear_fp8_groups(const LinearArgs& a, const void* W8, int64_t
     Fp8Params p = fp8_params(a, W8, ldw, w_scale, x8, ldx8, x_scale, nullptr, 0, y, ldy);
     p.S = S;
     // 32 columns a unit halve the reads of x; 16 where that leaves most of the
-    // compute units without one
+    // compute units without one (16 against 32 columns, K = 4096: 65 tokens to 2048
+    // columns 18.6 / 20.3 us, to 4096 25.4 / 21.8; 512 tokens to 512 20.4 / 22.5, to
+    // 1024 27.4 / 22.7)
     const int64_t units = (a.M + 63) / 64 * (a.slice_off[a.n_sl] / 32);
     return units >= 192 ? launch_linear_fp8_as<4, 2, false>(p, st) : launch_linear_fp8_as<4, 1, false>(p, st);
 }
