@@ -735,14 +735,14 @@ lora_status lora_linear_fp8(const lora_weights_t* w, const void* W8, int64_t ldw
     LinearArgs a = make_args(w, seg, M);
     a.err = ws_error(workspace);
     if (M <= LORA_DECODE_MAX_M) {
-        // 32-bit offsets over the token rows and over 16 rows of W8 or A
-        if (!below_2gib(M, ldx, 2) || !below_2gib(M, ldx8, 1) || !below_2gib(16, ldw, 1))
+        // 32-bit offsets over the token rows, 32 rows of W8 and 16 (bf16) of A
+        if (!below_2gib(M, ldx, 2) || !below_2gib(M, ldx8, 1) || !below_2gib(32, ldw, 1))
             return LORA_UNSUPPORTED;
         return from_hip(launch_linear_fp8(a, W8, ldw, w_scale, x8, ldx8, x_scale, x, ldx, y, ldy,
                                           workspace, stream));
     }
     float* S = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + L.S);
-    if (!below_2gib(256, ldw, 1)) return LORA_UNSUPPORTED;
+    if (!below_2gib(256, ldw, 1)) return LORA_UNSUPPORTED;     // 256 rows of W8
     return from_hip(launch_linear_fp8_many(a, W8, ldw, w_scale, x8, ldx8, x_scale, x, ldx, S, y, ldy, workspace,
                                            stream));
 }

@@ -79,6 +79,11 @@ def test_linear_fp8_refusals():
     assert call(w, seg, M=0, x=null) == abi().LORA_OK
     assert call(*table(K=136), ldw=144, ldx8=144, ldx=136) == UNS          # K % 16
     assert call(*table(dtype=0)) == UNS                                    # fp32 table
+    # byte offsets past 31 bits: 32 rows of W8 (16 of them would fit), 256 of the
+    # larger product, the token rows
+    assert call(w, seg, ldw=(1 << 31) // 20 // 16 * 16) == UNS
+    assert call(w, seg, M=100, ldw=(1 << 31) // 200 // 16 * 16, bytes=1 << 30) == UNS
+    assert call(w, seg, ldx=1 << 28) == UNS and call(w, seg, ldx8=1 << 29) == UNS
     seg.L = 5
     assert call(w, seg) == INV
 
