@@ -541,15 +541,12 @@ def lora_moe_topk_reduce(cache3: torch.Tensor, topk_weights: torch.Tensor, out: 
 E4M3 = torch.float8_e4m3fn
 
 
-def _check_e4m3(**named) -> None:
-    for name, t in named.items():
-        if t.dtype != E4M3:
-            raise LoraError(f"{name} is {t.dtype} but must be {E4M3}")
+_F32 = torch.float32
 
 
 def _scales(t: torch.Tensor, name: str, n: int) -> int:
     """Device address of one fp32 scale per row of an 8-bit tensor."""
-    if t.dtype != torch.float32 or t.numel() < n or not t.is_contiguous():
+    if t.dtype is not _F32 or t.numel() < n or not t.is_contiguous():
         raise LoraError(f"{name} must be contiguous fp32 with {n} values")
     if not t.is_cuda:
         raise LoraError(f"{name} must live on the GPU")
@@ -630,25 +627,26 @@ def lora_linear_fp8(table: LoraTable, W8: torch.Tensor, w_scale: torch.Tensor, x
     """y = (x8 W8^T) x_scale w_scale + (x A_i^T) B_i^T per token, y overwritten:
     a shared projection in 8 bits ([N, K], the table's slices stacked in
     order) beside the batch's adapters.  One launch for up to 64 tokens."""
-    K, N, dtype = table.K, table.N, table.dtype
-    _check_io(dtype, x=x, y=y)
-    _check_e4m3(W8=W8, x8=x8)
-    _cols(x, "x", K)
-    _cols(x8, "x8", K)
-    _cols(W8, "W8", K)
-    _cols(y, "y", N, exact=False)
-    M = x.shape[0]
-    if x8.shape[0] != M or y.shape[0] != M:
-        raise LoraError("x, x8 and y must have the same number of rows")
-    if W8.shape[0] != N:
-        raise LoraError("W8 must have one row per output column of the table")
-    ldx, ldx8, ldw, ldy = _rows(x, "x"), _rows(x8, "x8"), _rows(W8, "W8"), _rows(y, "y")
-    pw, px = _scales(w_scale, "w_scale", N), _scales(x_scale, "x_scale", M)
+    K, N, dtype, shape = table.K, table.N, table.dtype, x.shape
+    if not (x8.shape == shape and W8.shape == (N, K) and y.shape == (shape[0], N)):
+        _cols(x, "x", K)
+        _cols(x8, "x8", K)
+        _cols(W8, "W8", K)
+        _cols(y, "y", N, exact=False)
+        if x8.shape != shape or y.shape[0] != shape[0]:
+            raise LoraError("x, x8 and y must have the same number of rows")
+        if W8.shape[0] != N:
+            raise LoraError("W8 must have one row per output column of the table")
+    M = shape[0]
+    pw, ldw = _matrix(W8, "W8", (N, K), E4M3)
+    px8, ldx8 = _matrix(x8, "x8", shape, E4M3)
+    px, ldx = _matrix(x, "x", (M, K), dtype)
+    py, ldy = _matrix(y, "y", y.shape, dtype)
+    pws, pxs = _scales(w_scale, "w_scale", N), _scales(x_scale, "x_scale", M)
     if seg.L != table.L or M > seg.sorted_idx.shape[0]:
         raise LoraError("segment buffers do not match the table or the batch")
-    check(lib.lora_linear_fp8(table.ref, W8.data_ptr(), ldw, pw, x8.data_ptr(), ldx8, px,
-                              x.data_ptr(), ldx, M, seg.ref, y.data_ptr(), ldy, ws.ptr, ws.nbytes,
-                              stream_handle(stream)), "lora_linear_fp8")
+    check(lib.lora_linear_fp8(table.ref, pw, ldw, pws, px8, ldx8, pxs, px, ldx, M, seg.ref, py, ldy,
+                              ws.ptr, ws.nbytes, stream_handle(stream)), "lora_linear_fp8")
 
 
 class MoeExperts:
