@@ -771,15 +771,17 @@ static lora_status check_experts(const lora_moe_experts_t* ex, const lora_moe_we
 }
 
 namespace {
-// header | routing slots [2][P] | chosen experts [P] | S of gate/up [P][r] |
-// S of down [P][r] | joined partial sums [splits - 1][M][H] | h [P][I]
+// header | routing slots [2][P] | S of gate/up [P][r] | S of down [P][r] | joined
+// partial sums [splits - 1][M][H] of the M with most | chosen experts [P] | h [M
+// topk][I], with P = 64 topk.  The slot regions do not depend on M, so calls of any M may share a
+// workspace: no plain value ever stands where another call looks for a tag.
 struct MoeDecodeWs {
-    size_t route, ids, s_gu, s_d, join, h, total;
+    size_t route, s_gu, s_d, join, ids, h, total;
 };
 
 MoeDecodeWs moe_decode_ws(const lora_moe_experts_t* ex, int r, int M) {
     MoeDecodeWs l{};
-    const size_t P = (size_t)M * ex->topk;
+    const size_t P = (size_t)LORA_DECODE_MAX_M * ex->topk;
     size_t off = up(sizeof(WsHeader));
     auto take = [&off](size_t bytes) {
         const size_t at = off;
@@ -787,11 +789,13 @@ MoeDecodeWs moe_decode_ws(const lora_moe_experts_t* ex, int r, int M) {
         return at;
     };
     l.route = take(2 * P * sizeof(slot_t));
-    l.ids = take(P * sizeof(int32_t));
     l.s_gu = take(P * r * sizeof(slot_t));
     l.s_d = take(P * r * sizeof(slot_t));
-    l.join = take((size_t)(moe_decode_splits(ex->H, M) - 1) * M * ex->H * sizeof(slot_t));
-    l.h = take(P * ex->I * sizeof(uint16_t));
+    const size_t few = (size_t)(moe_decode_splits(ex->H, 32) - 1) * 32;
+    const size_t many = (size_t)(moe_decode_splits(ex->H, LORA_DECODE_MAX_M) - 1) * LORA_DECODE_MAX_M;
+    l.join = take(std::max(few, many) * ex->H * sizeof(slot_t));
+    l.ids = take(P * sizeof(int32_t));
+    l.h = take((size_t)M * ex->topk * ex->I * sizeof(uint16_t));
     l.total = off;
     return l;
 }
@@ -800,9 +804,7 @@ MoeDecodeWs moe_decode_ws(const lora_moe_experts_t* ex, int r, int M) {
 size_t lora_moe_decode_workspace_size(const lora_moe_weights_t* w, const lora_moe_experts_t* ex,
                                       int32_t M) {
     if (check_experts(ex, w) != LORA_OK || M < 0 || M > LORA_DECODE_MAX_M) return 0;
-    // enough for fewer tokens too (up to 32 take more splits)
-    const int r = w ? w->r : 0;
-    return std::max(moe_decode_ws(ex, r, M).total, moe_decode_ws(ex, r, std::min(M, 32)).total);
+    return moe_decode_ws(ex, w ? w->r : 0, M).total;
 }
 
 lora_status lora_moe_decode(const lora_moe_weights_t* w, const lora_moe_experts_t* ex,

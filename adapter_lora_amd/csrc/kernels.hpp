@@ -268,7 +268,7 @@ struct MoeDecodeParams {
     WaitCtl wc;
 };
 
-// Workgroups that share one tile of 16 output columns of the second launch.
+// Workgroups that share one tile of 32 output columns of the second launch.
 int moe_decode_splits(int H, int M);
 
 hipError_t launch_moe_decode(const MoeDecodeParams& p, hipStream_t st);

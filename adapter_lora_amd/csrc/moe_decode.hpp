@@ -9,14 +9,21 @@
 // What bounds it: each expert that some token chose is read once, 3 H I
 // values; tokens, adapters and the router are small beside that.  Both
 // launches are streams of expert rows through bf16 MFMA (16 x 16 x 32, the
-// expert's rows as the first operand, tokens as columns), with the rest done
-// by workgroups that come first in the grid and overlap the stream:
-//   first launch   router (one workgroup per token), then one per (token,
-//                  expert) pair that computes its adapter's A_gu x, then the
-//                  consumers, which walk (expert, 16 gate and 16 up rows);
-//   second launch  one per pair for A_d h, then the consumers of 16 output
-//                  rows, all chosen experts in one sum: the routing weight is
-//                  already in h, so a token's experts simply add up.
+// expert's rows as the first operand, the expert's own tokens as columns), with
+// the rest done by workgroups that come first in the grid and overlap the
+// stream:
+//   first launch   router (one workgroup per token), then 16 rows of A_gu x per
+//                  workgroup and (token, expert) pair, then the consumers, which
+//                  walk (up to 32 tokens of an expert, 16 gate and 16 up rows);
+//   second launch  16 rows of A_d h per workgroup and pair, then the consumers of
+//                  32 output rows and a share of all chosen experts: the routing
+//                  weight is already in h, so a token's experts simply add up.
+// Measured, first and second launch: 1 token, 2 of 8 experts of 4096 x 14336 in
+// bf16 78 and 41 us (6.0 and 5.7 TB/s of expert rows; a large copy reaches 5.1
+// with its writes); 64 tokens, all 8 of them 331 and 171 (5.7, 5.5); 27 tokens, 4
+// of 40 experts of 2064 x 1424 in 8 bits 72 and 44 (3.0, 2.5): there the stream
+// runs at 6 TB/s as well, between 12 us in which the router works and every
+// workgroup makes its tables, 6 until the first loads, and a ragged end.
 // Results cross workgroups of a launch through tagged exchange slots
 // (common.hpp); whoever waits comes later in the grid than whom it waits for,
 // and every wait is bounded.
@@ -128,7 +135,8 @@ __device__ __forceinline__ void widen16(const uint4& q, uint4& a, uint4& b) {
 }
 
 // S values of the gate / up products that a workgroup keeps in LDS; a call with
-// more (pairs times rank) reads the slots again for every unit.
+// more (pairs times rank) reads the slots again for every unit.  Measured with and
+// without, top 8 of 128 experts: 4 tokens 78 / 104 us a layer, 64 tokens 255 / 287; top 4 of 40, 27 tokens 116 / 111.
 constexpr int kMdMaxS = 4096;
 
 // Adapter of token m, or -1 (none, disabled, or outside the table).
@@ -349,9 +357,8 @@ __device__ __forceinline__ void md_issue(MdBlock<W8, XP>& b, __amdgpu_buffer_rsr
     }
 }
 
-// uint4 of LDS per wavefront: 32 expert rows and 16 token rows (32 of XP = 8,
-// whose partial sums need the room at the end)
-constexpr int md_stage_words(int XP) { return 32 * 8 + (XP < 8 ? 16 : 32) * 8; }
+// uint4 of LDS per wavefront: 32 expert rows and 16 token rows
+constexpr int kMdStage = (32 + 16) * 8;
 
 // acc[n][t] += rows 16 n .. 16 n + 15 times token block t over the block's
 // values.  `refill` issues the block's next loads once its registers are free.
@@ -362,19 +369,18 @@ __device__ __forceinline__ void md_consume(MdBlock<W8, XP>& b, uint4* st, const 
                                            f32x4_t (&acc)[2][md_blocks_of(XP)], F refill) {
     using B = MdBlock<W8, XP>;
     constexpr int TB = md_blocks_of(XP);
-    constexpr int XT = XP < 8 ? 1 : 2;             // token blocks staged at a time
-    constexpr int PT = XP == 1 ? 1 : 2 * XT;       // their pieces
+    constexpr int PT = XP == 1 ? 1 : 2;            // pieces of a token block
     uint4* sx = st + 32 * 8;
 #pragma unroll
     for (int i = 0; i < 4; ++i) st[at.piece(i)] = b.w[i];
 #pragma unroll
     for (int h = 0; h < B::XH; ++h)
 #pragma unroll
-        for (int t0 = 0; t0 < TB; t0 += XT) {
+        for (int t = 0; t < TB; ++t) {
 #pragma unroll
-            for (int i = 0; i < PT; ++i) sx[at.piece(i)] = b.x[h][2 * t0 + i];
+            for (int i = 0; i < PT; ++i) sx[at.piece(i)] = b.x[h][2 * t + i];
             stage_order();
-            if (h == B::XH - 1 && t0 + XT >= TB) refill();
+            if (h == B::XH - 1 && t == TB - 1) refill();
             uint4 a[2][2];
             if constexpr (W8) {
 #pragma unroll
@@ -386,14 +392,12 @@ __device__ __forceinline__ void md_consume(MdBlock<W8, XP>& b, uint4* st, const 
                     for (int j = 0; j < 2; ++j) a[n][j] = st[at.half(n, j)];
             }
 #pragma unroll
-            for (int t = 0; t < XT; ++t)
+            for (int j = 0; j < 2; ++j) {
+                // in 8 bits a lane's chunk is 16 values: their two halves
+                const uint4 v = sx[W8 ? at.two(0, j) : at.half(0, j)];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    // in 8 bits a lane's chunk is 16 values: their two halves
-                    const uint4 v = sx[W8 ? at.two(t, j) : at.half(t, j)];
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) acc[n][t0 + t] = mfma_bf16(a[n][j], v, acc[n][t0 + t]);
-                }
+                for (int n = 0; n < 2; ++n) acc[n][t] = mfma_bf16(a[n][j], v, acc[n][t]);
+            }
             stage_order();
         }
 }
@@ -477,9 +481,9 @@ __device__ __forceinline__ void md_step_add(const MoeDecodeParams& p, const uint
 }
 
 // ---------------------------------------------------------------- first launch
-// The consumers of one launch: units u = first, first + stride, ... of
-// (up to 32 tokens of an expert, 16 gate and 16 up rows).  The wavefronts share a unit's K, block
-// by block in turn; the loads of the next unit are issued from the last blocks of the
+// The consumers: units u = first, first + stride, ... of (up to 32 tokens of an
+// expert, 16 gate and 16 up rows).  The wavefronts share a unit's K, block by
+// block in turn; the loads of the next unit are issued from the last round of the
 // one before, so the stream does not stop at its end.
 template <bool W8, int XP>
 __device__ __forceinline__ void md_gate_up(const MoeDecodeParams& p, const MdRoute& rt, const float* s_w,
@@ -488,10 +492,9 @@ __device__ __forceinline__ void md_gate_up(const MoeDecodeParams& p, const MdRou
     using B = MdBlock<W8, XP>;
     constexpr int TB = md_blocks_of(XP);
     constexpr int kBytes = W8 ? 1 : 2, U = md_flight(W8);
-    constexpr int kWords = md_stage_words(XP);
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     const int lr = lane % 16, lq = lane / 16;
-    uint4* st = smem + wave * kWords;
+    uint4* st = smem + wave * kMdStage;
     const StageAt at;
     const int tiles = (p.I + 15) / 16;
     const int units = md_uni(rt.n_groups) * tiles;
@@ -608,7 +611,7 @@ __device__ __forceinline__ void md_gate_up(const MoeDecodeParams& p, const MdRou
             float g[4] = {0.f, 0.f, 0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 2
             for (int w = 0; w < kMdWaves; ++w) {
-                const float4* src = reinterpret_cast<const float4*>(smem + w * kWords);
+                const float4* src = reinterpret_cast<const float4*>(smem + w * kMdStage);
                 const float4 a = src[wave * kWave + lane], c = src[(TB + wave) * kWave + lane];
                 g[0] += a.x; g[1] += a.y; g[2] += a.z; g[3] += a.w;
                 v[0] += c.x; v[1] += c.y; v[2] += c.z; v[3] += c.w;
@@ -624,11 +627,15 @@ __device__ __forceinline__ void md_gate_up(const MoeDecodeParams& p, const MdRou
 }
 
 // XPM: most pieces of eight tokens of one group, by M: 1, 2 or 4.  The variant
-// taken is the one of the batch's busiest expert: fewer token registers leave
-// more for blocks of the expert in flight.
+// taken is the one of the batch's busiest expert, as fewer pieces are less to
+// load, stage and multiply (four pieces always, against this: 16 tokens, top 8 of
+// 128 experts in 8 bits 127 / 104 us a layer, 27 tokens, top 4 of 40 130 / 116, 1
+// token, 2 of 8 experts in bf16 128 / 125).  Kernels of their own for few tokens
+// spare those the registers of the widest (12 tokens of 8 experts 227 to 238 us,
+// from one kernel for all 239).
 template <bool W8, int XPM>
 __global__ __launch_bounds__(kMdThreads, 3) void k_moe_gate_up(MoeDecodeParams p, int shrinks) {
-    __shared__ uint4 smem[kMdWaves * md_stage_words(XPM)];
+    __shared__ uint4 smem[kMdWaves * kMdStage];
     __shared__ MdRoute rt;
     __shared__ float s_w[kMdMaxPairs];
     __shared__ __attribute__((aligned(16))) uint32_t s_S[kMdMaxS];
@@ -850,13 +857,13 @@ __device__ __forceinline__ void md_down(const MoeDecodeParams& p, const MdRoute&
     }
 }
 
-// MT: most tokens.  With more than 32 the outputs of a workgroup leave room for
-// two of them in a compute unit's LDS, and those have registers for more blocks
-// in flight.  XPM, and the choice by the busiest expert: as in the first launch.
-template <bool W8, int XPM, int MT>
+// MT: most tokens, 32 or 64.  The outputs of 64 leave LDS for two workgroups a
+// compute unit, those of 32 for three (two always: 16 tokens, top 8 of 128 experts
+// 113 us a layer in place of 108, 27 tokens, top 4 of 40 122 / 117, the others within
+// 2%).
+template <bool W8, int MT>
 __global__ __launch_bounds__(kMdThreads, MT > 32 ? 2 : 3) void k_moe_down(MoeDecodeParams p, int shrinks) {
-    constexpr int kWords = md_stage_words(XPM);
-    __shared__ uint4 smem[kMdWaves * kWords];
+    __shared__ uint4 smem[kMdWaves * kMdStage];
     __shared__ __attribute__((aligned(16))) float s_out[kMdWaves][MT * kMdOut];
     __shared__ MdRoute rt;
     __shared__ int16_t s_ad[LORA_DECODE_MAX_M];
@@ -882,10 +889,10 @@ __global__ __launch_bounds__(kMdThreads, MT > 32 ? 2 : 3) void k_moe_down(MoeDec
         reinterpret_cast<float4*>(s_out[wave])[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     md_tables(p, rt);
     const int most = md_uni(rt.n_max);
-    uint4* st = smem + wave * kWords;
-    if (XPM == 1 || most <= 8)
+    uint4* st = smem + wave * kMdStage;
+    if (most <= 8)
         md_down<W8, 1>(p, rt, s_ad, s_out[wave], st, n0, split, want, &lost);
-    else if (XPM == 2 || most <= 16)
+    else if (most <= 16)
         md_down<W8, 2>(p, rt, s_ad, s_out[wave], st, n0, split, want, &lost);
     else
         md_down<W8, 4>(p, rt, s_ad, s_out[wave], st, n0, split, want, &lost);
@@ -926,10 +933,11 @@ __global__ __launch_bounds__(kMdThreads, MT > 32 ? 2 : 3) void k_moe_down(MoeDec
 }
 
 int moe_decode_splits(int H, int M) {
-    // as many as keep every consumer resident at once (with more than 32
-    // tokens a consumer has the registers of two workgroups a compute unit)
+    // as many as keep every consumer resident at once; half of that: 64 tokens, top
+    // 8 of 128 experts 314 against 255 us a layer, 1 token, 2 of 8 experts 128 / 125,
+    // 8 tokens of 16 small experts 28 / 28
     const int tiles = (H + 31) / 32;
-    return max(1, min((M > 32 ? kMdResident / 3 * 2 : kMdResident) / tiles, 16));
+    return max(1, min(256 * (M > 32 ? 2 : 3) / tiles, 16));
 }
 
 template <bool W8>
@@ -944,10 +952,8 @@ hipError_t launch_moe_decode_t(const MoeDecodeParams& p, hipStream_t st) {
     else hipLaunchKernelGGL((k_moe_gate_up<W8, 4>), g1, t, 0, st, p, shrinks);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (p.M <= 8) hipLaunchKernelGGL((k_moe_down<W8, 1, 32>), g2, t, 0, st, p, shrinks);
-    else if (p.M <= 16) hipLaunchKernelGGL((k_moe_down<W8, 2, 32>), g2, t, 0, st, p, shrinks);
-    else if (p.M <= 32) hipLaunchKernelGGL((k_moe_down<W8, 4, 32>), g2, t, 0, st, p, shrinks);
-    else hipLaunchKernelGGL((k_moe_down<W8, 4, LORA_DECODE_MAX_M>), g2, t, 0, st, p, shrinks);
+    if (p.M <= 32) hipLaunchKernelGGL((k_moe_down<W8, 32>), g2, t, 0, st, p, shrinks);
+    else hipLaunchKernelGGL((k_moe_down<W8, LORA_DECODE_MAX_M>), g2, t, 0, st, p, shrinks);
     return hipGetLastError();
 }
 

@@ -623,7 +623,8 @@ typedef struct lora_moe_experts {
 /*
  * Bytes of device workspace of lora_moe_decode for up to M tokens (0: invalid
  * arguments): zero it once (lora_workspace_init) before its first use, order
- * the calls that share it on one stream.  w may be NULL.
+ * the calls that share it on one stream.  Layers of the same E, H, I, topk and
+ * r may share one, with any M up to its own.  w may be NULL.
  */
 size_t lora_moe_decode_workspace_size(const lora_moe_weights_t* w, const lora_moe_experts_t* ex,
                                       int32_t M);

@@ -140,6 +140,11 @@ def test_moe_decode_refusals():
     assert call(experts(), M=0, x=null) == abi().LORA_OK
     assert size(experts(), None, 65) == 0 and size(experts(), None, -1) == 0
     assert size(experts(), moe_weights()) > size(experts(), None) > 0
+    # a workspace serves every smaller batch
+    for H in (64, 4096):
+        ex = experts(H=H, topk=8)
+        sizes = [size(ex, None, m) for m in range(65)]
+        assert sizes == sorted(sizes)
 
 
 def test_binding_refusals():
