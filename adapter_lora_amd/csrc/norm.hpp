@@ -15,9 +15,11 @@
 // unrounded v or h.
 //
 // What bounds it: every operand crosses HBM once.  2048 rows of 4096 in bf16
-// with the residual and all outputs 16.5 us (75 MB: 4.6 TB/s, a large copy
-// 5.1), 4099 rows of 5128 in fp32 38 (5.0 TB/s with its four fp32 operands and the 8 bits), a weight of 28672 x 4096
-// to 8 bits 83 to 89 (4.1); 32 rows 4 us, a launch and two round trips.
+// with the residual and all outputs 16.4 us (75.5 MB, 4.6 TB/s; a large copy
+// reaches 5.1), 4099 rows of 5128 in fp32 to fp32 37.4 (168 MB, 4.5), a weight of
+// 28672 x 4096 to 8 bits 72.9 (352 MB, 4.8; 84 with the norm's branches in the same
+// kernel and clamps before the conversion: the arithmetic of a value counts). 32
+// rows 4 us, a launch and two round trips.
 #pragma once
 
 #include "common.hpp"
@@ -39,18 +41,12 @@ __device__ __forceinline__ void st8(uint16_t* p, const float* v) {
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Four fp32 values to four e4m3 bytes, round to nearest even; values past
-// the largest finite one (a last-bit excess of v / scale) are clamped, NaN
-// stays NaN (the compares are false for it).
+// Four fp32 values of at most 448 (1 + 2^-22) to four e4m3 bytes, round to nearest
+// even: the largest finite value, 448, takes everything below 464, so a last-bit
+// excess of v / scale needs no clamp.  NaN stays NaN.
 __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
-    float v[4] = {a, b, c, d};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[i] = v[i] > kE4M3Max ? kE4M3Max : v[i];
-        v[i] = v[i] < -kE4M3Max ? -kE4M3Max : v[i];
-    }
-    int r = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
-    r = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], r, true);
+    int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
     return (uint32_t)r;
 }
 
@@ -65,8 +61,8 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
 }
 
 // WPR wavefronts per row, CPL chunks of 8 values per lane: a row of up to
-// 512 * WPR * CPL values.
-template <typename T, int WPR, int CPL>
+// 512 * WPR * CPL values.  Without NORM: v = x, out8 and scale alone.
+template <typename T, int WPR, int CPL, bool NORM>
 __global__ __launch_bounds__(WPR * kWave < 256 ? 256 : WPR * kWave) void k_rms_norm(NormParams p) {
     constexpr int kRows = WPR < 4 ? 4 / WPR : 1;          // rows per workgroup
     __shared__ float s_sum[kRows * WPR];
@@ -91,8 +87,8 @@ __global__ __launch_bounds__(WPR * kWave < 256 ? 256 : WPR * kWave) void k_rms_n
         for (int e = 0; e < 8; ++e) h[c][e] = 0.f, g[c][e] = 0.f;
         if (k < p.K) {
             Io<T>::ld8(x + k, h[c]);
-            if (p.w) Io<T>::ld8(w + k, g[c]);
-            if (p.res) {
+            if constexpr (NORM) Io<T>::ld8(w + k, g[c]);
+            if (NORM && p.res) {
                 float r[8];
                 Io<T>::ld8(res + k, r);
 #pragma unroll
@@ -104,14 +100,14 @@ __global__ __launch_bounds__(WPR * kWave < 256 ? 256 : WPR * kWave) void k_rms_n
     for (int c = 0; c < CPL; ++c)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            sum += h[c][e] * h[c][e];
+            if constexpr (NORM) sum += h[c][e] * h[c][e];
             // |v| as an integer: ordered like the value, with NaN above
             // infinity, so a NaN of the row reaches its scale
-            const float v = p.w ? h[c][e] * g[c][e] : h[c][e];
+            const float v = NORM ? h[c][e] * g[c][e] : h[c][e];
             const uint32_t u = __float_as_uint(v) & 0x7fffffffu;
             top = top > u ? top : u;
         }
-    sum = wave_total(sum);
+    if constexpr (NORM) sum = wave_total(sum);
     top = wave_umax(top);
     if constexpr (WPR > 1) {
         if (lane == 0) s_sum[wave] = sum, s_max[wave] = top;
@@ -127,7 +123,7 @@ __global__ __launch_bounds__(WPR * kWave < 256 ? 256 : WPR * kWave) void k_rms_n
         }
     }
     if (!live) return;
-    const float rstd = p.w ? 1.f / sqrtf(sum / (float)p.K + p.eps) : 1.f;
+    const float rstd = NORM ? 1.f / sqrtf(sum / (float)p.K + p.eps) : 1.f;
     float inv = 0.f, den = 0.f;
     if (p.out8) {
         const float amax = __uint_as_float(top) * rstd;
@@ -142,11 +138,11 @@ __global__ __launch_bounds__(WPR * kWave < 256 ? 256 : WPR * kWave) void k_rms_n
     for (int c = 0; c < CPL; ++c) {
         const int k = ((c * WPR + wr) * kWave + lane) * 8;
         if (k >= p.K) continue;
-        if (p.res_out) st8(static_cast<T*>(p.res_out) + m * p.ldro + k, h[c]);
+        if (NORM && p.res_out) st8(static_cast<T*>(p.res_out) + m * p.ldro + k, h[c]);
         float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = p.w ? h[c][e] * rstd * g[c][e] : h[c][e];
-        if (p.out) st8(static_cast<T*>(p.out) + m * p.ldo + k, v);
+        for (int e = 0; e < 8; ++e) v[e] = NORM ? h[c][e] * rstd * g[c][e] : h[c][e];
+        if (NORM && p.out) st8(static_cast<T*>(p.out) + m * p.ldo + k, v);
         if (p.out8) {
             // v / scale, the reciprocal's product corrected by its residue:
             // bf16 values over a bf16 maximum are often ties of e4m3, and a
@@ -169,7 +165,8 @@ hipError_t launch_norm_as(const NormParams& p, hipStream_t st) {
     constexpr int kRows = WPR < 4 ? 4 / WPR : 1;
     constexpr int kThreads = WPR * kWave < 256 ? 256 : WPR * kWave;
     const unsigned grid = (unsigned)((p.M + kRows - 1) / kRows);
-    hipLaunchKernelGGL((k_rms_norm<T, WPR, CPL>), dim3(grid), dim3(kThreads), 0, st, p);
+    if (p.w) hipLaunchKernelGGL((k_rms_norm<T, WPR, CPL, true>), dim3(grid), dim3(kThreads), 0, st, p);
+    else hipLaunchKernelGGL((k_rms_norm<T, WPR, CPL, false>), dim3(grid), dim3(kThreads), 0, st, p);
     return hipGetLastError();
 }
 
