@@ -33,11 +33,10 @@
 // it at half the matrix rate.  Everything else is fp32; S enters its product as
 // the sum of two bf16 values (an error of 2^-17 of S at most); y is rounded once.
 //
-// Measured (kernel alone): one token to 4096 + 1024 + 1024 columns, K = 4096, rank
-// 64 11.3 us, without an adapter 9.6; 32 tokens of 32 mixed adapters to 4096
-// columns 12.2, without adapters 8.8.  W8's 25 and 17 MB would take 4.9 and 3.3
-// at the rate of a large copy: what is left is the launch, the first loads' round
-// trips (index, rows, S, join) and the producers' chain.
+// Measured: one token to 4096 + 1024 + 1024 columns, K = 4096, 9.9 us; 32 tokens of
+// 32 mixed adapters to 4096 columns 12.8, without adapters 8.3.  W8's 25 and 17 MB
+// would take 4.9 and 3.3 at the rate of a large copy: what is left is the launch,
+// the first loads' round trips (index, rows, S, join) and the producers' chain.
 #pragma once
 
 #include "common.hpp"

@@ -19,7 +19,7 @@
 //                  32 output rows and a share of all chosen experts: the routing
 //                  weight is already in h, so a token's experts simply add up.
 // Measured, first and second launch: 1 token, 2 of 8 experts of 4096 x 14336 in
-// bf16 78 and 41 us (6.0 and 5.7 TB/s of expert rows; a large copy reaches 5.1
+// bf16 80 and 41 us (5.9 and 5.7 TB/s of expert rows; a large copy reaches 5.1
 // with its writes); 64 tokens, all 8 of them 331 and 171 (5.7, 5.5); 27 tokens, 4
 // of 40 experts of 2064 x 1424 in 8 bits 72 and 44 (3.0, 2.5): there the stream
 // runs at 6 TB/s as well, between 12 us in which the router works and every
@@ -136,7 +136,8 @@ __device__ __forceinline__ void widen16(const uint4& q, uint4& a, uint4& b) {
 
 // S values of the gate / up products that a workgroup keeps in LDS; a call with
 // more (pairs times rank) reads the slots again for every unit.  Measured with and
-// without, top 8 of 128 experts: 4 tokens 78 / 104 us a layer, 64 tokens 255 / 287; top 4 of 40, 27 tokens 116 / 111.
+// without: top 8 of 128 experts, rank 16, 4 tokens 78 / 104 us a layer, 16 tokens
+// 104 / 136; top 4 of 40, rank 32, 27 tokens 116 / 111.
 constexpr int kMdMaxS = 4096;
 
 // Adapter of token m, or -1 (none, disabled, or outside the table).
