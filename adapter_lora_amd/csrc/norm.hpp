@@ -70,7 +70,7 @@ __global__ __launch_bounds__(WPR * kWave < 256 ? 256 : WPR * kWave) void k_rms_n
     const int wave = (int)threadIdx.x / kWave;
     const int lane = lane_id();
     const int wr = wave % WPR;
-    const int row = (int)blockIdx.x * kRows + wave / WPR;
+    const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kRows + wave / WPR;
     const bool live = row < p.M;
     const int64_t m = live ? row : p.M - 1;
     const T* x = static_cast<const T*>(p.x) + m * p.ldx;
@@ -164,9 +164,12 @@ template <typename T, int WPR, int CPL>
 hipError_t launch_norm_as(const NormParams& p, hipStream_t st) {
     constexpr int kRows = WPR < 4 ? 4 / WPR : 1;
     constexpr int kThreads = WPR * kWave < 256 ? 256 : WPR * kWave;
-    const unsigned grid = (unsigned)((p.M + kRows - 1) / kRows);
-    if (p.w) hipLaunchKernelGGL((k_rms_norm<T, WPR, CPL, true>), dim3(grid), dim3(kThreads), 0, st, p);
-    else hipLaunchKernelGGL((k_rms_norm<T, WPR, CPL, false>), dim3(grid), dim3(kThreads), 0, st, p);
+    // a grid has fewer than 2^32 threads along x: more rows continue along y
+    const unsigned wgs = (unsigned)(((int64_t)p.M + kRows - 1) / kRows);
+    const unsigned gx = wgs < (1u << 21) ? wgs : 1u << 21;
+    const dim3 grid(gx, (wgs + gx - 1) / gx);
+    if (p.w) hipLaunchKernelGGL((k_rms_norm<T, WPR, CPL, true>), grid, dim3(kThreads), 0, st, p);
+    else hipLaunchKernelGGL((k_rms_norm<T, WPR, CPL, false>), grid, dim3(kThreads), 0, st, p);
     return hipGetLastError();
 }
 

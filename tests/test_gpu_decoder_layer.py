@@ -224,3 +224,79 @@ def test_checked_library_tables():
 def test_checked_library_lost_waits_are_reported():
     res = child(True)
     assert res["decode"]["valid_err"] & 1 and res["moe_err"] & 1, res        # LORA_DEVERR_WAIT
+
+
+@pytest.mark.parametrize("kw", [
+    dict(M=64, E=256, topk=16, H=64, I=32, L=8, r=64),                  # every limit; S past the LDS copy
+    dict(M=64, E=256, topk=16, H=32, I=48, L=3, r=16, w8=True, renorm=True),
+    dict(M=64, E=3, topk=3, H=80, I=48, L=4, r=48, w8=True),            # two groups of every expert
+    dict(M=33, E=2, topk=1, H=136, I=8, L=1, r=32),
+    dict(M=8, E=64, topk=2, H=8, I=1000, L=2, r=64),
+])
+def test_moe_limits(kw):
+    print(kw, flush=True)
+    layer = Layer(**kw)
+    layer.check(layer.run())
+
+
+def test_experts_past_four_gigabytes():
+    """20 experts of 235 MB each: every token goes to the last one, whose
+    output has the bits of a layer that holds it alone (renormalized, so the
+    routing weight is 1 in both)."""
+    import adapter_lora_amd as ml
+    E, H, I = 20, 4096, 9560
+    small = Layer(M=5, E=1, topk=1, H=H, I=I, L=0, renorm=True)
+    W_gu = torch.zeros(E, 2 * I, H, dtype=torch.bfloat16, device="cuda")
+    W_d = torch.zeros(E, H, I, dtype=torch.bfloat16, device="cuda")
+    W_gu[E - 1], W_d[E - 1] = small.W_gu[0], small.W_d[0]
+    router = torch.zeros(E, H, dtype=torch.bfloat16, device="cuda")
+    router[:E - 1, 0] = -1000.0
+    x = small.x
+    x[:, 0] = 1.0
+    want = small.run()
+    ex = ml.MoeExperts(router, W_gu, W_d, 1, renormalize=True)
+    ws = ml.Workspace(ml.lora_moe_decode_workspace_size(None, ex, 5))
+    out = torch.empty_like(want)
+    ids = torch.empty(5, 1, dtype=torch.int32, device="cuda")
+    ml.lora_moe_decode(None, ex, None, x, out, ws, topk_ids=ids)
+    torch.cuda.synchronize()
+    assert W_gu.numel() * 2 > 1 << 31 and (W_gu.numel() + W_d.numel()) * 2 > 1 << 32
+    assert (ids == E - 1).all() and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("M", [20, 100])
+def test_rows_far_apart(M):
+    """Rows of W8, x8 and x millions of values apart: offsets past 32 bits."""
+    c = Case(M, 256, [264, 256], [16, 32], None, seed=9)
+    want = c.run()
+    c.check(want)
+
+    def far(t, ld):
+        buf = torch.empty((t.shape[0] - 1) * ld + t.shape[1], dtype=torch.uint8 if t.dtype == E4M3
+                          else t.dtype, device="cuda")
+        v = buf.view(t.dtype).as_strided(t.shape, (ld, 1))
+        (v.view(torch.uint8) if t.dtype == E4M3 else v).copy_(t.view(torch.uint8) if t.dtype == E4M3 else t)
+        return v
+
+    W8 = far(c.W8, 8388576)                                   # 520 rows: 4.3 GB
+    assert 519 * 8388576 > 1 << 32
+    wide = 50_000_000 if M > 64 else 1 << 20                  # 99 rows: 4.95 GB
+    x8 = far(c.x8, wide)
+    x = far(c.x, wide // 2)
+    assert torch.equal(c.run(x8=x8, W8=W8, x=x), want)
+
+
+def test_two_streams_at_once():
+    """Calls with workspaces of their own on two streams, many in flight."""
+    a, b = Case(48, 2064, [264], [16, 64], None, seed=1), Layer(M=20, E=6, topk=2, H=528, I=400, L=3, r=32, w8=True)
+    wa, wb = a.run(), b.run()
+    a.check(wa), b.check(wb)
+    torch.cuda.synchronize()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    ya, yb = [torch.zeros_like(wa) for _ in range(20)], [torch.zeros_like(wb) for _ in range(20)]
+    torch.cuda.synchronize()
+    for y, z in zip(ya, yb):
+        a.run(y, stream=sa)
+        b.run(z, stream=sb)
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, wa) for y in ya) and all(torch.equal(z, wb) for z in yb)

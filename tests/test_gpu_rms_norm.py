@@ -167,3 +167,18 @@ def test_no_rows_and_other_streams():
     ml.lora_rms_norm(x, w, out=b, stream=side)
     side.synchronize()
     assert torch.equal(a, b)
+
+
+def test_more_rows_than_one_grid_axis_holds():
+    """2^26 + 3 rows of eight values: more than 2^32 threads."""
+    import adapter_lora_amd as ml
+    M = (1 << 26) + 3
+    x = torch.full((M, 8), 2.0, dtype=torch.bfloat16, device="cuda")
+    at = torch.tensor([0, 5, (1 << 23) + 1, 1 << 25, (1 << 26) - 1, 1 << 26, M - 1], device="cuda")
+    x[at] = draw(len(at), 8, torch.bfloat16, 1)
+    out8 = torch.zeros(M, 8, dtype=torch.float8_e4m3fn, device="cuda")
+    scale = torch.zeros(M, device="cuda")
+    ml.lora_quantize_rows(x, out8, scale)
+    check_eight(out8[at], scale[at], F64(x[at]), "rows past 2^32 threads")
+    scale[at] = 2.0 / 448
+    assert float((scale - 2.0 / 448).abs().max()) <= 2.0 ** -24 * 2 / 448
