@@ -44,7 +44,11 @@ namespace mlora {
 
 constexpr int kMdThreads = 256;
 constexpr int kMdWaves = kMdThreads / kWave;
-constexpr int kMdResident = 3 * 256;           // workgroups: three per compute unit
+// Consumers of the first launch: three per compute unit, as many as its LDS holds
+// (five, with the same units in shorter turns: 27 tokens, top 4 of 40 experts 127 us
+// a layer against 117, 32 tokens of 8 experts in 8 bits 160 / 149; as many fewer as
+// there are producers: 92 / 76 the launch).
+constexpr int kMdResident = 3 * 256;
 constexpr int kMdMaxE = 256;
 constexpr int kMdMaxPairs = LORA_DECODE_MAX_M * 16;
 constexpr int kMdMaxGroups = kMdMaxE + kMdMaxPairs / 33 + 1;   // a second group takes 33 tokens
@@ -934,9 +938,10 @@ __global__ __launch_bounds__(kMdThreads, MT > 32 ? 2 : 3) void k_moe_down(MoeDec
 }
 
 int moe_decode_splits(int H, int M) {
-    // as many as keep every consumer resident at once; half of that: 64 tokens, top
-    // 8 of 128 experts 314 against 255 us a layer, 1 token, 2 of 8 experts 128 / 125,
-    // 8 tokens of 16 small experts 28 / 28
+    // as many as keep every consumer resident at once, without the producers; half
+    // of that: 64 tokens, top 8 of 128 experts 314 against 255 us a layer, 1 token, 2
+    // of 8 experts 128 / 125, 8 tokens of 16 small experts 28 / 28; half again as
+    // many: 281 / 258, 128 / 127, 31 / 30, and 27 tokens, top 4 of 40 125 / 117
     const int tiles = (H + 31) / 32;
     return max(1, min(256 * (M > 32 ? 2 : 3) / tiles, 16));
 }
