@@ -791,8 +791,8 @@ MoeDecodeWs moe_decode_ws(const lora_moe_experts_t* ex, int r, int M) {
     l.route = take(2 * P * sizeof(slot_t));
     l.s_gu = take(P * r * sizeof(slot_t));
     l.s_d = take(P * r * sizeof(slot_t));
-    const size_t few = (size_t)(moe_decode_splits(ex->H, 32) - 1) * 32;
-    const size_t many = (size_t)(moe_decode_splits(ex->H, LORA_DECODE_MAX_M) - 1) * LORA_DECODE_MAX_M;
+    const size_t few = (size_t)(moe_decode_max_splits(ex->H, 32) - 1) * 32;
+    const size_t many = (size_t)(moe_decode_max_splits(ex->H, LORA_DECODE_MAX_M) - 1) * LORA_DECODE_MAX_M;
     l.join = take(std::max(few, many) * ex->H * sizeof(slot_t));
     l.ids = take(P * sizeof(int32_t));
     l.h = take((size_t)M * ex->topk * ex->I * sizeof(uint16_t));
@@ -848,7 +848,8 @@ lora_status lora_moe_decode(const lora_moe_weights_t* w, const lora_moe_experts_
     p.S_d = reinterpret_cast<slot_t*>(ws + l.s_d);
     p.join = reinterpret_cast<slot_t*>(ws + l.join);
     p.h = reinterpret_cast<uint16_t*>(ws + l.h);
-    p.splits = moe_decode_splits(ex->H, M);
+    const int64_t row = (int64_t)ex->I * (ex->wdtype == LORA_E4M3 ? 1 : 2);
+    p.splits = moe_decode_splits(ex->H, M, (int64_t)std::min(ex->E, M * ex->topk) * ((row + 127) / 128));
     p.wc = wait_ctl();
     return from_hip(launch_moe_decode(p, stream));
 }

@@ -268,8 +268,10 @@ struct MoeDecodeParams {
     WaitCtl wc;
 };
 
-// Workgroups that share one tile of 32 output columns of the second launch.
-int moe_decode_splits(int H, int M);
+// Workgroups that share one tile of 32 output columns of the second launch, which
+// streams up to `blocks` blocks of 128 bytes of K per tile; and the most for any.
+int moe_decode_max_splits(int H, int M);
+int moe_decode_splits(int H, int M, int64_t blocks);
 
 hipError_t launch_moe_decode(const MoeDecodeParams& p, hipStream_t st);
 

@@ -49,6 +49,7 @@ constexpr int kMdWaves = kMdThreads / kWave;
 // a layer against 117, 32 tokens of 8 experts in 8 bits 160 / 149; as many fewer as
 // there are producers: 92 / 76 the launch).
 constexpr int kMdResident = 3 * 256;
+constexpr int kMdMaxSplits = 32;
 constexpr int kMdMaxE = 256;
 constexpr int kMdMaxPairs = LORA_DECODE_MAX_M * 16;
 constexpr int kMdMaxGroups = kMdMaxE + kMdMaxPairs / 33 + 1;   // a second group takes 33 tokens
@@ -93,21 +94,27 @@ __device__ __forceinline__ void slot_wait8(const slot_t* s, bool on, uint32_t wa
     }
 }
 
-// Twice four consecutive slots, in flight together.
-__device__ __forceinline__ void slot_wait4x2(const slot_t* a, const slot_t* b, uint32_t want, int max_spin, bool* lost,
-                                             float* f) {
+// v += four consecutive slots of each of n (at most four) places `step` apart, in
+// order, their loads in flight together.
+__device__ __forceinline__ void slot_add4x4(const slot_t* s, int64_t step, int n, uint32_t want, int max_spin,
+                                            bool* lost, float (&v)[4]) {
     for (int spin = 0;; ++spin) {
-        slot_t v[8];
+        slot_t f[4][4];
         bool full = true;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = slot_load(a + q), v[4 + q] = slot_load(b + q);
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            full &= slot_full(v[q], want);
-            f[q] = __uint_as_float((uint32_t)v[q]);
-        }
+            for (int q = 0; q < 4; ++q) f[j][q] = slot_load(s + min(j, n - 1) * step + q);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) full &= slot_full(f[j][q], want);
         if (full || spin >= max_spin) {
             *lost |= !full;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] += j < n ? __uint_as_float((uint32_t)f[j][q]) : 0.f;
             return;
         }
         __builtin_amdgcn_s_sleep(1);
@@ -902,48 +909,58 @@ __global__ __launch_bounds__(kMdThreads, MT > 32 ? 2 : 3) void k_moe_down(MoeDec
     else
         md_down<W8, 4>(p, rt, s_ad, s_out[wave], st, n0, split, want, &lost);
     __syncthreads();
-    // the wavefronts' sums in a fixed order, then the splits'
-    for (int i = tid; i < p.M * 8; i += kMdThreads) {
-        const int m = i / 8, c = i % 8 * 4, n = n0 + c;
+    // the wavefronts' sums in a fixed order, then the splits', four at a time and,
+    // for few tokens, by several threads a place (a power of two, side by side)
+    int subs = 1;
+    while (subs < 8 && p.M * 8 * subs * 2 <= kMdThreads) subs *= 2;
+    for (int i = tid; i < p.M * 8 * subs; i += kMdThreads) {
+        const int sub = i % subs, m = i / subs / 8, c = i / subs % 8 * 4, n = n0 + c;
         if (n >= p.H) continue;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (sub == 0)
 #pragma unroll
-        for (int w = 0; w < kMdWaves; ++w) {
-            const float4 a = *reinterpret_cast<const float4*>(s_out[w] + m * kMdOut + c);
-            v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-        }
-        if (split < p.splits - 1) {
-            slot_t* d = p.join + ((int64_t)split * p.M + m) * p.H + n;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) slot_put(d + q, v[q], tag);
-        } else {
-            // the last split of a tile adds the others, in split order, two at a time
-            const slot_t* d = p.join + (int64_t)m * p.H + n;
-            const int64_t per = (int64_t)p.M * p.H;
-            for (int s = 0; s < p.splits - 1; s += 2) {
-                const bool two = s + 1 < p.splits - 1;
-                float f[8];
-                slot_wait4x2(d + s * per, d + (two ? s + 1 : s) * per, want, p.wc.max_spin, &lost, f);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] += f[q];
-                if (two)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) v[q] += f[4 + q];
+            for (int w = 0; w < kMdWaves; ++w) {
+                const float4 a = *reinterpret_cast<const float4*>(s_out[w] + m * kMdOut + c);
+                v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
             }
+        const int64_t per = (int64_t)p.M * p.H;
+        slot_t* d = p.join + (int64_t)m * p.H + n;
+        if (split < p.splits - 1) {
+            if (sub == 0)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) slot_put(d + split * per + q, v[q], tag);
+            continue;
+        }
+        // the last split of a tile adds the others
+        for (int s = sub; s < p.splits - 1; s += 4 * subs)
+            slot_add4x4(d + s * per, subs * per, min((p.splits - 2 - s) / subs + 1, 4), want, p.wc.max_spin, &lost, v);
+        for (int o = 1; o < subs; o *= 2)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] += __shfl_xor(v[q], o, kWave);
+        if (sub == 0)
             *reinterpret_cast<uint2*>(p.out + (int64_t)m * p.ldo + n) =
                 make_uint2(f32_to_bf16(v[0]) | (f32_to_bf16(v[1]) << 16), f32_to_bf16(v[2]) | (f32_to_bf16(v[3]) << 16));
-        }
     }
     if (lost) atomicOr(p.err, LORA_DEVERR_WAIT);
 }
 
-int moe_decode_splits(int H, int M) {
+int moe_decode_max_splits(int H, int M) {
     // as many as keep every consumer resident at once, without the producers; half
     // of that: 64 tokens, top 8 of 128 experts 314 against 255 us a layer, 1 token, 2
     // of 8 experts 128 / 125, 8 tokens of 16 small experts 28 / 28; half again as
     // many: 281 / 258, 128 / 127, 31 / 30, and 27 tokens, top 4 of 40 125 / 117
     const int tiles = (H + 31) / 32;
-    return max(1, min(256 * (M > 32 ? 2 : 3) / tiles, 16));
+    const int most = 256 * (M > 32 ? 2 : 3) / tiles;
+    return most < 1 ? 1 : most > kMdMaxSplits ? kMdMaxSplits : most;
+}
+
+int moe_decode_splits(int H, int M, int64_t blocks) {
+    const int most = moe_decode_max_splits(H, M);
+    // two blocks a wavefront in each (with at most 16 splits whatever the blocks,
+    // against this: 49 tokens of 10 experts of 1120 x 144 35.4 / 33.5 us a layer, 8
+    // tokens, top 8 of 57 experts of 304 x 1648 67.7 / 62.6)
+    const int64_t n = blocks / (2 * kMdWaves);
+    return n < 1 ? 1 : n < most ? (int)n : most;
 }
 
 template <bool W8>

@@ -140,6 +140,9 @@ def test_moe_decode_refusals():
     assert call(experts(), M=0, x=null) == abi().LORA_OK
     assert size(experts(), None, 65) == 0 and size(experts(), None, -1) == 0
     assert size(experts(), moe_weights()) > size(experts(), None) > 0
+    # room for the partial sums of every split of a tile but one, fp32 with a tag
+    for H, at_least in ((384, 31), (4096, 3), (1024, 15)):
+        assert size(experts(H=H, I=320), None, 64) > at_least * 64 * H * 8
     # a workspace serves every smaller batch
     for H in (64, 4096):
         ex = experts(H=H, topk=8)
