@@ -82,17 +82,6 @@ struct Fp8Params {
     WaitCtl wc;
 };
 
-// fp32 as the sum of two bf16 values, in one word
-__device__ __forceinline__ uint32_t hi_lo(float f) {
-    const uint32_t h = f32_to_bf16(f);
-    const uint32_t l = f32_to_bf16(f - bf16_to_f32(h));
-    return (h << 16) | l;
-}
-
-__device__ __forceinline__ uint4 and4(const uint4& v, uint32_t m) {
-    return make_uint4(v.x & m, v.y & m, v.z & m, v.w & m);
-}
-
 // uint4 of a wavefront's stage: 16 NR rows of W (or A) and 16 token rows,
 // later its partial sums
 constexpr int fp8_stage(int TB, int NR) {

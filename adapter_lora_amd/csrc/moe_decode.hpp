@@ -54,12 +54,6 @@ constexpr int kMdMaxE = 256;
 constexpr int kMdMaxPairs = LORA_DECODE_MAX_M * 16;
 constexpr int kMdMaxGroups = kMdMaxE + kMdMaxPairs / 33 + 1;   // a second group takes 33 tokens
 
-__device__ __forceinline__ uint32_t md_hi_lo(float f) {
-    const uint32_t h = f32_to_bf16(f);
-    const uint32_t l = f32_to_bf16(f - bf16_to_f32(h));
-    return (h << 16) | l;
-}
-
 __device__ __forceinline__ uint32_t slot_wait(const slot_t* s, uint32_t want, int max_spin, bool* lost) {
     slot_t v = slot_load(s);
     int spin = 0;
@@ -262,7 +256,7 @@ __device__ __forceinline__ void md_shrink(const uint16_t* A, const uint16_t* v, 
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         c[q] = wave_total(c[q]);
-        if (lane == 0) slot_put(S + j + q, __uint_as_float(md_hi_lo(c[q])), tag);
+        if (lane == 0) slot_put(S + j + q, __uint_as_float(hi_lo(c[q])), tag);
     }
 }
 static_assert(kMdWaves * 4 == 16, "a shrink workgroup takes 16 rows");
@@ -414,10 +408,6 @@ __device__ __forceinline__ void md_consume(MdBlock<W8, XP>& b, uint4* st, const 
         }
 }
 
-__device__ __forceinline__ uint4 md_and(const uint4& v, uint32_t m) {
-    return make_uint4(v.x & m, v.y & m, v.z & m, v.w & m);
-}
-
 // Deltas of one expert, dealt to the wavefronts: step d is one 32-wide part j
 // of the rank for one adapter among the expert's tokens (`ad`: lane t holds
 // the adapter of column t, -1 for none), and wavefront d % kMdWaves takes it.
@@ -450,7 +440,7 @@ __device__ __forceinline__ void md_step_load(const MoeDecodeParams& p, const uin
     const uint32_t mj = opaque_mask(j < p.r);
 #pragma unroll
     for (int n = 0; n < 2; ++n)
-        b[n] = md_and(ld16(B + max(s.l, 0) * per_l + row[n] * p.r + min(j, p.r - 8)), mj);
+        b[n] = and4(ld16(B + max(s.l, 0) * per_l + row[n] * p.r + min(j, p.r - 8)), mj);
 }
 
 // acc += B S for the step's columns.  S rows by pair: from `sS` when the
@@ -469,8 +459,8 @@ __device__ __forceinline__ void md_step_add(const MoeDecodeParams& p, const uint
         uint32_t w[8];
         if (sS) {
             const uint32_t m = opaque_mask(on);
-            const uint4 a = md_and(*reinterpret_cast<const uint4*>(sS + at), m);
-            const uint4 c = md_and(*reinterpret_cast<const uint4*>(sS + at + 4), m);
+            const uint4 a = and4(*reinterpret_cast<const uint4*>(sS + at), m);
+            const uint4 c = and4(*reinterpret_cast<const uint4*>(sS + at + 4), m);
             w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
             w[4] = c.x; w[5] = c.y; w[6] = c.z; w[7] = c.w;
         } else {

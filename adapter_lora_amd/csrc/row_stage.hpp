@@ -5,7 +5,7 @@
 // piece is a cache line of its own, and the vector memory unit handles one
 // line per cycle, 64 cycles for the kilobyte of one load.  Measured on the
 // MoE layer, the streams ran at that unit's pace (experts in 8 bits 2.2 TB/s,
-// in bf16 3.4 to 5.0).  Here a load takes eight whole 128-byte row segments
+// in bf16 3.4 to 5.0; as here 6 and 5.5 to 5.9).  Here a load takes eight whole 128-byte row segments
 // (eight lanes each, 16 cycles), and the rows change lanes through a region of
 // LDS that belongs to the wavefront alone: no barrier, and the loads of later
 // blocks stay in flight in registers meanwhile.
@@ -40,6 +40,17 @@ struct StageAt {
     __device__ __forceinline__ int half(int n, int i) const { return get[i] + 128 * n; }
     __device__ __forceinline__ int two(int n, int i) const { return pair[i] + 128 * n; }
 };
+
+// fp32 as the sum of two bf16 values, in one word
+__device__ __forceinline__ uint32_t hi_lo(float f) {
+    const uint32_t h = f32_to_bf16(f);
+    const uint32_t l = f32_to_bf16(f - bf16_to_f32(h));
+    return (h << 16) | l;
+}
+
+__device__ __forceinline__ uint4 and4(const uint4& v, uint32_t m) {
+    return make_uint4(v.x & m, v.y & m, v.z & m, v.w & m);
+}
 
 // Orders a wavefront's LDS writes before its later reads of other lanes'
 // data: LDS serves a wavefront in order, the compiler only has to keep it.
