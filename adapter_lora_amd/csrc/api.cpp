@@ -830,6 +830,7 @@ lora_status lora_moe_decode(const lora_moe_weights_t* w, const lora_moe_experts_
     MoeDecodeParams p{};
     p.M = M; p.topk = ex->topk; p.E = ex->E; p.H = ex->H; p.I = ex->I;
     p.renorm = ex->renormalize != 0;
+    p.topk_inv = (65536 + ex->topk - 1) / ex->topk;
     p.x = u16(x); p.ldx = ldx;
     p.router = u16(ex->router);
     p.W_gu = ex->W_gu; p.W_d = ex->W_d; p.s_gu = ex->s_gu; p.s_d = ex->s_d;

@@ -239,6 +239,7 @@ hipError_t launch_linear_fp8_many(const LinearArgs& a, const void* W8, int64_t l
 // A whole MoE layer for few tokens (moe_decode.hpp).
 struct MoeDecodeParams {
     int M, topk, E, H, I, renorm;
+    int topk_inv;                 // 65536 / topk, rounded up
     int L, r, shared_outer;       // L == 0: no adapters
     const uint16_t* x;
     int64_t ldx;

@@ -145,6 +145,10 @@ __device__ __forceinline__ void widen16(const uint4& q, uint4& a, uint4& b) {
 // 104 / 136; top 4 of 40, rank 32, 27 tokens 116 / 111.
 constexpr int kMdMaxS = 4096;
 
+// Token of pair f < 1024: f / topk by the reciprocal, rounded up to 16 bits (off by
+// less than f / 65536 < 1 / 16, and topk <= 16).
+__device__ __forceinline__ int md_token(const MoeDecodeParams& p, int f) { return f * p.topk_inv >> 16; }
+
 // Adapter of token m, or -1 (none, disabled, or outside the table).
 __device__ __forceinline__ int md_adapter(const MoeDecodeParams& p, int m) {
     if (p.L == 0) return -1;
@@ -279,7 +283,7 @@ __device__ __forceinline__ void md_tables(const MoeDecodeParams& p, MdRoute& r) 
     for (int e = tid; e < kMdMaxE; e += kMdThreads) r.mask[e] = 0ull;
     __syncthreads();
     for (int f = tid; f < P; f += kMdThreads)
-        if (r.exp_[f] >= 0) atomicOr(&r.mask[r.exp_[f]], 1ull << (f / p.topk));
+        if (r.exp_[f] >= 0) atomicOr(&r.mask[r.exp_[f]], 1ull << md_token(p, f));
     __syncthreads();
     if (tid < kWave) {
         int pairs = 0, most = 0, groups = 0;
@@ -305,7 +309,7 @@ __device__ __forceinline__ void md_tables(const MoeDecodeParams& p, MdRoute& r) 
     __syncthreads();
     for (int f = tid; f < P; f += kMdThreads) {
         const int e = r.exp_[f];
-        if (e >= 0) r.list[r.base[e] + __popcll(r.mask[e] & ((1ull << (f / p.topk)) - 1ull))] = (int16_t)f;
+        if (e >= 0) r.list[r.base[e] + __popcll(r.mask[e] & ((1ull << md_token(p, f)) - 1ull))] = (int16_t)f;
     }
     __syncthreads();
 }
@@ -523,7 +527,7 @@ __device__ __forceinline__ void md_gate_up(const MoeDecodeParams& p, const MdRou
 #pragma unroll
         for (int i = 0; i < XP; ++i) {
             const int t = 8 * i + lane / 8;
-            rows.x[i] = t < ne ? (uint32_t)((int)rt.list[base + t] / p.topk) * (uint32_t)p.ldx * 2u + (lane % 8) * 16
+            rows.x[i] = t < ne ? (uint32_t)(md_token(p, rt.list[base + t])) * (uint32_t)p.ldx * 2u + (lane % 8) * 16
                                : kBufOff;
         }
     };
@@ -565,7 +569,7 @@ __device__ __forceinline__ void md_gate_up(const MoeDecodeParams& p, const MdRou
             for (int q = 0; q < 4; ++q) sg[q] = sc[q], sg[4 + q] = sc[p.I + q];
         }
         const int f = rt.list[base + min(lane, ne - 1)];
-        const int ad = p.L > 0 && lane < ne ? s_ad[f / p.topk] : -1;
+        const int ad = p.L > 0 && lane < ne ? s_ad[md_token(p, f)] : -1;
         const int64_t row_g = (int64_t)e * 2 * p.I + min(n0 + lr, p.I - 1);
         const int64_t row[2] = {row_g, row_g + p.I};
         MdStep step = md_step(ad, p.r, wave);
@@ -654,7 +658,7 @@ __global__ __launch_bounds__(kMdThreads, 3) void k_moe_gate_up(MoeDecodeParams p
     blk -= p.M;
     if (blk < shrinks) {
         const int parts = p.r / 16, f = blk / parts, j0 = blk % parts * 16;
-        const int m = f / p.topk, l = md_adapter(p, m);
+        const int m = md_token(p, f), l = md_adapter(p, m);
         if (l < 0) return;
         const int e = (int)slot_wait(p.route + f, want, p.wc.max_spin, &lost);
         if (lost) {
@@ -777,7 +781,7 @@ __device__ __forceinline__ void md_down(const MoeDecodeParams& p, const MdRoute&
 #pragma unroll
         for (int t = 0; t < TB; ++t) {
             if (16 * t + lr >= g.ne) continue;
-            float* d = out + (int)rt.list[g.base + 16 * t + lr] / p.topk * kMdOut + lq * 4;
+            float* d = out + md_token(p, rt.list[g.base + 16 * t + lr]) * kMdOut + lq * 4;
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 float4* o = reinterpret_cast<float4*>(d + 16 * n);
@@ -829,7 +833,7 @@ __device__ __forceinline__ void md_down(const MoeDecodeParams& p, const MdRoute&
             for (; i < ng; i += p.splits, d = -1) {
                 const Group g = group(i);
                 const int f = lane < g.ne ? rt.list[g.base + lane] : 0;
-                const int ad = lane < g.ne ? s_ad[f / p.topk] : -1;
+                const int ad = lane < g.ne ? s_ad[md_token(p, f)] : -1;
                 for (++d;; ++d) {
                     const MdStep s = md_step(ad, p.r, d);
                     if (s.l < 0) break;
@@ -876,7 +880,7 @@ __global__ __launch_bounds__(kMdThreads, MT > 32 ? 2 : 3) void k_moe_down(MoeDec
     int id = (int)blockIdx.x;
     if (id < shrinks) {
         const int parts = p.r / 16, f = id / parts, j0 = id % parts * 16;
-        const int l = md_adapter(p, f / p.topk);
+        const int l = md_adapter(p, md_token(p, f));
         if (l < 0) return;
         md_shrink(p.A_d + (((int64_t)l * p.E + p.route_ids[f]) * p.r + j0) * p.I, p.h + (int64_t)f * p.I, p.I,
                   p.S_d + (int64_t)f * p.r + j0, tag);
