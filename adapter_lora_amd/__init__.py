@@ -89,7 +89,19 @@ def _rows(t: torch.Tensor, name: str) -> int:
         raise LoraError(f"{name} must be a 2-D tensor with unit column stride")
     if not t.is_cuda:
         raise LoraError(f"{name} must live on the GPU")
-    return max(t.stride(0), t.shape[1])
+    return _row_stride(t, name)
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Distance of a tensor's rows; with less than two of them there is none,
+    and the width stands in.  Rows that overlap (broadcast ones are 0 apart)
+    have no leading dimension."""
+    ld, width = t.stride(0), t.shape[1]
+    if ld >= width:
+        return ld
+    if t.shape[0] > 1:
+        raise LoraError(f"the rows of {name} overlap: they are {ld} values apart and {width} wide")
+    return width
 
 
 # ------------------------------------------------------------------------- table
@@ -566,10 +578,9 @@ def _matrix(t: Optional[torch.Tensor], name: str, shape, dtype):
         raise LoraError(f"{name} must live on the GPU")
     if t.is_contiguous():
         return t.data_ptr(), shape[1]
-    ld, unit = t.stride()
-    if unit != 1 and t.numel() > 0:
+    if t.stride(1) != 1 and t.numel() > 0:
         raise LoraError(f"{name} must have unit column stride")
-    return t.data_ptr(), max(ld, shape[1])
+    return t.data_ptr(), _row_stride(t, name)
 
 
 def lora_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
