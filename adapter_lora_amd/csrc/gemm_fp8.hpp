@@ -489,15 +489,17 @@ __global__ __launch_bounds__(kGThreads, G::Waves) void k_gemm_fp8(GemmFp8Params 
                     make_uint2(pack_bf16(acc[rb][cb][4 * g], acc[rb][cb][4 * g + 1]),
                                pack_bf16(acc[rb][cb][4 * g + 2], acc[rb][cb][4 * g + 3]));
     stage_order();
-    if (special && lane < kWN) {
+    if (special) {
         // what the product left out, one column a lane: an infinity or NaN
-        // whatever the finite terms are, so it may be added to the rounded sum
-        const int n = n0 + wave * kWN + lane;
+        // whatever the finite terms are, so it may be added to the rounded sum.
+        // The whole wavefront walks the segments, whose entries any lane may
+        // hold; only the columns are fewer than the lanes.
+        const int col = min(n0 + wave * kWN + lane, n1 - 1);
         for (int s = s0;; ++s) {
             const Seg g = segment(s);
             if (g.beg >= p0 + rows) break;
-            const uint16_t* B = reinterpret_cast<const uint16_t*>(a.B) + g.bo + (int64_t)min(n, n1 - 1) * g.rp;
-            for (int j = 0; j < g.rp; ++j) {
+            const uint16_t* B = reinterpret_cast<const uint16_t*>(a.B) + g.bo + (int64_t)col * g.rp;
+            for (int j = 0; lane < kWN && j < g.rp; ++j) {
                 if ((B[j] & 0x7f80u) != 0x7f80u) continue;
                 const float b = bf16_to_f32(B[j]);
                 for (int row = max(g.beg - p0, 0); row < min(g.end - p0, rows); ++row) {
