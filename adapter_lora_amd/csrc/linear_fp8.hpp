@@ -525,11 +525,12 @@ __global__ __launch_bounds__(kFpThreads, 4) void k_shrink_rows(LinearArgs a, con
     const __amdgpu_buffer_rsrc_t ra = uniform_rsrc(A, (uint32_t)(16 * a.K * 2));
     uint32_t off_a[2];
     const uint16_t* xr[2];
+    const int first = __builtin_amdgcn_readfirstlane(m_row[0]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         off_a[i] = (uint32_t)((8 * i + lane / 8) * a.K * 2 + (lane % 8) * 16);
         // rows past the tile's repeat its first one and are not stored
-        int m = 8 * i + lane / 8 < ms ? m_row[i] : __shfl(m_row[0], 0, kWave);
+        int m = 8 * i + lane / 8 < ms ? m_row[i] : first;
         if (table_fault(a.err, m < 0 || m >= a.M)) m = min(max(m, 0), a.M - 1);
         xr[i] = x + (int64_t)m * ldx + (lane % 8) * 8;
     }
