@@ -559,14 +559,21 @@ hipError_t launch_gemm_fp8(const LinearArgs& a, const void* x8, int64_t ldx8, co
     const int nk = (a.K + kG8K - 1) / kG8K;
     p.nk2 = (nk + 1) / 2 * 2;
     p.seg_stride = (a.L + 1 + kWave - 1) / kWave;
-    // Small units finish sooner while they fit the chip in few rounds: with K =
-    // 4096 a round of 256 small ones (two share a compute unit) takes 12 us, a
-    // round of 256 large ones 38, the rest of the call 12 and 6.  Measured, small
-    // against large: 256 x 4096 24.5 / 42.8 us, 768 x 4096 33.6 / 44.5, 768 x 8192
-    // 45.9 / 43.2, 2048 x 4096 54.8 / 47.7, 512 x 28672 112 / 96.
-    const int64_t ns = columns(128), nl = columns(256);
+    // Small units finish sooner while they fit the chip in few rounds.  A round of
+    // 256 small ones (two share a compute unit) takes 1.4 us and 8.5 for every 4096
+    // of K, a round of 256 large ones 8 and 20 (the first loads, deltas and store do
+    // not grow with K, so short K favours the small ones).  Measured calls, small
+    // against large (8 adapters): K = 512, 256 x 4096 12.6 / 21.6 us, 768 x 8192 20.4
+    // / 22.4, 512 x 28672 32.2 / 38.1; K = 1024, 512 x 14336 25.9 / 26.4, 512 x 28672
+    // 43.4 / 46.9; K = 2048, 768 x 4096 22.8 / 30.3, 512 x 14336 37.9 / 34.1; K = 4096,
+    // 256 x 4096 25.3 / 43.2, 768 x 8192 49.8 / 47.0, 2048 x 4096 61.0 / 52.4, 512 x 28672
+    // 103 / 87; K = 8192, 768 x 4096 61.2 / 73.0, 768 x 8192 85.5 / 74.6; K = 16384, 768 x
+    // 4096 107 / 124, 2048 x 4096 202 / 146.  (Past 4096 rounds, 2^20 units, large ones
+    // keep the grid below 2^32 threads.)
+    const int64_t ns = columns(128), nl = columns(256), K = a.K;
     const int64_t small = ((a.M + 63) / 64 * ns + 255) / 256, large = ((a.M + 127) / 128 * nl + 255) / 256;
-    if (6 + 12 * small < 38 * large) return launch_gemm_fp8_as<G8Shape<2, 1>>(p, st);
+    if (small <= 4096 && small * (14 * 4096 + 85 * K) < large * (80 * 4096 + 200 * K))
+        return launch_gemm_fp8_as<G8Shape<2, 1>>(p, st);
     return launch_gemm_fp8_as<G8Shape<4, 2>>(p, st);
 }
 

@@ -1,16 +1,17 @@
 """Forms of the 8-bit decoder-layer calls that a rule on sizes chooses, each at
 a size that makes it the chosen one.  Tolerances are those of the files that
 Case and Layer come from."""
+import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_linear_fp8 import Case
+from tests.test_gpu_linear_fp8 import F64, Case
 
 pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("M,K,sizes,L", [(260, 272, [264, 72], 48), (260, 272, [264, 72], 63), (130, 528, [40], 40),
-                                         (300, 144, [13320], 50)])
+                                         (300, 144, [13320], 50), (450, 1040, [15688, 72], 50)])
 def test_infinities_of_a_late_slot_stay_with_its_tokens(M, K, sizes, L):
     """Past 64 tokens, with tables of up to 63 slots: an infinite and a NaN value
     in the B of an adapter whose slot and whose segment are 32 or more."""
@@ -35,3 +36,48 @@ def test_infinities_of_a_late_slot_stay_with_its_tokens(M, K, sizes, L):
     rest = [n for n in range(c.N) if n not in hit]
     assert torch.equal(y[~other][:, rest], clean[~other][:, rest])
     assert ml.lora_read_device_error(c.ws_buf.buf) == 0
+
+
+# (M, K, slices, ranks): units of 128 x 256 need four times as many small ones, and
+# the longer K the fewer
+LARGE = {
+    "ragged": (450, 1040, [15688, 72], [20, 0, 64, 8]),
+    "many_slots": (450, 1040, [15688, 72], [16, 32] * 40),
+    "one_segment": (400, 1168, [16120], [64]),
+    "long_k": (300, 4112, [13320], [16, 64, 0]),
+}
+
+
+@pytest.mark.parametrize("name", list(LARGE))
+def test_large_units_match_oracle(name):
+    M, K, sizes, ranks = LARGE[name]
+    print(name, flush=True)
+    c = Case(M, K, sizes, ranks, None, seed=len(name))
+    c.check(c.run())
+
+
+def test_large_units_integers_bit_exact():
+    """All 32 stages of K = 4096 with factors in {-1, 0, 1}: sums are exact in
+    fp32, outputs up to 256 in bf16."""
+    c = Case(280, 4096, [13320], [16, 32, 0], None, seed=3, integers=True)
+    want = c.oracle()[0]
+    got = F64(c.run())
+    small = np.abs(want) <= 256
+    assert small.mean() > 0.5 and np.array_equal(got[small], want[small])
+
+
+def test_large_units_adapters_infinities_stay_with_its_tokens():
+    import adapter_lora_amd as ml
+    c = Case(450, 1040, [15688, 72], [16, 32, 64], None, seed=5)
+    clean = c.run()
+    c.check(clean)
+    c.B[1][3, 1] = float("inf")
+    c.B[1][15687, 0] = float("nan")
+    c.B[1][15700, 31] = float("-inf")
+    c.table = ml.LoraTable(c.A, c.B, c.ranks, c.sizes, c.K, torch.bfloat16)
+    y = c.run()
+    other, hit = c.ids != 1, [3, 15687, 15700]
+    assert torch.equal(y[other], clean[other])
+    assert not torch.isfinite(y[~other][:, hit]).any()
+    y[:, hit] = clean[:, hit]
+    assert torch.equal(y, clean)
