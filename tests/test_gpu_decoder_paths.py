@@ -81,3 +81,43 @@ def test_large_units_adapters_infinities_stay_with_its_tokens():
     assert not torch.isfinite(y[~other][:, hit]).any()
     y[:, hit] = clean[:, hit]
     assert torch.equal(y, clean)
+
+
+# (M, K, slices, ranks): slice widths that cut a unit's second 16 columns, K past one
+# round of a workgroup's blocks, S by way of partial sums
+FORMS = {
+    # decode, units of 32 columns
+    "wide_one_token_three_rounds": (1, 4112, [4104, 1032, 1064], [16, 64, 32]),
+    "wide_sixteen": (16, 1040, [2568, 1544], [16, 0, 64, 20]),
+    "wide_nine_long_k": (9, 8208, [14344], [32, 16, 0]),
+    "wide_seventeen": (17, 2064, [4104, 4104], [20, 64, 16]),
+    "wide_thirty_two": (32, 528, [8216], [16, 32, 64] * 11),
+    "wide_thirty_three": (33, 1040, [8216], [64, 16]),
+    "wide_full": (64, 4112, [5128, 3080], [16, 0, 64, 20] * 10),
+    "wide_many_slots": (64, 272, [8200], [16, 32] * 50),
+    # decode, K past one round: consumers and, on halves or all of K, producers
+    "long_k_one": (1, 8208, [40], [64]),
+    "long_k_twenty": (20, 8208, [72], [16, 64, 0, 32]),
+    "long_k_full": (64, 8208, [24, 8], [16, 32]),
+    "one_chunk": (64, 2576, [264, 72, 40], [64, 16] * 20),
+    "one_chunk_many_slots": (64, 2576, [72], [64, 16] * 70),
+    # groups of 64 tokens, units of 32 columns
+    "groups_wide": (129, 2064, [1032, 1024], [16, 64, 0]),
+    "groups_wide_four": (200, 4112, [1000, 640], [20, 64]),
+    "groups_wide_two_many_slots": (70, 2064, [4088], [16, 32] * 45),
+    # S by way of partial sums, before each product
+    "partial_sums_small_units": (700, 1040, [264, 72], [64, 16, 0, 20]),
+    "partial_sums_groups": (520, 2064, [200, 56, 8], [64, 16, 0, 20]),
+    "partial_sums_large_units": (450, 1040, [15640, 40, 16], [64, 16, 0, 20] * 18),
+}
+
+
+@pytest.mark.parametrize("name", list(FORMS))
+def test_every_form_matches_oracle(name):
+    M, K, sizes, ranks = FORMS[name]
+    print(name, flush=True)
+    c = Case(M, K, sizes, ranks, None, seed=len(name))
+    y = c.run()
+    c.check(y)
+    torch.cuda.synchronize()
+    assert torch.equal(y, c.run())
