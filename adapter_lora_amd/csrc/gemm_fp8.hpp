@@ -592,8 +592,13 @@ hipError_t launch_linear_fp8_many(const LinearArgs& a, const void* W8, int64_t l
     if (e != hipSuccess) return e;
     // The decode kernel over groups of 64 tokens while one round of its units
     // (32 columns a group) is enough and K is long enough for eight wavefronts
-    // to share: 65 tokens, 4096 x 4096 22.0 against 24.9 us with small units, K =
-    // 8192 and 512 tokens to 1024 columns 30.9 / 36.9; K = 1024 16.5 / 13.5.
+    // to share.  Measured, small units of the product against groups, with 24
+    // adapters (segments follow each other in a unit of the product, in a group the
+    // eight wavefronts share them), 8, and none: 65 tokens, 2048 columns, K = 2048 31.6 /
+    // 19.0 us, -, 11.4 / 11.9, K = 4096 41.5 / 22.6, -, 16.3 / 12.0; 128 tokens, 4096
+    // columns, K = 1024 -, 14.9 / 18.2, -, K = 2048 25.7 / 21.0, 17.5 / 18.8, 11.5 / 13.6, K
+    // = 4096 36.0 / 25.7, 26.0 / 22.6, 17.6 / 15.6; 512 tokens, 1024 columns, 8 adapters, K =
+    // 2048 16.0 / 20.3, 4096 23.4 / 23.4, 8192 36.6 / 31.6.
     const int64_t units = (a.M + 63) / 64 * ((a.slice_off[a.n_sl] + 31) / 32);
     if (units <= 256 && a.K >= 2048 && ldx8 < INT32_MAX / (int64_t)a.M)
         return launch_linear_fp8_groups(a, W8, ldw, w_scale, x8, ldx8, x_scale, S, y, ldy, st);

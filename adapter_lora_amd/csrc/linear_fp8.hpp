@@ -634,12 +634,21 @@ hipError_t launch_linear_fp8(const LinearArgs& a, const void* W8, int64_t ldw, c
     p.slots = reinterpret_cast<slot_t*>(static_cast<char*>(ws) + linear_ws_layout(0, a.K, a.cols).slots);
     p.wc = wait_ctl();
     // A unit reads every token row once: twice the columns halve that and the
-    // units.  Measured, 16 against 32 columns, K = 4096: N = 8192 1 token 12.0 /
-    // 10.6 us, 32 tokens 18.9 / 16.5, 64 25.3 / 23.6; N = 28672 32.8 / 27.7, 53.0 /
-    // 41.8, 73.3 / 72.0; N = 6144 10.4 / 9.2, 20.6 / 24.2, 28.6 / 28.3; N = 4096
-    // 8.0 / 8.4, 12.9 / 14.5, 16.9 / 21.6.
+    // units, which pays from the width where units of 32 keep enough compute units
+    // busy: for up to 16 tokens the later the longer K.  Measured, 16 against 32
+    // columns, one slice with 32 adapters, 1 / 16 tokens: K = 512, N = 2048 6.1 / 6.2 and
+    // 7.2 / 7.2 us, 4096 7.2 / 6.4 and 8.3 / 7.5; K = 2048, N = 4096 8.2 / 7.0 and 9.5 / 8.5,
+    // 14336 17.3 / 10.9 and 21.1 / 15.0; K = 4096, N = 4096 8.9 / 9.5 and 10.8 / 11.5, 6144
+    // 10.9 / 9.7 and 13.2 / 12.8, 28672 34.8 / 28.7 and 42.7 / 34.5; K = 8192, N = 6144 14.7 /
+    // 14.8 and 18.1 / 19.5, 8192 18.2 / 19.5 and 21.8 / 22.8, 14336 26.6 / 27.0 and 33.9 / 33.2.
+    // For more tokens the deltas count: 32 and 64 tokens, N = 6144, K = 4096, one slice 18.9
+    // / 16.7 and 24.0 / 23.0, three slices 21.4 / 25.4 and 26.9 / 29.4, without adapters 12.2 /
+    // 10.2 and 16.2 / 14.0; N = 8192 20.0 / 17.6 and 25.7 / 24.1, 25.6 / 26.6 and 31.3 / 39.0,
+    // 12.9 / 11.2 and 16.9 / 15.2 (K = 512 to 8192 alike); one slice, N = 4096 13.5 / 16.0 and
+    // 17.0 / 22.3, 28672 52.3 / 45.2 and 70.6 / 73.5.
     const int64_t units = a.slice_off[a.n_sl] / 32;
-    const bool wide = units >= (a.M <= 16 ? 192 : 256);
+    const int64_t few = a.K <= 2048 ? 128 : a.K < 8192 ? 192 : 448;
+    const bool wide = units >= (a.M <= 16 ? few : 256);
     if (a.M <= 16) return wide ? launch_linear_fp8_as<1, 2>(p, st) : launch_linear_fp8_as<1, 1>(p, st);
     if (a.M <= 32) return wide ? launch_linear_fp8_as<2, 2>(p, st) : launch_linear_fp8_as<2, 1>(p, st);
     return wide ? launch_linear_fp8_as<4, 2>(p, st) : launch_linear_fp8_as<4, 1>(p, st);
