@@ -5,7 +5,9 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_linear_fp8 import F64, Case
+from tests.test_gpu_linear_fp8 import E4M3, F64, Case
+from tests.test_gpu_moe_decode import Layer
+from tests.test_gpu_rms_norm import draw
 
 pytestmark = pytest.mark.gpu
 
@@ -121,3 +123,44 @@ def test_every_form_matches_oracle(name):
     c.check(y)
     torch.cuda.synchronize()
     assert torch.equal(y, c.run())
+
+
+# More units (groups of an expert's tokens times 16 inner columns) than the first
+# launch has consumers (768), so that each walks to other experts, rows and tokens
+UNITS = {
+    "few_tokens_fp8": dict(M=8, E=3, topk=2, H=48, I=6160, L=3, r=16, w8=True),
+    "few_tokens": dict(M=5, E=4, topk=3, H=200, I=3208, L=2, r=48),
+    "to_sixteen": dict(M=14, E=2, topk=2, H=136, I=8200, L=3, r=32),
+    "to_sixteen_fp8": dict(M=16, E=2, topk=2, H=272, I=7184, L=2, r=16, w8=True, renorm=True),
+    "many_experts_fp8": dict(M=27, E=12, topk=3, H=144, I=3216, L=4, r=32, w8=True),
+    "some_experts": dict(M=20, E=4, topk=1, H=72, I=4104, L=3, r=16),
+    "busy_experts_fp8": dict(M=40, E=4, topk=2, H=144, I=4112, L=5, r=16, w8=True),
+    "two_groups_each": dict(M=64, E=4, topk=3, H=72, I=4104, L=4, r=16),
+    "two_groups_each_fp8": dict(M=64, E=3, topk=2, H=80, I=4112, L=4, r=16, w8=True, renorm=True),
+    "s_past_lds": dict(M=32, E=9, topk=3, H=72, I=2056, L=6, r=64),
+    "s_past_lds_fp8": dict(M=48, E=9, topk=3, H=80, I=2064, L=6, r=64, w8=True),
+    "s_past_lds_to_sixteen": dict(M=16, E=16, topk=8, H=72, I=1000, L=4, r=48),
+    "shared_outer": dict(M=33, E=8, topk=2, H=80, I=1608, L=3, r=32, shared=True),
+    "long_rows_fp8": dict(M=27, E=10, topk=4, H=2064, I=1424, L=6, r=32, w8=True, renorm=True),
+}
+
+
+@pytest.mark.parametrize("name", list(UNITS))
+def test_moe_several_units_a_consumer(name):
+    print(name, flush=True)
+    layer = Layer(**UNITS[name], seed=len(name))
+    out = layer.run()
+    layer.check(out)
+    chosen = torch.bincount(layer.topk_ids.flatten().long(), minlength=layer.E)
+    groups = int(((chosen + 31) // 32).sum())
+    assert groups * ((layer.I + 15) // 16) > 768
+    torch.cuda.synchronize()
+    assert torch.equal(out, layer.run())
+
+
+@pytest.mark.parametrize("kw", [dict(M=2, E=2, topk=1, H=24592, I=40, L=2), dict(M=33, E=2, topk=1, H=16400, I=48, L=2, w8=True)])
+def test_moe_one_split(kw):
+    """So many output columns that one workgroup has each tile of them alone."""
+    print(kw, flush=True)
+    layer = Layer(**kw)
+    layer.check(layer.run())
