@@ -164,3 +164,71 @@ def test_moe_one_split(kw):
     print(kw, flush=True)
     layer = Layer(**kw)
     layer.check(layer.run())
+
+
+@pytest.mark.parametrize("w8", [False, True])
+def test_last_expert_past_32_bit_offsets_in_each_matrix(w8):
+    """Every token goes to the last expert, which starts past 2^32 bytes in W_gu
+    and in W_d alike; its output has the bits of a layer that holds it alone
+    (renormalized, so the routing weight is 1 in both)."""
+    import adapter_lora_amd as ml
+    E, H, I = 120 if w8 else 60, 4096, 9568
+    small = Layer(M=5, E=1, topk=1, H=H, I=I, L=0, renorm=True, w8=w8)
+    dt = torch.uint8 if w8 else torch.bfloat16
+    W_gu = torch.zeros(E, 2 * I, H, dtype=dt, device="cuda")
+    W_d = torch.zeros(E, H, I, dtype=dt, device="cuda")
+    for big, one in ((W_gu, small.W_gu), (W_d, small.W_d)):
+        big[E - 1] = one[0].view(dt)
+        assert big.stride(0) * big.element_size() * (E - 1) >= 1 << 32
+    s_gu = s_d = None
+    if w8:
+        W_gu, W_d = W_gu.view(E4M3), W_d.view(E4M3)
+        s_gu, s_d = torch.zeros(E, 2 * I, device="cuda"), torch.zeros(E, H, device="cuda")
+        s_gu[E - 1], s_d[E - 1] = small.s_gu[0], small.s_d[0]
+    router = torch.zeros(E, H, dtype=torch.bfloat16, device="cuda")
+    router[:E - 1, 0] = -1000.0
+    x = small.x
+    x[:, 0] = 1.0
+    want = small.run()
+    ex = ml.MoeExperts(router, W_gu, W_d, 1, renormalize=True, s_gu=s_gu, s_d=s_d)
+    ws = ml.Workspace(ml.lora_moe_decode_workspace_size(None, ex, 5))
+    out = torch.empty_like(want)
+    ids = torch.empty(5, 1, dtype=torch.int32, device="cuda")
+    ml.lora_moe_decode(None, ex, None, x, out, ws, topk_ids=ids)
+    torch.cuda.synchronize()
+    assert (ids == E - 1).all() and torch.equal(out, want)
+    assert out.float().abs().max() > 0
+
+
+@pytest.mark.parametrize("M,K", [(1, 512), (37, 4096), (5, 14336)])
+def test_norm_and_quantization_captured_and_replayed(M, K):
+    """Captured once, replayed with new inputs and eager work between."""
+    import adapter_lora_amd as ml
+    x, res, w = (draw(m, K, torch.bfloat16, i) for i, m in enumerate((M, M, 1)))
+    other = [(draw(M, K, torch.bfloat16, 10 + i), draw(M, K, torch.bfloat16, 20 + i, 3.0)) for i in range(5)]
+
+    def outputs():
+        e8 = lambda: torch.zeros(M, K, dtype=E4M3, device="cuda")     # noqa: E731
+        return [torch.zeros_like(x), torch.zeros_like(x), e8(), torch.zeros(M, device="cuda"), e8(),
+                torch.zeros(M, device="cuda")]
+
+    def run(o):
+        ml.lora_rms_norm(x, w[0], 1e-5, residual=res, residual_out=o[0], out=o[1], out8=o[2], scale=o[3])
+        ml.lora_quantize_rows(o[1], o[4], o[5])
+
+    got, eager = outputs(), outputs()
+    run(eager)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(got)
+    for a, b in other:
+        x.copy_(a), res.copy_(b)
+        for t in got:
+            t.view(torch.uint8).zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        run(eager)
+        torch.cuda.synchronize()
+        assert all(torch.equal(s.view(torch.uint8), t.view(torch.uint8)) for s, t in zip(got, eager))
+        assert got[1].float().abs().max() > 0
