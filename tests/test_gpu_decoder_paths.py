@@ -5,9 +5,10 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import decoder as O
 from tests.test_gpu_linear_fp8 import E4M3, F64, Case
 from tests.test_gpu_moe_decode import Layer
-from tests.test_gpu_rms_norm import draw
+from tests.test_gpu_rms_norm import draw, near
 
 pytestmark = pytest.mark.gpu
 
@@ -232,3 +233,23 @@ def test_norm_and_quantization_captured_and_replayed(M, K):
         torch.cuda.synchronize()
         assert all(torch.equal(s.view(torch.uint8), t.view(torch.uint8)) for s, t in zip(got, eager))
         assert got[1].float().abs().max() > 0
+
+
+@pytest.mark.parametrize("K,lane,waves", [(64, 8, 1), (512, 8, 1), (1024, 8, 2), (4096, 8, 8), (8192, 8, 16),
+                                          (16384, 16, 16), (32768, 32, 16)])
+def test_norm_fp32_within_its_count_of_roundings(K, lane, waves):
+    """In units of u = 2^-24: a lane adds `lane` squares one after the other, six
+    additions join a wavefront's lanes and `waves` the wavefronts; with a
+    square's own rounding, those of h = x + residual (once in each factor), of
+    the mean and of the added eps, the sum is off by lane + waves + 11 u, its
+    square root by half of that; the root, the reciprocal, the two products
+    and h add one each, the stored fp32 value is the last product itself."""
+    import adapter_lora_amd as ml
+    x, res = draw(33, K, torch.float32, 1), draw(33, K, torch.float32, 2, 3.0)
+    w = (1 + 0.1 * draw(1, K, torch.float32, 3)[0])
+    out, res_out = torch.empty_like(x), torch.empty_like(x)
+    ml.lora_rms_norm(x, w, 1e-5, residual=res, residual_out=res_out, out=out)
+    h, v = O.rms_norm(F64(x), F64(w), 1e-5, F64(res))
+    near(F64(res_out), h, 2.0 ** -24, what="residual")
+    # a sum near zero has lost nothing: it is one rounding of the exact value
+    near(F64(out), v, ((lane + waves + 11) / 2 + 5) * 2.0 ** -24 * 1.001, what="out")
