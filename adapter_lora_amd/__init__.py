@@ -556,26 +556,54 @@ E4M3 = torch.float8_e4m3fn
 _F32 = torch.float32
 
 
-def _scales(t: torch.Tensor, name: str, n: int) -> int:
+def _elsewhere(name: str, on: int, dev: int) -> LoraError:
+    if on < 0 or dev < 0:
+        return LoraError(f"{name if on < 0 else 'x'} must live on the GPU")
+    return LoraError(f"{name} lives on device {on}, x on device {dev}")
+
+
+def _together(dev: int, **named) -> None:
+    """What a call's plan, workspace and other buffers are made of lives on the
+    device of x."""
+    for name, t in named.items():
+        if t is not None and t.get_device() != dev:
+            raise _elsewhere(name, t.get_device(), dev)
+
+
+def _stream_on(dev: int, stream) -> int:
+    """hipStream_t of a call on operands of device `dev`."""
+    if stream is not None:
+        on, handle = stream.device_index, stream.cuda_stream
+    else:
+        on = _cur_device() if _cur_device is not None else torch.cuda.current_device()
+        handle = stream_handle() if on == dev else 0
+    if on != dev:
+        raise LoraError(f"x lives on device {dev}, the call's stream on device {on}")
+    return handle
+
+
+def _scales(t: torch.Tensor, name: str, n: int, dev: int) -> int:
     """Device address of one fp32 scale per row of an 8-bit tensor."""
     if t.dtype is not _F32 or t.numel() < n or not t.is_contiguous():
         raise LoraError(f"{name} must be contiguous fp32 with {n} values")
-    if not t.is_cuda:
-        raise LoraError(f"{name} must live on the GPU")
+    on = t.get_device()
+    if on != dev or on < 0:
+        raise _elsewhere(name, on, dev)
     return t.data_ptr()
 
 
-def _matrix(t: Optional[torch.Tensor], name: str, shape, dtype):
-    """(address, leading dimension) of a row-major 2-D device operand of
-    exactly this shape and dtype; zeros for None."""
+def _matrix(t: Optional[torch.Tensor], name: str, shape, dtype, dev: int):
+    """(address, leading dimension) of a row-major 2-D operand of exactly this
+    shape and dtype on device `dev`; zeros for None."""
     if t is None:
         return 0, 0
     if t.dtype is not dtype:
         raise LoraError(f"{name} is {t.dtype} but must be {dtype}")
     if t.shape != shape:
         raise LoraError(f"{name} must be a tensor of shape {tuple(shape)}, not {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise LoraError(f"{name} must live on the GPU")
+    on = t.get_device()
+    if on != dev or on < 0:
+        raise _elsewhere(name, on, dev)
     if t.is_contiguous():
         return t.data_ptr(), shape[1]
     if t.stride(1) != 1 and t.numel() > 0:
@@ -606,16 +634,17 @@ def lora_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
         raise LoraError("residual_out needs a residual")
     if weight.dtype != dtype or weight.shape != (K,) or not weight.is_contiguous():
         raise LoraError(f"weight must be a contiguous {dtype} vector of {K} values")
-    pr, ldr = _matrix(residual, "residual", shape, dtype)
-    pro, ldro = _matrix(residual_out, "residual_out", shape, dtype)
-    po, ldo = _matrix(out, "out", shape, dtype)
-    po8, ldo8 = _matrix(out8, "out8", shape, E4M3)
-    px, ldx = _matrix(x, "x", shape, dtype)
-    if not weight.is_cuda:
-        raise LoraError("weight must live on the GPU")
+    dev = x.get_device()
+    pr, ldr = _matrix(residual, "residual", shape, dtype, dev)
+    pro, ldro = _matrix(residual_out, "residual_out", shape, dtype, dev)
+    po, ldo = _matrix(out, "out", shape, dtype, dev)
+    po8, ldo8 = _matrix(out8, "out8", shape, E4M3, dev)
+    px, ldx = _matrix(x, "x", shape, dtype, dev)
+    if weight.get_device() != dev:
+        raise _elsewhere("weight", weight.get_device(), dev)
     check(lib.lora_rms_norm(code, px, ldx, pr, ldr, weight.data_ptr(), eps, M, K, pro, ldro, po,
-                            ldo, po8, ldo8, 0 if scale is None else _scales(scale, "scale", M),
-                            stream_handle(stream)), "lora_rms_norm")
+                            ldo, po8, ldo8, 0 if scale is None else _scales(scale, "scale", M, dev),
+                            _stream_on(dev, stream)), "lora_rms_norm")
 
 
 def lora_quantize_rows(x: torch.Tensor, out8: torch.Tensor, scale: torch.Tensor,
@@ -624,11 +653,11 @@ def lora_quantize_rows(x: torch.Tensor, out8: torch.Tensor, scale: torch.Tensor,
     shape = x.shape
     if len(shape) != 2:
         raise LoraError("x must be a 2-D tensor")
-    code = _dtype_code(x.dtype)
-    po8, ldo8 = _matrix(out8, "out8", shape, E4M3)
-    px, ldx = _matrix(x, "x", shape, x.dtype)
+    code, dev = _dtype_code(x.dtype), x.get_device()
+    po8, ldo8 = _matrix(out8, "out8", shape, E4M3, dev)
+    px, ldx = _matrix(x, "x", shape, x.dtype, dev)
     check(lib.lora_quantize_rows(code, px, ldx, shape[0], shape[1], po8, ldo8,
-                                 _scales(scale, "scale", shape[0]), stream_handle(stream)),
+                                 _scales(scale, "scale", shape[0], dev), _stream_on(dev, stream)),
           "lora_quantize_rows")
 
 
@@ -648,16 +677,17 @@ def lora_linear_fp8(table: LoraTable, W8: torch.Tensor, w_scale: torch.Tensor, x
             raise LoraError("x, x8 and y must have the same number of rows")
         if W8.shape[0] != N:
             raise LoraError("W8 must have one row per output column of the table")
-    M = shape[0]
-    pw, ldw = _matrix(W8, "W8", (N, K), E4M3)
-    px8, ldx8 = _matrix(x8, "x8", shape, E4M3)
-    px, ldx = _matrix(x, "x", (M, K), dtype)
-    py, ldy = _matrix(y, "y", y.shape, dtype)
-    pws, pxs = _scales(w_scale, "w_scale", N), _scales(x_scale, "x_scale", M)
+    M, dev = shape[0], x.get_device()
+    pw, ldw = _matrix(W8, "W8", (N, K), E4M3, dev)
+    px8, ldx8 = _matrix(x8, "x8", shape, E4M3, dev)
+    px, ldx = _matrix(x, "x", (M, K), dtype, dev)
+    py, ldy = _matrix(y, "y", y.shape, dtype, dev)
+    pws, pxs = _scales(w_scale, "w_scale", N, dev), _scales(x_scale, "x_scale", M, dev)
     if seg.L != table.L or M > seg.sorted_idx.shape[0]:
         raise LoraError("segment buffers do not match the table or the batch")
+    _together(dev, table=table.A_table, segments=seg.sorted_idx, workspace=ws.buf)
     check(lib.lora_linear_fp8(table.ref, pw, ldw, pws, px8, ldx8, pxs, px, ldx, M, seg.ref, py, ldy,
-                              ws.ptr, ws.nbytes, stream_handle(stream)), "lora_linear_fp8")
+                              ws.ptr, ws.nbytes, _stream_on(dev, stream)), "lora_linear_fp8")
 
 
 class MoeExperts:
@@ -685,6 +715,8 @@ class MoeExperts:
                      ("s_d", s_d)):
             if t is not None and not t.is_cuda:
                 raise LoraError(f"{n} must live on the GPU")
+            if t is not None and t.get_device() != router.get_device():
+                raise LoraError(f"{n} lives on another device than the router")
         self.router, self.W_gu, self.W_d = router.contiguous(), W_gu.contiguous(), W_d.contiguous()
         self.s_gu = self.s_d = None
         if eight:
@@ -727,7 +759,11 @@ def lora_moe_decode(w: Optional[MoeWeights], experts: MoeExperts, ids: Optional[
         if t is not None and (t.dtype != dt or tuple(t.shape) != (M, experts.topk)
                               or not t.is_contiguous() or not t.is_cuda):
             raise LoraError(f"{n} must be a contiguous {dt} device tensor [M, topk]")
+    dev = x.get_device()
+    _together(dev, out=out, ids=ids if w is not None else None, topk_ids=topk_ids,
+              topk_weights=topk_weights, experts=experts.router, workspace=ws.buf,
+              adapters=None if w is None else w.A_gu)
     check(lib.lora_moe_decode(ctypes.byref(w.c) if w is not None else None, experts.ref,
                               _ptr(ids), _ptr(x), ldx, M, _ptr(out), ldo, _ptr(topk_ids),
-                              _ptr(topk_weights), ws.ptr, ws.nbytes, stream_handle(stream)),
+                              _ptr(topk_weights), ws.ptr, ws.nbytes, _stream_on(dev, stream)),
           "lora_moe_decode")

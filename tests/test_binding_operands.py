@@ -1,6 +1,7 @@
 """Operands that the binding has to refuse before a launch: rows that overlap
-(broadcast or strided by less than their width).  Tensors in host memory stand
-in for device ones, so nothing here needs a GPU."""
+(broadcast or strided by less than their width), and operands on another device
+than the call.  Tensors in host memory stand in for device ones, so nothing here
+needs a GPU."""
 import pytest
 import torch
 
@@ -40,6 +41,7 @@ def no_launch(monkeypatch):
                  "lora_moe_topk_reduce"):
         monkeypatch.setattr(ml.lib, name, launched)
     monkeypatch.setattr(ml, "stream_handle", lambda stream=None: 0)
+    monkeypatch.setattr(ml, "_cur_device", lambda: 0)
 
 
 @pytest.mark.parametrize("i", range(3))
@@ -49,7 +51,7 @@ def test_overlapping_rows_are_refused(i):
     bad, bad8 = overlapping(M, K)[i], overlapping(M, K, torch.uint8)[i].view(E4M3).as_subclass(OnGpu)
     tb = type("T", (), dict(dtype=BF, K=K, N=N, L=4, cols=16, ref=None))()
     seg = type("S", (), dict(L=4, sorted_idx=z(M, dtype=torch.int32), ref=None))()
-    ws = type("W", (), dict(ptr=0, nbytes=0))()
+    ws = type("W", (), dict(ptr=0, nbytes=0, buf=z(8)))()
     W8, sn, y = z(N, K, dtype=E4M3), z(N, dtype=torch.float32), z(M, N)
     ex = type("X", (), dict(H=K, topk=2, ref=None))()
     calls = [lambda: ml.lora_rms_norm(bad, w, out=x),
@@ -80,5 +82,59 @@ def test_rows_that_do_not_overlap_keep_their_stride():
     none = dev(torch.zeros(64).as_strided((0, 64), (3, 1)))
     wide = dev(torch.zeros(4, 96)[:, 16:80])
     for t, ld in ((one, 64), (none, 64), (wide, 96)):
-        assert ml._matrix(t, "x", t.shape, torch.float32)[1] == ld
+        assert ml._matrix(t, "x", t.shape, torch.float32, 0)[1] == ld
         assert ml._rows(t, "x") == ld
+
+
+class OnOther(OnGpu):
+    """A host tensor that says it lives on device 1."""
+    def get_device(self):
+        return 1
+
+
+def calls_of(op):
+    """The call with its operands by name, and the names that are tensors or hold them."""
+    M, K, N = 4, 64, 64
+    x, x8, s = z(M, K), z(M, K, dtype=E4M3), z(M, dtype=torch.float32)
+    ws = lambda t: type("W", (), dict(ptr=0, nbytes=0, buf=t))()                                 # noqa: E731
+    if op == "norm":
+        return ml.lora_rms_norm, dict(x=x, weight=z(K), residual=x, residual_out=z(M, K), out=z(M, K), out8=x8, scale=s)
+    if op == "quantize":
+        return ml.lora_quantize_rows, dict(x=x, out8=x8, scale=s)
+    if op == "linear":
+        tb = lambda t: type("T", (), dict(dtype=BF, K=K, N=N, L=4, cols=16, ref=None, A_table=t))()  # noqa: E731
+        seg = lambda t: type("S", (), dict(L=4, sorted_idx=t, ref=None))()                      # noqa: E731
+        return ml.lora_linear_fp8, dict(table=(tb, z(8)), W8=z(N, K, dtype=E4M3), w_scale=z(N, dtype=torch.float32),
+                                        x8=x8, x_scale=s, x=x, seg=(seg, z(M, dtype=torch.int32)), y=z(M, N),
+                                        ws=(ws, z(8)))
+    ex = lambda t: type("X", (), dict(H=K, topk=2, ref=None, router=t))()                       # noqa: E731
+    w = lambda t: type("M", (), dict(c=ml.lora_moe_weights_t(), A_gu=t))()                      # noqa: E731
+    return ml.lora_moe_decode, dict(w=(w, z(8)), experts=(ex, z(8)), ids=z(M, dtype=torch.int32), x=x, out=z(M, K),
+                                    ws=(ws, z(8)), topk_ids=z(M, 2, dtype=torch.int32),
+                                    topk_weights=z(M, 2, dtype=torch.float32))
+
+
+@pytest.mark.parametrize("op", ["norm", "quantize", "linear", "moe"])
+def test_operands_of_another_device_are_refused(op, monkeypatch):
+    call, args = calls_of(op)
+    real = lambda a: {k: v[0](v[1]) if isinstance(v, tuple) else v for k, v in a.items()}       # noqa: E731
+    reached = []
+    monkeypatch.setattr(ml.lib, call.__name__, lambda *a: reached.append(a) or 0)
+    call(**real(args))
+    assert len(reached) == 1                                     # one device: the call goes through
+    for k, v in args.items():
+        holder = isinstance(v, tuple)
+        for t in ((v[1] if holder else v).as_subclass(OnOther), (v[1] if holder else v).as_subclass(torch.Tensor)):
+            with pytest.raises(ml.LoraError, match="device|GPU"):
+                call(**real(dict(args, **{k: (v[0], t) if holder else t})))
+    # all together on a device that is not the call's
+    other = {k: (v[0], v[1].as_subclass(OnOther)) if isinstance(v, tuple) else v.as_subclass(OnOther)
+             for k, v in args.items()}
+    with pytest.raises(ml.LoraError, match="stream on device 0"):
+        call(**real(other))
+    stream = type("St", (), dict(device_index=1, cuda_stream=0))()
+    with pytest.raises(ml.LoraError, match="stream on device 1"):
+        call(**real(args), stream=stream)
+    assert len(reached) == 1
+    call(**real(other), stream=stream)
+    assert len(reached) == 2
