@@ -441,6 +441,18 @@ class MoeWeights:
     [L, 1, H, r]) are recognised from their single expert slot."""
 
     def __init__(self, A_gu, B_gu, A_d, B_d, adapter_enabled):
+        stacks = dict(A_gu=A_gu, B_gu=B_gu, A_d=A_d, B_d=B_d)
+        if any(t.dtype != A_gu.dtype for t in stacks.values()):
+            raise LoraError("the MoE LoRA stacks must be of one type")
+        for name, t in dict(stacks, adapter_enabled=adapter_enabled).items():
+            if not t.is_cuda:
+                raise LoraError(f"{name} must live on the GPU")
+            if t.get_device() != A_gu.get_device():
+                raise LoraError(f"{name} lives on another device than A_gu")
+        if any(t.dim() != 4 for t in stacks.values()):
+            raise LoraError("inconsistent MoE LoRA shapes")
+        if adapter_enabled.numel() < B_gu.shape[0]:
+            raise LoraError("adapter_enabled must have an entry for every adapter")
         self.A_gu, self.B_gu = A_gu.contiguous(), B_gu.contiguous()
         self.A_d, self.B_d = A_d.contiguous(), B_d.contiguous()
         self.enabled = adapter_enabled.to(torch.int32).contiguous()
@@ -449,7 +461,7 @@ class MoeWeights:
         H = self.A_gu.shape[3]
         eo = self.A_gu.shape[1]
         self.shared_outer = eo == 1 and E > 1
-        if tuple(self.A_gu.shape) != (L, eo, r, H) or eo not in (1, E) \
+        if tuple(self.A_gu.shape) != (L, eo, r, H) or eo not in (1, E) or I2 != 2 * I \
                 or tuple(self.A_d.shape) != (L, E, r, I) or tuple(self.B_d.shape) != (L, eo, H, r):
             raise LoraError("inconsistent MoE LoRA shapes")
         self.L, self.E, self.r, self.H, self.I = L, E, r, H, I

@@ -138,3 +138,22 @@ def test_operands_of_another_device_are_refused(op, monkeypatch):
     assert len(reached) == 1
     call(**real(other), stream=stream)
     assert len(reached) == 2
+
+
+def test_moe_adapters_of_mixed_types_places_or_a_short_mask_are_refused():
+    L, E, r, H, I = 3, 4, 16, 64, 32
+    shapes = [(L, E, r, H), (L, E, 2 * I, r), (L, E, r, I), (L, E, H, r)]
+    good = [z(*s) for s in shapes] + [z(L, dtype=torch.int32)]
+    w = ml.MoeWeights(*good)
+    assert (w.L, w.E, w.r, w.H, w.I, w.shared_outer) == (L, E, r, H, I, False)
+    for i in range(5):
+        for t in (good[i].as_subclass(OnOther), good[i].as_subclass(torch.Tensor)):
+            with pytest.raises(ml.LoraError, match="device|GPU"):
+                ml.MoeWeights(*good[:i], t, *good[i + 1:])
+    for i in range(4):
+        with pytest.raises(ml.LoraError, match="one type"):
+            ml.MoeWeights(*good[:i], good[i].float(), *good[i + 1:])
+    with pytest.raises(ml.LoraError, match="adapter_enabled"):
+        ml.MoeWeights(*good[:4], z(L - 1, dtype=torch.int32))
+    with pytest.raises(ml.LoraError, match="inconsistent"):
+        ml.MoeWeights(good[0], z(L, E, 2 * I + 1, r), *good[2:])
