@@ -584,14 +584,15 @@ def _together(dev: int, **named) -> None:
 
 def _stream_on(dev: int, stream) -> int:
     """hipStream_t of a call on operands of device `dev`."""
-    if stream is not None:
-        on, handle = stream.device_index, stream.cuda_stream
-    else:
+    if stream is None:
         on = _cur_device() if _cur_device is not None else torch.cuda.current_device()
-        handle = stream_handle() if on == dev else 0
-    if on != dev:
-        raise LoraError(f"x lives on device {dev}, the call's stream on device {on}")
-    return handle
+        if on == dev:
+            return _raw_stream(dev) if _raw_stream is not None else stream_handle()
+    else:
+        on = stream.device_index
+        if on == dev:
+            return stream.cuda_stream
+    raise LoraError(f"x lives on device {dev}, the call's stream on device {on}")
 
 
 def _scales(t: torch.Tensor, name: str, n: int, dev: int) -> int:

@@ -42,6 +42,7 @@ def no_launch(monkeypatch):
         monkeypatch.setattr(ml.lib, name, launched)
     monkeypatch.setattr(ml, "stream_handle", lambda stream=None: 0)
     monkeypatch.setattr(ml, "_cur_device", lambda: 0)
+    monkeypatch.setattr(ml, "_raw_stream", lambda device: 0)
 
 
 @pytest.mark.parametrize("i", range(3))
