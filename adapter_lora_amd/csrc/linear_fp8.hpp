@@ -195,7 +195,9 @@ __device__ __forceinline__ void fp8_producer(const Fp8Params& p, uint32_t tag, u
 // SLOTS: up to 64 tokens, producers in the same launch.  Otherwise S is read
 // from memory (p.S, an earlier launch's), and a consumer takes the columns'
 // product for one group of 64 sorted positions; the groups of a column tile
-// follow each other on one L2 (every eighth workgroup).
+// follow each other on one L2 (every eighth workgroup).  With TB = 4 and NR = 1 the
+// 128 registers are full: one value (SLOTS) or six are spilled across the loop over K,
+// none within it.
 template <int TB, int NR, bool SLOTS>
 __global__ __launch_bounds__(kFpThreads, TB * NR == 8 ? 2 : 4) void k_linear_fp8(Fp8Params p) {
     constexpr int kStage = fp8_stage(TB, NR);

@@ -22,8 +22,8 @@
 // bf16 80 and 41 us (5.9 and 5.7 TB/s of expert rows; a large copy reaches 5.1
 // with its writes); 64 tokens, all 8 of them 331 and 171 (5.7, 5.5); 27 tokens, 4
 // of 40 experts of 2064 x 1424 in 8 bits 72 and 44 (3.0, 2.5): there the stream
-// runs at 6 TB/s as well, between 12 us in which the router works and every
-// workgroup makes its tables, 6 until the first loads, and a ragged end.
+// runs at 6 TB/s as well, between 12 us in which the router works (9 as a launch of its
+// own) and every workgroup makes its tables, 6 until the first loads, and a ragged end.
 // Results cross workgroups of a launch through tagged exchange slots
 // (common.hpp); whoever waits comes later in the grid than whom it waits for,
 // and every wait is bounded.
@@ -638,7 +638,9 @@ __device__ __forceinline__ void md_gate_up(const MoeDecodeParams& p, const MdRou
 // 128 experts in 8 bits 127 / 104 us a layer, 27 tokens, top 4 of 40 130 / 116, 1
 // token, 2 of 8 experts in bf16 128 / 125).  Kernels of their own for few tokens
 // spare those the registers of the widest (12 tokens of 8 experts 227 to 238 us,
-// from one kernel for all 239).
+// from one kernel for all 239).  The widest, XPM = 4, fills its 168 registers: five or
+// six values are spilled before the units and read back after them (one or two once a
+// unit), 70 to 80 scalar ones go to lanes of vector registers.
 template <bool W8, int XPM>
 __global__ __launch_bounds__(kMdThreads, 3) void k_moe_gate_up(MoeDecodeParams p, int shrinks) {
     __shared__ uint4 smem[kMdWaves * kMdStage];

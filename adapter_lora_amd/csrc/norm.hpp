@@ -15,7 +15,7 @@
 // unrounded v or h.
 //
 // What bounds it: every operand crosses HBM once.  2048 rows of 4096 in bf16
-// with the residual and all outputs 16.4 us (75.5 MB, 4.6 TB/s; a large copy
+// with the residual and all outputs 16.3 us (75.5 MB, 4.6 TB/s; a large copy
 // reaches 5.1), 4099 rows of 5128 in fp32 to fp32 37.4 (168 MB, 4.5), a weight of
 // 28672 x 4096 to 8 bits 72.9 (352 MB, 4.8; 84 with the norm's branches in the same
 // kernel and clamps before the conversion: the arithmetic of a value counts). 32
@@ -174,9 +174,12 @@ hipError_t launch_norm_as(const NormParams& p, hipStream_t st) {
 }
 
 // A row is spread over as many wavefronts as have work: its loads are all in
-// flight at once, in few registers.  Measured against rows of one wavefront (two
-// to eight past K = 4096): 32 x 4096 3.7 / 11.8 us, 2048 x 4096 19.6 / 25.5, 64 x
-// 14336 6.8 / 11.9; against half the wavefronts: 4.8, 20.7 and 8.0.
+// flight at once, in few registers.  Measured against one wavefront (four past K =
+// 4096) and against half the wavefronts, in a graph over twelve inputs in turn, each
+// with all outputs (colder than the trace's 16.3 us for the second): 32 x 4096 4.2 / 10.4
+// / 4.9 us, 2048 x 4096 19.7 / 24.3 / 19.8, 64 x 14336 7.3 / 12.4 / 8.6, 2048 x 14336 58.0 /
+// 64.8 / 59.1; to 8 bits alone 3.3 / 4.6 / 3.4, 8.8 / 10.1 / 8.3, 3.8 / 4.7 / 3.9, 20.1 / 21.7 /
+// 20.5.
 template <typename T>
 hipError_t launch_norm_t(const NormParams& p, hipStream_t st) {
     const int chunks = (p.K + 511) / 512;        // 512 values per wavefront and chunk

@@ -544,7 +544,8 @@ lora_status lora_moe_topk_reduce(int32_t dtype, const void* cache3, int64_t ld3,
  *     scale[m]        = max|v| / 448
  *     out8[m]         = v / scale[m]                  rounded to e4m3 (nearest even)
  * (the sum of squares is fp32: values up to about 1e18).
- * A row of zeros has scale 1; a scale is at least 2^-126.  A NaN in v makes
+ * A row of zeros has scale 1 (with eps = 0 the norm makes it NaN, 0 / 0); a scale is at
+ * least 2^-126.  A NaN in v makes
  * its row's scale NaN and with it the whole row of out8; an infinity makes the
  * scale infinite and its own value NaN, the row's others 0.
  *   x, weight [K], residual, residual_out, out: dtype (LORA_BF16, LORA_F32);
@@ -624,7 +625,8 @@ typedef struct lora_moe_experts {
  * Bytes of device workspace of lora_moe_decode for up to M tokens (0: invalid
  * arguments): zero it once (lora_workspace_init) before its first use, order
  * the calls that share it on one stream.  Layers of the same E, H, I, topk and
- * r may share one, with any M up to its own.  w may be NULL.
+ * r may share one, with any M up to its own.  w may be NULL (r counts as 0 then: calls
+ * with and without adapters do not share a workspace).
  */
 size_t lora_moe_decode_workspace_size(const lora_moe_weights_t* w, const lora_moe_experts_t* ex,
                                       int32_t M);
@@ -639,7 +641,8 @@ size_t lora_moe_decode_workspace_size(const lora_moe_weights_t* w, const lora_mo
  *     h      = c silu(g) u                               rounded to bf16
  *     out[m] = sum over the chosen e of W_d[e] h + B_d[l, e] (A_d[l, e] h)
  * with l = ids[m]; a token whose id lies outside [0, L) or whose adapter is
- * disabled gets no deltas.  Nothing is rounded between but h.
+ * disabled gets no deltas.  Between, h is rounded to bf16 and A x and A h enter their
+ * products as the sum of two bf16 values (2^-17 of each); all else is fp32.
  *   w NULL: no adapters (ids is not read); else bf16, of the experts' E, H, I;
  *   ids device [M] int32; x device bf16 [M, ldx]; out device bf16 [M, ldo],
  *   overwritten; topk_ids device int32 [M, topk] and topk_weights device fp32
