@@ -89,19 +89,18 @@ def _rows(t: torch.Tensor, name: str) -> int:
         raise LoraError(f"{name} must be a 2-D tensor with unit column stride")
     if not t.is_cuda:
         raise LoraError(f"{name} must live on the GPU")
-    return _row_stride(t, name)
+    ld = t.stride(0)
+    return ld if ld >= t.shape[1] else _few_rows(t, name)
 
 
-def _row_stride(t: torch.Tensor, name: str) -> int:
-    """Distance of a tensor's rows; with less than two of them there is none,
-    and the width stands in.  Rows that overlap (broadcast ones are 0 apart)
-    have no leading dimension."""
-    ld, width = t.stride(0), t.shape[1]
-    if ld >= width:
-        return ld
+def _few_rows(t: torch.Tensor, name: str) -> int:
+    """Leading dimension where the rows' distance is less than their width:
+    with fewer than two rows there is no distance, and the width stands in.
+    More of them overlap (broadcast ones are 0 apart)."""
     if t.shape[0] > 1:
-        raise LoraError(f"the rows of {name} overlap: they are {ld} values apart and {width} wide")
-    return width
+        raise LoraError(f"the rows of {name} overlap: they are {t.stride(0)} values apart "
+                        f"and {t.shape[1]} wide")
+    return t.shape[1]
 
 
 # ------------------------------------------------------------------------- table
@@ -621,7 +620,8 @@ def _matrix(t: Optional[torch.Tensor], name: str, shape, dtype, dev: int):
         return t.data_ptr(), shape[1]
     if t.stride(1) != 1 and t.numel() > 0:
         raise LoraError(f"{name} must have unit column stride")
-    return t.data_ptr(), _row_stride(t, name)
+    ld = t.stride(0)
+    return t.data_ptr(), ld if ld >= shape[1] else _few_rows(t, name)
 
 
 def lora_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
