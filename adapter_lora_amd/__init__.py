@@ -13,17 +13,17 @@ from typing import List, Optional, Sequence
 
 import torch
 
-from ._abi import (LORA_BF16, LORA_E4M3, LORA_F32, LORA_MAX_ADAPTERS, LORA_MAX_RANK,
+from ._abi import (LORA_BF16, LORA_E4M3, LORA_F32, LORA_INT8, LORA_MAX_ADAPTERS, LORA_MAX_RANK,
                    LORA_MAX_SLICES, LORA_DECODE_MAX_M, LORA_TILE_ROWS, LORA_DEVERR_WAIT,
                    LORA_DEVERR_BAD_ID, LORA_DEVERR_TABLE, LoraError, lib, lora_weights_t,
                    lora_segments_t, lora_moe_weights_t, lora_moe_align_t,
                    lora_moe_experts_t, check)
 
 __all__ = [
-    "LORA_BF16", "LORA_E4M3", "LORA_F32", "LORA_DEVERR_WAIT", "LORA_DEVERR_BAD_ID",
+    "LORA_BF16", "LORA_E4M3", "LORA_F32", "LORA_INT8", "LORA_DEVERR_WAIT", "LORA_DEVERR_BAD_ID",
     "LORA_DEVERR_TABLE", "LoraError", "LoraTable",
     "Segments", "Workspace",
-    "MoeWeights", "MoeAlign", "MoeExperts",
+    "MoeWeights", "MoeAlign", "MoeExperts", "MoeGroups",
     "lora_build_segments", "lora_tile_capacity", "lora_shrink", "lora_expand_add",
     "lora_shrink_expand_add", "lora_fused_decode", "lora_fused_decode_noalloc",
     "lora_pack_embedding_adapter", "lora_embedding_shrink", "lora_embedding_decode",
@@ -32,6 +32,7 @@ __all__ = [
     "lora_moe_align_capacity", "lora_moe_align", "lora_moe_workspace_size",
     "lora_moe_gate_up_add", "lora_moe_silu_and_mul", "lora_moe_down_add",
     "lora_moe_topk_reduce", "lora_rms_norm", "lora_quantize_rows", "lora_linear_fp8",
+    "lora_linear_int8", "lora_moe_group", "lora_moe_linear",
     "lora_moe_decode_workspace_size", "lora_moe_decode", "stream_handle",
 ]
 
@@ -564,7 +565,7 @@ def lora_moe_topk_reduce(cache3: torch.Tensor, topk_weights: torch.Tensor, out: 
 E4M3 = torch.float8_e4m3fn
 
 
-_F32 = torch.float32
+_F32, _I8, _I32 = torch.float32, torch.int8, torch.int32
 
 
 def _elsewhere(name: str, on: int, dev: int) -> LoraError:
@@ -631,7 +632,8 @@ def lora_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
                   scale: Optional[torch.Tensor] = None, stream=None) -> None:
     """The residual's addition and the root-mean-square norm of x's rows:
     h = x + residual, residual_out = h, v = h * weight / sqrt(mean(h^2) + eps),
-    out = v, and in 8 bits out8 = v / scale with scale = max|v| / 448 per row.
+    out = v, and in 8 bits out8 = v / scale with scale = max|v| / 448 per row
+    (out8 of e4m3) or max|v| / 127 (out8 of int8).
     Each output is written when given; out or out8 (with scale) has to be.
     residual_out may be `residual` or `x` itself, `out` may be `x`."""
     shape, dtype = x.shape, x.dtype
@@ -651,35 +653,37 @@ def lora_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     pr, ldr = _matrix(residual, "residual", shape, dtype, dev)
     pro, ldro = _matrix(residual_out, "residual_out", shape, dtype, dev)
     po, ldo = _matrix(out, "out", shape, dtype, dev)
-    po8, ldo8 = _matrix(out8, "out8", shape, E4M3, dev)
+    int8 = out8 is not None and out8.dtype is _I8
+    po8, ldo8 = _matrix(out8, "out8", shape, _I8 if int8 else E4M3, dev)
     px, ldx = _matrix(x, "x", shape, dtype, dev)
     if weight.get_device() != dev:
         raise _elsewhere("weight", weight.get_device(), dev)
-    check(lib.lora_rms_norm(code, px, ldx, pr, ldr, weight.data_ptr(), eps, M, K, pro, ldro, po,
-                            ldo, po8, ldo8, 0 if scale is None else _scales(scale, "scale", M, dev),
-                            _stream_on(dev, stream)), "lora_rms_norm")
+    norm = lib.lora_rms_norm_int8 if int8 else lib.lora_rms_norm
+    check(norm(code, px, ldx, pr, ldr, weight.data_ptr(), eps, M, K, pro, ldro, po,
+               ldo, po8, ldo8, 0 if scale is None else _scales(scale, "scale", M, dev),
+               _stream_on(dev, stream)), "lora_rms_norm")
 
 
 def lora_quantize_rows(x: torch.Tensor, out8: torch.Tensor, scale: torch.Tensor,
                        stream=None) -> None:
-    """Rows of x in 8 bits: scale = max|x| / 448 per row, out8 = x / scale."""
+    """Rows of x in 8 bits: out8 = x / scale with scale = max|x| / 448 per row
+    (out8 of e4m3) or max|x| / 127 (out8 of int8, the nearest integers)."""
     shape = x.shape
     if len(shape) != 2:
         raise LoraError("x must be a 2-D tensor")
     code, dev = _dtype_code(x.dtype), x.get_device()
-    po8, ldo8 = _matrix(out8, "out8", shape, E4M3, dev)
+    int8 = out8.dtype is _I8
+    po8, ldo8 = _matrix(out8, "out8", shape, _I8 if int8 else E4M3, dev)
     px, ldx = _matrix(x, "x", shape, x.dtype, dev)
-    check(lib.lora_quantize_rows(code, px, ldx, shape[0], shape[1], po8, ldo8,
-                                 _scales(scale, "scale", shape[0], dev), _stream_on(dev, stream)),
+    quantize = lib.lora_quantize_rows_int8 if int8 else lib.lora_quantize_rows
+    check(quantize(code, px, ldx, shape[0], shape[1], po8, ldo8,
+                   _scales(scale, "scale", shape[0], dev), _stream_on(dev, stream)),
           "lora_quantize_rows")
 
 
-def lora_linear_fp8(table: LoraTable, W8: torch.Tensor, w_scale: torch.Tensor, x8: torch.Tensor,
-                    x_scale: torch.Tensor, x: torch.Tensor, seg: Segments, y: torch.Tensor,
-                    ws: Workspace, stream=None) -> None:
-    """y = (x8 W8^T) x_scale w_scale + (x A_i^T) B_i^T per token, y overwritten:
-    a shared projection in 8 bits ([N, K], the table's slices stacked in
-    order) beside the batch's adapters.  One launch for up to 64 tokens."""
+def _linear_8bit(call, name: str, dtype8, table: LoraTable, W8: torch.Tensor, w_scale: torch.Tensor,
+                 x8: torch.Tensor, x_scale: torch.Tensor, x: torch.Tensor, seg: Segments,
+                 y: torch.Tensor, ws: Workspace, stream) -> None:
     K, N, dtype, shape = table.K, table.N, table.dtype, x.shape
     if not (x8.shape == shape and W8.shape == (N, K) and y.shape == (shape[0], N)):
         _cols(x, "x", K)
@@ -691,16 +695,111 @@ def lora_linear_fp8(table: LoraTable, W8: torch.Tensor, w_scale: torch.Tensor, x
         if W8.shape[0] != N:
             raise LoraError("W8 must have one row per output column of the table")
     M, dev = shape[0], x.get_device()
-    pw, ldw = _matrix(W8, "W8", (N, K), E4M3, dev)
-    px8, ldx8 = _matrix(x8, "x8", shape, E4M3, dev)
+    pw, ldw = _matrix(W8, "W8", (N, K), dtype8, dev)
+    px8, ldx8 = _matrix(x8, "x8", shape, dtype8, dev)
     px, ldx = _matrix(x, "x", (M, K), dtype, dev)
     py, ldy = _matrix(y, "y", y.shape, dtype, dev)
     pws, pxs = _scales(w_scale, "w_scale", N, dev), _scales(x_scale, "x_scale", M, dev)
     if seg.L != table.L or M > seg.sorted_idx.shape[0]:
         raise LoraError("segment buffers do not match the table or the batch")
     _together(dev, table=table.A_table, segments=seg.sorted_idx, workspace=ws.buf)
-    check(lib.lora_linear_fp8(table.ref, pw, ldw, pws, px8, ldx8, pxs, px, ldx, M, seg.ref, py, ldy,
-                              ws.ptr, ws.nbytes, _stream_on(dev, stream)), "lora_linear_fp8")
+    check(call(table.ref, pw, ldw, pws, px8, ldx8, pxs, px, ldx, M, seg.ref, py, ldy,
+               ws.ptr, ws.nbytes, _stream_on(dev, stream)), name)
+
+
+def lora_linear_fp8(table: LoraTable, W8: torch.Tensor, w_scale: torch.Tensor, x8: torch.Tensor,
+                    x_scale: torch.Tensor, x: torch.Tensor, seg: Segments, y: torch.Tensor,
+                    ws: Workspace, stream=None) -> None:
+    """y = (x8 W8^T) x_scale w_scale + (x A_i^T) B_i^T per token, y overwritten:
+    a shared projection in 8 bits ([N, K], the table's slices stacked in
+    order) beside the batch's adapters.  One launch for up to 64 tokens."""
+    _linear_8bit(lib.lora_linear_fp8, "lora_linear_fp8", E4M3, table, W8, w_scale, x8, x_scale, x,
+                 seg, y, ws, stream)
+
+
+def lora_linear_int8(table: LoraTable, W8: torch.Tensor, w_scale: torch.Tensor, x8: torch.Tensor,
+                     x_scale: torch.Tensor, x: torch.Tensor, seg: Segments, y: torch.Tensor,
+                     ws: Workspace, stream=None) -> None:
+    """lora_linear_fp8 with W8 and x8 in 8-bit integers (lora_quantize_rows and
+    lora_rms_norm into int8 tensors); the sums over K are exact."""
+    _linear_8bit(lib.lora_linear_int8, "lora_linear_int8", _I8, table, W8, w_scale, x8, x_scale, x,
+                 seg, y, ws, stream)
+
+
+# ------------------------------------------------------------------------- experts' products
+class MoeGroups:
+    """Device buffers of a batch's (token, chosen expert) pairs by expert: up to
+    `pairs_cap` pairs (tokens times top-k) over E experts."""
+
+    def __init__(self, pairs_cap: int, E: int, device="cuda"):
+        if not 1 <= E <= 256:
+            raise LoraError("expert count out of range")
+        self.E, self.count, self.topk = int(E), 0, 0
+        self.pairs = torch.empty(max(int(pairs_cap), 1), dtype=_I32, device=device)
+        self.offsets = torch.zeros(self.E + 1, dtype=_I32, device=device)
+
+
+def lora_moe_group(topk_ids: torch.Tensor, groups: MoeGroups, stream=None) -> None:
+    """The pairs of topk_ids int32 [M, topk] in the experts' order: groups.pairs
+    holds pair indices m * topk + k by ascending expert, groups.offsets where
+    each expert's begin; ids outside [0, E) come last and belong to no share."""
+    if topk_ids.dtype is not _I32 or topk_ids.dim() != 2 or not topk_ids.is_contiguous():
+        raise LoraError("topk_ids must be a contiguous int32 tensor [M, topk]")
+    M, topk = topk_ids.shape
+    dev = topk_ids.get_device()
+    if M * topk > groups.pairs.shape[0]:
+        raise LoraError(f"the groups hold {groups.pairs.shape[0]} pairs, {M * topk} needed")
+    if dev < 0 or groups.pairs.get_device() != dev:
+        raise LoraError("topk_ids and the groups must live on one GPU")
+    check(lib.lora_moe_group(topk_ids.data_ptr(), M, topk, groups.E, groups.pairs.data_ptr(),
+                             groups.offsets.data_ptr(), _stream_on(dev, stream)), "lora_moe_group")
+    groups.count, groups.topk = M * topk, topk
+
+
+def lora_moe_linear(W: torch.Tensor, x: torch.Tensor, topk: int, groups: MoeGroups, y: torch.Tensor,
+                    w_scale: Optional[torch.Tensor] = None, x_scale: Optional[torch.Tensor] = None,
+                    stream=None) -> None:
+    """y[f] = W[e] x[r] for every pair f of the groups, e its expert: the experts'
+    base products that the MoE deltas are added to.  W [E, N, K] in bfloat16, or
+    in e4m3 or int8 with w_scale [E, N] and x_scale (one a row of x); x of W's
+    type, one row per token (r = f // topk) or one per pair (r = f); y bfloat16,
+    one row per pair.  Rows of y whose pair has no share are left as they are."""
+    dtype = W.dtype
+    if dtype is torch.bfloat16:
+        code = LORA_BF16
+    elif dtype is _I8:
+        code = LORA_INT8
+    elif dtype is E4M3:
+        code = LORA_E4M3
+    else:
+        raise LoraError(f"unsupported dtype {dtype}")
+    if W.dim() != 3 or W.shape[0] != groups.E or not W.is_contiguous():
+        raise LoraError(f"W must be a contiguous tensor [E, N, K] of the groups' {groups.E} experts")
+    E, N, K = W.shape
+    if x.dim() != 2 or y.dim() != 2:
+        raise LoraError("x and y must be 2-D tensors")
+    P, rows = y.shape[0], x.shape[0]
+    if P != groups.count or (P and topk != groups.topk):
+        raise LoraError(f"the groups were made for {groups.count} pairs with top-{groups.topk}, y has {P} rows")
+    if topk < 1 or P % topk or rows not in (P, P // topk):
+        raise LoraError("x must have one row per token or one per pair, y one per pair")
+    dev = x.get_device()
+    px, ldx = _matrix(x, "x", (rows, K), dtype, dev)
+    py, ldy = _matrix(y, "y", (P, N), torch.bfloat16, dev)
+    pws = pxs = 0
+    if code == LORA_BF16:
+        if w_scale is not None or x_scale is not None:
+            raise LoraError("w_scale and x_scale go with the 8-bit types")
+    else:
+        if w_scale is None or x_scale is None:
+            raise LoraError("the 8-bit types need w_scale and x_scale")
+        pws, pxs = _scales(w_scale, "w_scale", E * N, dev), _scales(x_scale, "x_scale", rows, dev)
+    _together(dev, W=W, groups=groups.pairs)
+    check(lib.lora_moe_linear(code, W.data_ptr(), pws, E, N, K, groups.pairs.data_ptr(),
+                              groups.offsets.data_ptr(), px, ldx, pxs, P // topk, topk, rows == P, py, ldy,
+                              _stream_on(dev, stream)), "lora_moe_linear")
+
+
 
 
 class MoeExperts:

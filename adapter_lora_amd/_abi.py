@@ -11,7 +11,7 @@ LIB_PATH = os.environ.get("MLORA_LIB", os.path.join(HERE, "libmlora.so"))
 
 LORA_OK, LORA_INVALID_ARG, LORA_UNSUPPORTED, LORA_HIP_ERROR = 0, 1, 2, 3
 LORA_DEVERR_WAIT, LORA_DEVERR_BAD_ID, LORA_DEVERR_TABLE = 1, 2, 4
-LORA_F32, LORA_BF16, LORA_E4M3 = 0, 1, 2
+LORA_F32, LORA_BF16, LORA_E4M3, LORA_INT8 = 0, 1, 2, 3
 LORA_MAX_SLICES = 4
 LORA_RANK_ALIGN = 16
 LORA_MAX_RANK = 64
@@ -19,7 +19,7 @@ LORA_MAX_ADAPTERS = 1024
 LORA_DECODE_MAX_M = 64
 LORA_NOALLOC_SCRATCH_BYTES = 1 << 20
 LORA_TILE_ROWS = 64
-MLORA_ABI_VERSION = 6
+MLORA_ABI_VERSION = 7
 
 
 class LoraError(RuntimeError):
@@ -108,6 +108,11 @@ SIGNATURES = {
     "lora_moe_topk_reduce": (I32, [I32, P, I64, P, P, I64, I32, I32, I32, P]),
     "lora_rms_norm": (I32, [I32, P, I64, P, I64, P, F32, I32, I32, P, I64, P, I64, P, I64, P, P]),
     "lora_quantize_rows": (I32, [I32, P, I64, I32, I32, P, I64, P, P]),
+    "lora_rms_norm_int8": (I32, [I32, P, I64, P, I64, P, F32, I32, I32, P, I64, P, I64, P, I64, P, P]),
+    "lora_quantize_rows_int8": (I32, [I32, P, I64, I32, I32, P, I64, P, P]),
+    "lora_linear_int8": (I32, [PW, P, I64, P, P, I64, P, P, I64, I32, PS, P, I64, P, SZ, P]),
+    "lora_moe_group": (I32, [P, I32, I32, I32, P, P, P]),
+    "lora_moe_linear": (I32, [I32, P, P, I32, I32, I32, P, P, P, I64, P, I32, I32, I32, P, I64, P]),
     "lora_linear_fp8": (I32, [PW, P, I64, P, P, I64, P, P, I64, I32, PS, P, I64, P, SZ, P]),
     "lora_moe_decode_workspace_size": (SZ, [PMW, PME, I32]),
     "lora_moe_decode": (I32, [PMW, PME, P, P, I64, I32, P, I64, P, P, P, SZ, P]),

@@ -663,16 +663,15 @@ lora_status lora_moe_topk_reduce(int32_t dtype, const void* cache3, int64_t ld3,
 }
 
 // ------------------------------------------------------------------ 8-bit decoder layer
-lora_status lora_rms_norm(int32_t dtype, const void* x, int64_t ldx, const void* residual,
-                          int64_t ldr, const void* weight, float eps, int32_t M, int32_t K,
-                          void* residual_out, int64_t ldro, void* out, int64_t ldo, void* out8,
-                          int64_t ldo8, float* scale, hipStream_t stream) {
-    const Range range("lora_rms_norm");
+static lora_status rms_norm(int int8, int32_t dtype, const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                            const void* weight, float eps, int32_t M, int32_t K, void* residual_out, int64_t ldro,
+                            void* out, int64_t ldo, void* out8, int64_t ldo8, float* scale, hipStream_t stream) {
     if (dtype != LORA_F32 && dtype != LORA_BF16) return LORA_INVALID_ARG;
     if (M < 0 || K <= 0 || K % 8) return LORA_INVALID_ARG;
     if (K > kNormMaxK) return LORA_UNSUPPORTED;
     if (M == 0) return LORA_OK;
     if ((!out && !out8) || !scale != !out8 || (residual_out && !residual)) return LORA_INVALID_ARG;
+    if (int8 && !out8) return LORA_INVALID_ARG;
     if (!(eps >= 0.f)) return LORA_INVALID_ARG;
     lora_status st = check_rows(x, ldx, K);
     if (st == LORA_OK) st = check_rows(weight, K, K);
@@ -682,13 +681,12 @@ lora_status lora_rms_norm(int32_t dtype, const void* x, int64_t ldx, const void*
     if (st == LORA_OK && out8) st = check_rows(out8, ldo8, K);
     if (st != LORA_OK) return st;
     const NormParams p{x, ldx, residual, ldr, residual_out, ldro, weight, eps, out, ldo,
-                       static_cast<uint8_t*>(out8), ldo8, scale, M, K};
+                       static_cast<uint8_t*>(out8), ldo8, scale, M, K, int8};
     return from_hip(launch_rms_norm(dtype, p, stream));
 }
 
-lora_status lora_quantize_rows(int32_t dtype, const void* x, int64_t ldx, int32_t M, int32_t K,
-                               void* out8, int64_t ldo8, float* scale, hipStream_t stream) {
-    const Range range("lora_quantize_rows");
+static lora_status quantize_rows(int int8, int32_t dtype, const void* x, int64_t ldx, int32_t M, int32_t K, void* out8,
+                                 int64_t ldo8, float* scale, hipStream_t stream) {
     if (dtype != LORA_F32 && dtype != LORA_BF16) return LORA_INVALID_ARG;
     if (M < 0 || K <= 0 || K % 8) return LORA_INVALID_ARG;
     if (K > kNormMaxK) return LORA_UNSUPPORTED;
@@ -698,8 +696,38 @@ lora_status lora_quantize_rows(int32_t dtype, const void* x, int64_t ldx, int32_
     if (st != LORA_OK) return st;
     if (!scale) return LORA_INVALID_ARG;
     const NormParams p{x, ldx, nullptr, 0, nullptr, 0, nullptr, 0.f, nullptr, 0,
-                       static_cast<uint8_t*>(out8), ldo8, scale, M, K};
+                       static_cast<uint8_t*>(out8), ldo8, scale, M, K, int8};
     return from_hip(launch_rms_norm(dtype, p, stream));
+}
+
+lora_status lora_rms_norm(int32_t dtype, const void* x, int64_t ldx, const void* residual,
+                          int64_t ldr, const void* weight, float eps, int32_t M, int32_t K,
+                          void* residual_out, int64_t ldro, void* out, int64_t ldo, void* out8,
+                          int64_t ldo8, float* scale, hipStream_t stream) {
+    const Range range("lora_rms_norm");
+    return rms_norm(0, dtype, x, ldx, residual, ldr, weight, eps, M, K, residual_out, ldro, out, ldo, out8,
+                    ldo8, scale, stream);
+}
+
+lora_status lora_quantize_rows(int32_t dtype, const void* x, int64_t ldx, int32_t M, int32_t K,
+                               void* out8, int64_t ldo8, float* scale, hipStream_t stream) {
+    const Range range("lora_quantize_rows");
+    return quantize_rows(0, dtype, x, ldx, M, K, out8, ldo8, scale, stream);
+}
+
+lora_status lora_rms_norm_int8(int32_t dtype, const void* x, int64_t ldx, const void* residual,
+                               int64_t ldr, const void* weight, float eps, int32_t M, int32_t K,
+                               void* residual_out, int64_t ldro, void* out, int64_t ldo, void* out8,
+                               int64_t ldo8, float* scale, hipStream_t stream) {
+    const Range range("lora_rms_norm_int8");
+    return rms_norm(1, dtype, x, ldx, residual, ldr, weight, eps, M, K, residual_out, ldro, out, ldo, out8,
+                    ldo8, scale, stream);
+}
+
+lora_status lora_quantize_rows_int8(int32_t dtype, const void* x, int64_t ldx, int32_t M, int32_t K,
+                                    void* out8, int64_t ldo8, float* scale, hipStream_t stream) {
+    const Range range("lora_quantize_rows_int8");
+    return quantize_rows(1, dtype, x, ldx, M, K, out8, ldo8, scale, stream);
 }
 
 // rows that are addressed with 32-bit byte offsets
@@ -711,15 +739,17 @@ static lora_status check_rows8(const void* p, int64_t ld, int64_t width) {
     return LORA_OK;
 }
 
-lora_status lora_linear_fp8(const lora_weights_t* w, const void* W8, int64_t ldw,
-                            const float* w_scale, const void* x8, int64_t ldx8,
-                            const float* x_scale, const void* x, int64_t ldx, int32_t M,
-                            const lora_segments_t* seg, void* y, int64_t ldy, void* workspace,
-                            size_t workspace_bytes, hipStream_t stream) {
-    const Range range("lora_linear_fp8");
+// sums of products of two 8-bit integers (-128 among them) stay within 32 bits
+constexpr int kInt8MaxK = 131056;
+
+static lora_status linear_8bit(bool int8, const lora_weights_t* w, const void* W8, int64_t ldw, const float* w_scale,
+                               const void* x8, int64_t ldx8, const float* x_scale, const void* x, int64_t ldx,
+                               int32_t M, const lora_segments_t* seg, void* y, int64_t ldy, void* workspace,
+                               size_t workspace_bytes, hipStream_t stream) {
     lora_status st = check_weights(w);
     if (st != LORA_OK) return st;
     if (w->dtype != LORA_BF16 || w->K % 16) return LORA_UNSUPPORTED;
+    if (int8 && w->K > kInt8MaxK) return LORA_UNSUPPORTED;
     if (M < 0 || M > (1 << 24)) return LORA_INVALID_ARG;
     if ((st = check_segments(seg, w, M)) != LORA_OK) return st;
     if (M == 0) return LORA_OK;
@@ -738,13 +768,81 @@ lora_status lora_linear_fp8(const lora_weights_t* w, const void* W8, int64_t ldw
         // 32-bit offsets over the token rows, 32 rows of W8 and 16 (bf16) of A
         if (!below_2gib(M, ldx, 2) || !below_2gib(M, ldx8, 1) || !below_2gib(32, ldw, 1))
             return LORA_UNSUPPORTED;
-        return from_hip(launch_linear_fp8(a, W8, ldw, w_scale, x8, ldx8, x_scale, x, ldx, y, ldy,
-                                          workspace, stream));
+        return from_hip(launch_linear_8bit(int8, a, W8, ldw, w_scale, x8, ldx8, x_scale, x, ldx, y, ldy,
+                                           workspace, stream));
     }
     float* S = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + L.S);
     if (!below_2gib(256, ldw, 1)) return LORA_UNSUPPORTED;     // 256 rows of W8
-    return from_hip(launch_linear_fp8_many(a, W8, ldw, w_scale, x8, ldx8, x_scale, x, ldx, S, y, ldy, workspace,
-                                           stream));
+    return from_hip(launch_linear_8bit_many(int8, a, W8, ldw, w_scale, x8, ldx8, x_scale, x, ldx, S, y, ldy,
+                                            workspace, stream));
+}
+
+lora_status lora_linear_fp8(const lora_weights_t* w, const void* W8, int64_t ldw,
+                            const float* w_scale, const void* x8, int64_t ldx8,
+                            const float* x_scale, const void* x, int64_t ldx, int32_t M,
+                            const lora_segments_t* seg, void* y, int64_t ldy, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream) {
+    const Range range("lora_linear_fp8");
+    return linear_8bit(false, w, W8, ldw, w_scale, x8, ldx8, x_scale, x, ldx, M, seg, y, ldy, workspace,
+                       workspace_bytes, stream);
+}
+
+lora_status lora_linear_int8(const lora_weights_t* w, const void* W8, int64_t ldw,
+                             const float* w_scale, const void* x8, int64_t ldx8,
+                             const float* x_scale, const void* x, int64_t ldx, int32_t M,
+                             const lora_segments_t* seg, void* y, int64_t ldy, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream) {
+    const Range range("lora_linear_int8");
+    return linear_8bit(true, w, W8, ldw, w_scale, x8, ldx8, x_scale, x, ldx, M, seg, y, ldy, workspace,
+                       workspace_bytes, stream);
+}
+
+// ------------------------------------------------------------------ experts' products
+static bool pairs_ok(int32_t M, int32_t topk, int32_t E) {
+    return M >= 0 && topk >= 1 && topk <= 16 && E >= 1 && E <= 256 && (int64_t)M * topk <= (1 << 24);
+}
+
+lora_status lora_moe_group(const int32_t* topk_ids, int32_t M, int32_t topk, int32_t E, int32_t* pairs,
+                           int32_t* offsets, hipStream_t stream) {
+    const Range range("lora_moe_group");
+    if (!pairs_ok(M, topk, E) || !offsets) return LORA_INVALID_ARG;
+    if (M > 0 && (!topk_ids || !pairs)) return LORA_INVALID_ARG;
+    return from_hip(launch_moe_group(topk_ids, M * topk, E, pairs, offsets, stream));
+}
+
+lora_status lora_moe_linear(int32_t wdtype, const void* W, const float* w_scale, int32_t E, int32_t N, int32_t K,
+                            const int32_t* pairs, const int32_t* offsets, const void* x, int64_t ldx,
+                            const float* x_scale, int32_t M, int32_t topk, int32_t pair_rows, void* y, int64_t ldy,
+                            hipStream_t stream) {
+    const Range range("lora_moe_linear");
+    if (wdtype != LORA_BF16 && wdtype != LORA_E4M3 && wdtype != LORA_INT8) return LORA_INVALID_ARG;
+    const bool eight = wdtype != LORA_BF16;
+    if (!pairs_ok(M, topk, E)) return LORA_INVALID_ARG;
+    if (N <= 0 || N % 8 || K <= 0 || K % (eight ? 16 : 8)) return LORA_INVALID_ARG;
+    if (eight != (w_scale != nullptr) || eight != (x_scale != nullptr)) return LORA_INVALID_ARG;
+    if (K > kInt8MaxK) return LORA_UNSUPPORTED;      // and 32-bit offsets within 256 rows of W
+    if (M == 0) return LORA_OK;
+    if (!pairs || !offsets || !W || !aligned16(W)) return LORA_INVALID_ARG;
+    lora_status st = eight ? check_rows8(x, ldx, K) : check_rows(x, ldx, K);
+    if (st == LORA_OK) st = check_rows(y, ldy, N);
+    if (st != LORA_OK) return st;
+    const int P = M * topk, wide = eight ? 1 : 2;
+    // a grid has fewer than 2^32 threads
+    if (((int64_t)P / 256 + std::min(E, P) + 1) * (((int64_t)N + 255) / 256) > (1 << 23)) return LORA_UNSUPPORTED;
+    ExpertsParams p{};
+    p.W = static_cast<const char*>(W);
+    p.w_scale = w_scale;
+    p.pairs = pairs;
+    p.offsets = offsets;
+    p.x = static_cast<const char*>(x);
+    p.ldx = ldx * wide;
+    p.x_scale = x_scale;
+    p.y = static_cast<uint16_t*>(y);
+    p.ldy = ldy;
+    p.E = E; p.N = N; p.Kb = K * wide; p.P = P;
+    p.x_div = pair_rows ? 1 : topk;
+    p.x_rows = pair_rows ? P : M;
+    return from_hip(launch_experts(wdtype, p, stream));
 }
 
 static lora_status check_experts(const lora_moe_experts_t* ex, const lora_moe_weights_t* w) {

@@ -52,24 +52,6 @@ template <int RB_, int CB_> struct G8Shape {
     static constexpr int Waves = RB * CB >= 8 ? 1 : 2;   // per SIMD
 };
 
-// 32 x 32 x 64 on e4m3 operands, without block scales: lane l supplies row /
-// column l % 32 and 32 values of K (any 32, the same for both operands).
-__device__ __forceinline__ f32x16_t mfma32_e4m3(const uint4& a0, const uint4& a1, const uint4& b0,
-                                                const uint4& b1, f32x16_t c) {
-    const i32x8_t a = {(int)a0.x, (int)a0.y, (int)a0.z, (int)a0.w, (int)a1.x, (int)a1.y, (int)a1.z, (int)a1.w};
-    const i32x8_t b = {(int)b0.x, (int)b0.y, (int)b0.z, (int)b0.w, (int)b1.x, (int)b1.y, (int)b1.z, (int)b1.w};
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
-}
-
-typedef __bf16 bf16x2_fp8_t __attribute__((ext_vector_type(2)));
-
-// Two fp32 values to a bf16 pair in one instruction, round to nearest even.
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    typedef float f2 __attribute__((ext_vector_type(2)));
-    const f2 v = {a, b};
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_fp8_t));
-}
-
 // Running maximum of bf16 values without their signs, two by two: an infinity or
 // NaN is 0x7f80 or more.
 typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
@@ -107,8 +89,8 @@ struct GemmFp8Params {
     int seg_stride;              // ceil((L + 1) / 64): first-round search stride
 };
 
-template <typename G>
-__global__ __launch_bounds__(kGThreads, G::Waves) void k_gemm_fp8(GemmFp8Params p) {
+template <typename F, typename G>
+__global__ __launch_bounds__(kGThreads, G::Waves) void k_gemm_8bit(GemmFp8Params p) {
     constexpr int kGM = G::M, kGN = G::N, kGXL = G::XL, kGWL = G::WL, kGRB = G::RB, kGCB = G::CB;
     constexpr int kG8Stage = G::Stage, kWN = 32 * kGCB;          // columns of a wave
     __shared__ uint4 smem[kGRing * kG8Stage / 16];
@@ -221,16 +203,16 @@ __global__ __launch_bounds__(kGThreads, G::Waves) void k_gemm_fp8(GemmFp8Params 
         else o.w[blk - kGRB][h] = *reinterpret_cast<const uint4*>(lds + (get[t][h] + ring + wpart) + (blk - kGRB) * 4096);
     };
 
-    f32x16_t acc[kGRB][kGCB];
+    typename F::Acc32 sum[kGRB][kGCB];
 #pragma unroll
     for (int rb = 0; rb < kGRB; ++rb)
 #pragma unroll
         for (int cb = 0; cb < kGCB; ++cb)
 #pragma unroll
-            for (int q = 0; q < 16; ++q) acc[rb][cb][q] = 0.f;
+            for (int q = 0; q < 16; ++q) sum[rb][cb][q] = 0;
     auto mfma1 = [&](const Ops& o, int i) {
         const int rb = i / kGCB, cb = i % kGCB;
-        acc[rb][cb] = mfma32_e4m3(o.w[cb][0], o.w[cb][1], o.x[rb][0], o.x[rb][1], acc[rb][cb]);
+        sum[rb][cb] = F::mma32(o.w[cb][0], o.w[cb][1], o.x[rb][0], o.x[rb][1], sum[rb][cb]);
     };
 
     // prologue: stages 0 and 1 in LDS, stages 2 and 3 in flight, the first
@@ -382,6 +364,7 @@ __global__ __launch_bounds__(kGThreads, G::Waves) void k_gemm_fp8(GemmFp8Params 
     step(ks, 0, 2);
     step(ks + 1, 1, 3);
     // ---- dequantization: row lr of block rb, columns 8 (q / 4) + 4 lh + q % 4 of block cb
+    f32x16_t acc[kGRB][kGCB];
     float xs[kGRB];
 #pragma unroll
     for (int rb = 0; rb < kGRB; ++rb) xs[rb] = s_xs[rb * 32 + lr];
@@ -392,10 +375,10 @@ __global__ __launch_bounds__(kGThreads, G::Waves) void k_gemm_fp8(GemmFp8Params 
             const float4 ws = *reinterpret_cast<const float4*>(s_ws + wave * kWN + cb * 32 + 8 * g + 4 * lh);
 #pragma unroll
             for (int rb = 0; rb < kGRB; ++rb) {
-                acc[rb][cb][4 * g] *= xs[rb] * ws.x;
-                acc[rb][cb][4 * g + 1] *= xs[rb] * ws.y;
-                acc[rb][cb][4 * g + 2] *= xs[rb] * ws.z;
-                acc[rb][cb][4 * g + 3] *= xs[rb] * ws.w;
+                acc[rb][cb][4 * g] = (float)sum[rb][cb][4 * g] * (xs[rb] * ws.x);
+                acc[rb][cb][4 * g + 1] = (float)sum[rb][cb][4 * g + 1] * (xs[rb] * ws.y);
+                acc[rb][cb][4 * g + 2] = (float)sum[rb][cb][4 * g + 2] * (xs[rb] * ws.z);
+                acc[rb][cb][4 * g + 3] = (float)sum[rb][cb][4 * g + 3] * (xs[rb] * ws.w);
             }
         }
     __syncthreads();     // every wave is done with the ring
@@ -521,8 +504,8 @@ __global__ __launch_bounds__(kGThreads, G::Waves) void k_gemm_fp8(GemmFp8Params 
     }
 }
 
-template <typename G>
-hipError_t launch_gemm_fp8_as(GemmFp8Params& p, hipStream_t st) {
+template <typename F, typename G>
+hipError_t launch_gemm_8bit_as(GemmFp8Params& p, hipStream_t st) {
     const LinearArgs& a = p.a;
     int t = 0;
     for (int s = 0; s < a.n_sl; ++s) {
@@ -533,11 +516,12 @@ hipError_t launch_gemm_fp8_as(GemmFp8Params& p, hipStream_t st) {
     p.col_tiles = t;
     p.row_tiles = (a.M + G::M - 1) / G::M;
     const unsigned grid = (unsigned)(p.row_tiles * ((p.col_tiles + 7) / 8 * 8));
-    hipLaunchKernelGGL((k_gemm_fp8<G>), dim3(grid), dim3(kGThreads), 0, st, p);
+    hipLaunchKernelGGL((k_gemm_8bit<F, G>), dim3(grid), dim3(kGThreads), 0, st, p);
     return hipGetLastError();
 }
 
-hipError_t launch_gemm_fp8(const LinearArgs& a, const void* x8, int64_t ldx8, const float* x_scale,
+template <typename F>
+hipError_t launch_gemm_8bit(const LinearArgs& a, const void* x8, int64_t ldx8, const float* x_scale,
                            const void* W8, int64_t ldw, const float* w_scale, const float* S, void* y,
                            int64_t ldy, hipStream_t st) {
     GemmFp8Params p{};
@@ -573,12 +557,13 @@ hipError_t launch_gemm_fp8(const LinearArgs& a, const void* x8, int64_t ldx8, co
     const int64_t ns = columns(128), nl = columns(256), K = a.K;
     const int64_t small = ((a.M + 63) / 64 * ns + 255) / 256, large = ((a.M + 127) / 128 * nl + 255) / 256;
     if (small <= 4096 && small * (14 * 4096 + 85 * K) < large * (80 * 4096 + 200 * K))
-        return launch_gemm_fp8_as<G8Shape<2, 1>>(p, st);
-    return launch_gemm_fp8_as<G8Shape<4, 2>>(p, st);
+        return launch_gemm_8bit_as<F, G8Shape<2, 1>>(p, st);
+    return launch_gemm_8bit_as<F, G8Shape<4, 2>>(p, st);
 }
 
 // Any number of tokens, S by way of memory: shrink, then one of the products.
-hipError_t launch_linear_fp8_many(const LinearArgs& a, const void* W8, int64_t ldw, const float* w_scale,
+template <typename F>
+hipError_t launch_linear_8bit_many(const LinearArgs& a, const void* W8, int64_t ldw, const float* w_scale,
                                   const void* x8, int64_t ldx8, const float* x_scale, const void* x,
                                   int64_t ldx, float* S, void* y, int64_t ldy, void* ws, hipStream_t st) {
     // One launch over all of K reads the rows of x again for every 16 columns of
@@ -601,8 +586,22 @@ hipError_t launch_linear_fp8_many(const LinearArgs& a, const void* W8, int64_t l
     // 2048 16.0 / 20.3, 4096 23.4 / 23.4, 8192 36.6 / 31.6.
     const int64_t units = (a.M + 63) / 64 * ((a.slice_off[a.n_sl] + 31) / 32);
     if (units <= 256 && a.K >= 2048 && ldx8 < INT32_MAX / (int64_t)a.M)
-        return launch_linear_fp8_groups(a, W8, ldw, w_scale, x8, ldx8, x_scale, S, y, ldy, st);
-    return launch_gemm_fp8(a, x8, ldx8, x_scale, W8, ldw, w_scale, S, y, ldy, st);
+        return launch_linear_8bit_groups<F>(a, W8, ldw, w_scale, x8, ldx8, x_scale, S, y, ldy, st);
+    return launch_gemm_8bit<F>(a, x8, ldx8, x_scale, W8, ldw, w_scale, S, y, ldy, st);
+}
+
+hipError_t launch_linear_8bit(bool int8, const LinearArgs& a, const void* W8, int64_t ldw, const float* w_scale,
+                              const void* x8, int64_t ldx8, const float* x_scale, const void* x, int64_t ldx,
+                              void* y, int64_t ldy, void* ws, hipStream_t st) {
+    return int8 ? launch_linear_8bit<FmtInt8>(a, W8, ldw, w_scale, x8, ldx8, x_scale, x, ldx, y, ldy, ws, st)
+                : launch_linear_8bit<FmtE4m3>(a, W8, ldw, w_scale, x8, ldx8, x_scale, x, ldx, y, ldy, ws, st);
+}
+
+hipError_t launch_linear_8bit_many(bool int8, const LinearArgs& a, const void* W8, int64_t ldw, const float* w_scale,
+                                   const void* x8, int64_t ldx8, const float* x_scale, const void* x, int64_t ldx,
+                                   float* S, void* y, int64_t ldy, void* ws, hipStream_t st) {
+    return int8 ? launch_linear_8bit_many<FmtInt8>(a, W8, ldw, w_scale, x8, ldx8, x_scale, x, ldx, S, y, ldy, ws, st)
+                : launch_linear_8bit_many<FmtE4m3>(a, W8, ldw, w_scale, x8, ldx8, x_scale, x, ldx, S, y, ldy, ws, st);
 }
 
 }  // namespace mlora

@@ -222,19 +222,41 @@ struct NormParams {
     int64_t ldo8;
     float* scale;
     int M, K;
+    int int8;               // out8 holds 8-bit integers
 };
 
 hipError_t launch_rms_norm(int dtype, const NormParams& p, hipStream_t st);
 
-// y = xs ws (x8 W8^T) + S B_i^T on e4m3 operands: M <= LORA_DECODE_MAX_M in one
-// launch (linear_fp8.hpp; `ws` holds the exchange slots), any M by way of S in
+// y = xs ws (x8 W8^T) + S B_i^T on e4m3 or int8 operands: M <= LORA_DECODE_MAX_M in
+// one launch (linear_fp8.hpp; `ws` holds the exchange slots), any M by way of S in
 // memory (gemm_fp8.hpp; fp32 [M][cols], sorted rows, `ws` the partial sums).
-hipError_t launch_linear_fp8(const LinearArgs& a, const void* W8, int64_t ldw, const float* w_scale,
-                             const void* x8, int64_t ldx8, const float* x_scale, const void* x,
-                             int64_t ldx, void* y, int64_t ldy, void* ws, hipStream_t st);
-hipError_t launch_linear_fp8_many(const LinearArgs& a, const void* W8, int64_t ldw, const float* w_scale,
-                                  const void* x8, int64_t ldx8, const float* x_scale, const void* x,
-                                  int64_t ldx, float* S, void* y, int64_t ldy, void* ws, hipStream_t st);
+hipError_t launch_linear_8bit(bool int8, const LinearArgs& a, const void* W8, int64_t ldw, const float* w_scale,
+                              const void* x8, int64_t ldx8, const float* x_scale, const void* x, int64_t ldx,
+                              void* y, int64_t ldy, void* ws, hipStream_t st);
+hipError_t launch_linear_8bit_many(bool int8, const LinearArgs& a, const void* W8, int64_t ldw, const float* w_scale,
+                                   const void* x8, int64_t ldx8, const float* x_scale, const void* x, int64_t ldx,
+                                   float* S, void* y, int64_t ldy, void* ws, hipStream_t st);
+
+// Pairs by expert, and the experts' products over their shares (experts.hpp).
+// Rows of W and x in bytes: Kb of values, x rows ldx apart; x row of pair f: f / x_div.
+struct ExpertsParams {
+    const char* W;
+    const float* w_scale;
+    const int32_t* pairs;
+    const int32_t* offsets;
+    const char* x;
+    int64_t ldx;
+    const float* x_scale;
+    uint16_t* y;
+    int64_t ldy;
+    int E, N, Kb, P;
+    int x_div, x_rows;
+    int col_tiles;
+};
+
+hipError_t launch_moe_group(const int32_t* topk_ids, int P, int E, int32_t* pairs, int32_t* offsets,
+                            hipStream_t st);
+hipError_t launch_experts(int wdtype, ExpertsParams& p, hipStream_t st);
 
 // A whole MoE layer for few tokens (moe_decode.hpp).
 struct MoeDecodeParams {

@@ -40,22 +40,11 @@
 #pragma once
 
 #include "common.hpp"
+#include "formats.hpp"
 #include "kernels.hpp"
 #include "row_stage.hpp"
 
 namespace mlora {
-
-typedef int i32x8_t __attribute__((ext_vector_type(8)));
-
-// 16 x 16 x 128 on e4m3 operands (format code 0 for both), without block
-// scales.  Lane l supplies row / column l % 16 and 32 values of K; which 32
-// does not matter as long as both operands agree.
-__device__ __forceinline__ f32x4_t mfma_e4m3(const uint4& a0, const uint4& a1, const uint4& b0,
-                                             const uint4& b1, f32x4_t c) {
-    const i32x8_t a = {(int)a0.x, (int)a0.y, (int)a0.z, (int)a0.w, (int)a1.x, (int)a1.y, (int)a1.z, (int)a1.w};
-    const i32x8_t b = {(int)b0.x, (int)b0.y, (int)b0.z, (int)b0.w, (int)b1.x, (int)b1.y, (int)b1.z, (int)b1.w};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
-}
 
 constexpr int kFpThreads = 512;
 constexpr int kFpWaves = kFpThreads / kWave;
@@ -198,8 +187,8 @@ __device__ __forceinline__ void fp8_producer(const Fp8Params& p, uint32_t tag, u
 // follow each other on one L2 (every eighth workgroup).  With TB = 4 and NR = 1 the
 // 128 registers are full: one value (SLOTS) or six are spilled across the loop over K,
 // none within it.
-template <int TB, int NR, bool SLOTS>
-__global__ __launch_bounds__(kFpThreads, TB * NR == 8 ? 2 : 4) void k_linear_fp8(Fp8Params p) {
+template <typename F, int TB, int NR, bool SLOTS>
+__global__ __launch_bounds__(kFpThreads, TB * NR == 8 ? 2 : 4) void k_linear_8bit(Fp8Params p) {
     constexpr int kStage = fp8_stage(TB, NR);
     __shared__ uint4 smem[kFpWaves * kStage];
     __shared__ __attribute__((aligned(16))) uint16_t sHi[TB * 16 * kFpSLD], sLo[TB * 16 * kFpSLD];
@@ -312,11 +301,13 @@ __global__ __launch_bounds__(kFpThreads, TB * NR == 8 ? 2 : 4) void k_linear_fp8
     uint4* st = smem + wave * kStage;
     uint4* sx = st + NR * 16 * 8;
     const StageAt at;
-    f32x4_t acc[NR][TB];
+    typename F::Acc16 sum[NR][TB];
 #pragma unroll
     for (int r = 0; r < NR; ++r)
 #pragma unroll
-        for (int t = 0; t < TB; ++t) acc[r][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < TB; ++t)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) sum[r][t][q] = 0;
     for (int b0 = wave; b0 < KB; b0 += U * kFpWaves) {
 #pragma unroll
         for (int q = 0; q < U; ++q) {
@@ -334,19 +325,20 @@ __global__ __launch_bounds__(kFpThreads, TB * NR == 8 ? 2 : 4) void k_linear_fp8
                     for (int r = 0; r < NR; ++r) w[r][0] = st[at.half(r, 0)], w[r][1] = st[at.half(r, 1)];
                 const uint4 x0 = sx[at.half(0, 0)], x1 = sx[at.half(0, 1)];
 #pragma unroll
-                for (int r = 0; r < NR; ++r) acc[r][t] = mfma_e4m3(w[r][0], w[r][1], x0, x1, acc[r][t]);
+                for (int r = 0; r < NR; ++r) sum[r][t] = F::mma16(w[r][0], w[r][1], x0, x1, sum[r][t]);
                 stage_order();
             }
             load_w(q, b0 + (q + U) * kFpWaves);
             load_x(q % UX, b0 + (q + UX) * kFpWaves);
         }
     }
+    f32x4_t acc[NR][TB];
 #pragma unroll
     for (int r = 0; r < NR; ++r)
 #pragma unroll
         for (int t = 0; t < TB; ++t)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) acc[r][t][q] *= xs[t] * ws[r][q];
+            for (int q = 0; q < 4; ++q) acc[r][t][q] = (float)sum[r][t][q] * (xs[t] * ws[r][q]);
 
     // ---- deltas
     const int q_rp = seg_ok && q_p0 < q_p1 && (!kTableChecks || range_ok) ? rank_l : 0;
@@ -586,8 +578,8 @@ hipError_t launch_shrink_rows(const LinearArgs& a, const void* x, int64_t ldx, f
     return hipGetLastError();
 }
 
-template <int TB, int NR, bool SLOTS = true>
-hipError_t launch_linear_fp8_as(Fp8Params& p, hipStream_t st) {
+template <typename F, int TB, int NR, bool SLOTS = true>
+hipError_t launch_linear_8bit_as(Fp8Params& p, hipStream_t st) {
     int t = 0;
     for (int s = 0; s < p.a.n_sl; ++s) {
         p.tile_start[s] = t;
@@ -608,7 +600,7 @@ hipError_t launch_linear_fp8_as(Fp8Params& p, hipStream_t st) {
     } else {
         grid = (unsigned)((p.a.M + 63) / 64 * ((t + 7) / 8 * 8));
     }
-    hipLaunchKernelGGL((k_linear_fp8<TB, NR, SLOTS>), dim3(grid), dim3(kFpThreads), 0, st, p);
+    hipLaunchKernelGGL((k_linear_8bit<F, TB, NR, SLOTS>), dim3(grid), dim3(kFpThreads), 0, st, p);
     return hipGetLastError();
 }
 
@@ -629,7 +621,8 @@ static Fp8Params fp8_params(const LinearArgs& a, const void* W8, int64_t ldw, co
     return p;
 }
 
-hipError_t launch_linear_fp8(const LinearArgs& a, const void* W8, int64_t ldw, const float* w_scale,
+template <typename F>
+hipError_t launch_linear_8bit(const LinearArgs& a, const void* W8, int64_t ldw, const float* w_scale,
                              const void* x8, int64_t ldx8, const float* x_scale, const void* x,
                              int64_t ldx, void* y, int64_t ldy, void* ws, hipStream_t st) {
     Fp8Params p = fp8_params(a, W8, ldw, w_scale, x8, ldx8, x_scale, x, ldx, y, ldy);
@@ -651,12 +644,13 @@ hipError_t launch_linear_fp8(const LinearArgs& a, const void* W8, int64_t ldw, c
     const int64_t units = a.slice_off[a.n_sl] / 32;
     const int64_t few = a.K <= 2048 ? 128 : a.K < 8192 ? 192 : 448;
     const bool wide = units >= (a.M <= 16 ? few : 256);
-    if (a.M <= 16) return wide ? launch_linear_fp8_as<1, 2>(p, st) : launch_linear_fp8_as<1, 1>(p, st);
-    if (a.M <= 32) return wide ? launch_linear_fp8_as<2, 2>(p, st) : launch_linear_fp8_as<2, 1>(p, st);
-    return wide ? launch_linear_fp8_as<4, 2>(p, st) : launch_linear_fp8_as<4, 1>(p, st);
+    if (a.M <= 16) return wide ? launch_linear_8bit_as<F, 1, 2>(p, st) : launch_linear_8bit_as<F, 1, 1>(p, st);
+    if (a.M <= 32) return wide ? launch_linear_8bit_as<F, 2, 2>(p, st) : launch_linear_8bit_as<F, 2, 1>(p, st);
+    return wide ? launch_linear_8bit_as<F, 4, 2>(p, st) : launch_linear_8bit_as<F, 4, 1>(p, st);
 }
 
-hipError_t launch_linear_fp8_groups(const LinearArgs& a, const void* W8, int64_t ldw, const float* w_scale,
+template <typename F>
+hipError_t launch_linear_8bit_groups(const LinearArgs& a, const void* W8, int64_t ldw, const float* w_scale,
                                     const void* x8, int64_t ldx8, const float* x_scale, const float* S,
                                     void* y, int64_t ldy, hipStream_t st) {
     Fp8Params p = fp8_params(a, W8, ldw, w_scale, x8, ldx8, x_scale, nullptr, 0, y, ldy);
@@ -666,7 +660,7 @@ hipError_t launch_linear_fp8_groups(const LinearArgs& a, const void* W8, int64_t
     // columns 18.6 / 20.3 us, to 4096 25.4 / 21.8; 512 tokens to 512 20.4 / 22.5, to
     // 1024 27.4 / 22.7)
     const int64_t units = (a.M + 63) / 64 * (a.slice_off[a.n_sl] / 32);
-    return units >= 192 ? launch_linear_fp8_as<4, 2, false>(p, st) : launch_linear_fp8_as<4, 1, false>(p, st);
+    return units >= 192 ? launch_linear_8bit_as<F, 4, 2, false>(p, st) : launch_linear_8bit_as<F, 4, 1, false>(p, st);
 }
 
 }  // namespace mlora

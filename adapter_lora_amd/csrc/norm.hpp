@@ -1,10 +1,11 @@
 // Root-mean-square norm of rows with the residual's addition before it and
-// an output in 8 bits (OCP e4m3, one fp32 scale per row) beside or instead of
-// the output in the storage type.  With h = x + residual in fp32:
+// an output in 8 bits (OCP e4m3 or integers, one fp32 scale per row) beside or
+// instead of the output in the storage type.  With h = x + residual in fp32:
 //     residual_out = round(h)
 //     v            = h * rsqrt(mean(h^2) + eps) * weight
 //     out          = round(v)
 //     scale        = max|v| / 448,   out8 = e4m3(v / scale)
+//     scale        = max|v| / 127,   out8 = the integer nearest to v / scale
 // and, without the norm, v = x (weights at load time, activations).
 //
 // One pass: a row's values stay in registers between the two uses, so x and
@@ -50,6 +51,43 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
     return (uint32_t)r;
 }
 
+// The integer nearest to v / s, ties to the even one, in the low byte, for
+// |v| <= 127 s (1 + 2^-23) and inv = 1 / s.  The sum v inv + 1.5 2^23 rounds the
+// product to an integer at once and leaves it in its low bits; r = v - q s is
+// exact (q has 7 bits, and next to s the values lie as close as v's own), so |r|
+// against s / 2 tells whether the reciprocal's last bit took the wrong side.
+constexpr float kIntMagic = 12582912.f;
+__device__ __forceinline__ uint32_t int8_of(float v, float inv, float s, float& r) {
+    const float m = fmaf(v, inv, kIntMagic);
+    r = fmaf(kIntMagic - m, s, v);
+    return __float_as_uint(m);
+}
+
+// Eight values to bytes.  A quotient's last bit matters next to a tie only: one
+// branch over all eight (bf16 rows have many values of half the largest one,
+// 63.5 scales, so the side is the scale's own rounding and cannot be left open).
+__device__ __forceinline__ uint2 pack_int8(const float (&v)[8], float inv, float s) {
+    uint32_t q[8];
+    float r[8], far = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        q[e] = int8_of(v[e], inv, s, r[e]);
+        far = fmaxf(far, fabsf(r[e]));
+    }
+    const float h = 0.5f * s;
+    if (far >= h) {                      // infinite and NaN scales: no |r| reaches them
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const bool up = r[e] > h || (r[e] == h && (q[e] & 1u));
+            const bool down = r[e] < -h || (r[e] == -h && (q[e] & 1u));
+            q[e] += up ? 1u : down ? 0xffffffffu : 0u;
+        }
+    }
+    const uint32_t a = __builtin_amdgcn_perm(q[1], q[0], 0x0c0c0400u), b = __builtin_amdgcn_perm(q[3], q[2], 0x04000c0cu);
+    const uint32_t c = __builtin_amdgcn_perm(q[5], q[4], 0x0c0c0400u), d = __builtin_amdgcn_perm(q[7], q[6], 0x04000c0cu);
+    return make_uint2(a | b, c | d);
+}
+
 // Largest of the wavefront's values, as unsigned integers (wave-uniform).
 __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
 #pragma unroll
@@ -62,7 +100,7 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
 
 // WPR wavefronts per row, CPL chunks of 8 values per lane: a row of up to
 // 512 * WPR * CPL values.  Without NORM: v = x, out8 and scale alone.
-template <typename T, int WPR, int CPL, bool NORM>
+template <typename T, int WPR, int CPL, bool NORM, bool INT8>
 __global__ __launch_bounds__(WPR * kWave < 256 ? 256 : WPR * kWave) void k_rms_norm(NormParams p) {
     constexpr int kRows = WPR < 4 ? 4 / WPR : 1;          // rows per workgroup
     __shared__ float s_sum[kRows * WPR];
@@ -124,13 +162,14 @@ __global__ __launch_bounds__(WPR * kWave < 256 ? 256 : WPR * kWave) void k_rms_n
     }
     if (!live) return;
     const float rstd = NORM ? 1.f / sqrtf(sum / (float)p.K + p.eps) : 1.f;
-    float inv = 0.f, den = 0.f;
+    float inv = 0.f, den = 0.f, s8 = 0.f;
     if (p.out8) {
         const float amax = __uint_as_float(top) * rstd;
         // the smallest normal number bounds the scale, so 1 / scale is finite
-        float s = amax / kE4M3Max;
+        float s = amax / (INT8 ? 127.f : kE4M3Max);
         s = s < 1.17549435e-38f ? (amax == 0.f ? 1.f : 1.17549435e-38f) : s;
         inv = 1.f / s;
+        s8 = s;
         den = s < INFINITY ? s : 0.f;
         if (wr == 0 && lane == 0) p.scale[m] = s;
     }
@@ -143,7 +182,18 @@ __global__ __launch_bounds__(WPR * kWave < 256 ? 256 : WPR * kWave) void k_rms_n
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = NORM ? h[c][e] * rstd * g[c][e] : h[c][e];
         if (NORM && p.out) st8(static_cast<T*>(p.out) + m * p.ldo + k, v);
-        if (p.out8) {
+        if constexpr (INT8) {
+            uint2 q = pack_int8(v, inv, s8);
+            if (s8 == INFINITY) {        // the row's infinities take the largest integer
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t b = fabsf(v[e]) < INFINITY ? 0u : v[e] > 0.f ? 0x7fu : 0x81u;
+                    uint32_t& w = e < 4 ? q.x : q.y;
+                    w = (w & ~(0xffu << 8 * (e % 4))) | b << 8 * (e % 4);
+                }
+            }
+            *reinterpret_cast<uint2*>(p.out8 + m * p.ldo8 + k) = q;
+        } else if (p.out8) {
             // v / scale, the reciprocal's product corrected by its residue:
             // bf16 values over a bf16 maximum are often ties of e4m3, and a
             // last-bit error of the quotient would round them the wrong way
@@ -168,8 +218,13 @@ hipError_t launch_norm_as(const NormParams& p, hipStream_t st) {
     const unsigned wgs = (unsigned)(((int64_t)p.M + kRows - 1) / kRows);
     const unsigned gx = wgs < (1u << 21) ? wgs : 1u << 21;
     const dim3 grid(gx, (wgs + gx - 1) / gx);
-    if (p.w) hipLaunchKernelGGL((k_rms_norm<T, WPR, CPL, true>), grid, dim3(kThreads), 0, st, p);
-    else hipLaunchKernelGGL((k_rms_norm<T, WPR, CPL, false>), grid, dim3(kThreads), 0, st, p);
+    if (p.int8) {                    // out8 is there (checked by the caller)
+        if (p.w) hipLaunchKernelGGL((k_rms_norm<T, WPR, CPL, true, true>), grid, dim3(kThreads), 0, st, p);
+        else hipLaunchKernelGGL((k_rms_norm<T, WPR, CPL, false, true>), grid, dim3(kThreads), 0, st, p);
+    } else {
+        if (p.w) hipLaunchKernelGGL((k_rms_norm<T, WPR, CPL, true, false>), grid, dim3(kThreads), 0, st, p);
+        else hipLaunchKernelGGL((k_rms_norm<T, WPR, CPL, false, false>), grid, dim3(kThreads), 0, st, p);
+    }
     return hipGetLastError();
 }
 

@@ -53,7 +53,7 @@
 extern "C" {
 #endif
 
-#define MLORA_ABI_VERSION 6
+#define MLORA_ABI_VERSION 7
 
 typedef enum lora_status {
     LORA_OK = 0,
@@ -65,7 +65,8 @@ typedef enum lora_status {
 typedef enum lora_dtype {
     LORA_F32 = 0,
     LORA_BF16 = 1,
-    LORA_E4M3 = 2 /* OCP e4m3 (largest value 448): 8-bit outputs and weights, with fp32 scales */
+    LORA_E4M3 = 2, /* OCP e4m3 (largest value 448): 8-bit outputs and weights, with fp32 scales */
+    LORA_INT8 = 3  /* 8-bit integers (-127 to 127 are written): outputs and weights, with fp32 scales */
 } lora_dtype;
 
 #define LORA_MAX_SLICES 4      /* stacked output slices per call (QKV = 3, gate-up = 2) */
@@ -572,6 +573,24 @@ lora_status lora_quantize_rows(int32_t dtype, const void* x, int64_t ldx, int32_
                                void* out8, int64_t ldo8, float* scale, hipStream_t stream);
 
 /*
+ * lora_rms_norm_int8, lora_quantize_rows_int8: the same with 8-bit integers in
+ * out8 (int8 [M, ldo8]; it has to be given),
+ *     scale[m] = max|v| / 127                         rounded to fp32
+ *     out8[m]  = v / scale[m]                         to the nearest integer, ties to even
+ * and of that quotient exactly: no rounding of it to fp32 comes between.  A row of
+ * zeros has scale 1; a scale is at least 2^-126.  A NaN in v makes its row's scale
+ * NaN; an infinity makes the scale infinite, its own integer 127 or -127 and the
+ * others of its row 0.
+ */
+lora_status lora_rms_norm_int8(int32_t dtype, const void* x, int64_t ldx, const void* residual,
+                               int64_t ldr, const void* weight, float eps, int32_t M, int32_t K,
+                               void* residual_out, int64_t ldro, void* out, int64_t ldo, void* out8,
+                               int64_t ldo8, float* scale, hipStream_t stream);
+
+lora_status lora_quantize_rows_int8(int32_t dtype, const void* x, int64_t ldx, int32_t M, int32_t K,
+                                    void* out8, int64_t ldo8, float* scale, hipStream_t stream);
+
+/*
  * lora_linear_fp8: a shared projection held in 8 bits, written together with
  * the batch's adapter deltas (the layer output of lora_linear_fused with base
  * operands in e4m3):
@@ -600,6 +619,57 @@ lora_status lora_linear_fp8(const lora_weights_t* w, const void* W8, int64_t ldw
                             const float* x_scale, const void* x, int64_t ldx, int32_t M,
                             const lora_segments_t* seg, void* y, int64_t ldy, void* workspace,
                             size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * lora_linear_int8: lora_linear_fp8 with int8 W8 and x8 (lora_quantize_rows_int8,
+ * lora_rms_norm_int8).  The sums over K are 32-bit integers, hence exact: K up to
+ * 131056 (LORA_UNSUPPORTED past it), and the base product's only roundings are
+ * those of its conversion to fp32, of the scales and of y.
+ */
+lora_status lora_linear_int8(const lora_weights_t* w, const void* W8, int64_t ldw,
+                             const float* w_scale, const void* x8, int64_t ldx8,
+                             const float* x_scale, const void* x, int64_t ldx, int32_t M,
+                             const lora_segments_t* seg, void* y, int64_t ldy, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------- experts' base products */
+
+/*
+ * lora_moe_group: the batch's pairs f = m*topk + k in the experts' order.
+ *   topk_ids device int32 [M, topk]: the chosen experts; an id outside [0, E) (an
+ *       expert that lives elsewhere) belongs to no share;
+ *   pairs   device int32 [M*topk] (out): ascending expert, equal experts in
+ *       ascending f, the pairs without a share last, in ascending f;
+ *   offsets device int32 [E + 1] (out): expert e's share is
+ *       pairs[offsets[e]] .. pairs[offsets[e + 1] - 1].
+ * M*topk <= 2^24, topk <= 16, E <= 256.  M == 0 writes the (empty) shares.
+ */
+lora_status lora_moe_group(const int32_t* topk_ids, int32_t M, int32_t topk, int32_t E,
+                           int32_t* pairs, int32_t* offsets, hipStream_t stream);
+
+/*
+ * lora_moe_linear: one product with each expert's weights over its share of the
+ * pairs (SGLang "LoRA + MoE" page: the expert GEMMs whose outputs, cache1 and
+ * cache3, the deltas are added to):
+ *     y[f, n] = x_scale[r] w_scale[e, n] sum_k x[r, k] W[e, n, k]
+ * for every pair f of expert e's share; r = f / topk, or r = f with pair_rows set.
+ * Rows of y without a share are neither read nor written.
+ *   W device [E, N, K] of wdtype (LORA_BF16, LORA_E4M3 or LORA_INT8), x device rows of
+ *   the same type: [M, ldx], or [M*topk, ldx] with pair_rows; y device bf16
+ *   [M*topk, ldy], overwritten;
+ *   w_scale device fp32 [E, N], x_scale device fp32, one a row of x: with the 8-bit
+ *   types (NULL for LORA_BF16, whose sums have no scales);
+ *   pairs, offsets: lora_moe_group's, of the same M, topk and E.
+ * N a multiple of 8; K and ldx of 8 (16 for the 8-bit types), K at most 131056
+ * (LORA_UNSUPPORTED past it).  Sums are fp32 (LORA_INT8: 32-bit integers; LORA_E4M3:
+ * as in lora_linear_fp8), y is rounded once.  No row of x past its share's is
+ * read, and none of y written, whatever pairs and offsets hold.
+ */
+lora_status lora_moe_linear(int32_t wdtype, const void* W, const float* w_scale, int32_t E,
+                            int32_t N, int32_t K, const int32_t* pairs, const int32_t* offsets,
+                            const void* x, int64_t ldx, const float* x_scale, int32_t M,
+                            int32_t topk, int32_t pair_rows, void* y, int64_t ldy,
+                            hipStream_t stream);
 
 /*
  * Router and experts of one MoE layer (SGLang "LoRA + MoE" page, the base
