@@ -840,7 +840,7 @@ lora_status lora_moe_linear(int32_t wdtype, const void* W, const float* w_scale,
     p.y = static_cast<uint16_t*>(y);
     p.ldy = ldy;
     p.E = E; p.N = N; p.Kb = K * wide; p.P = P;
-    p.x_div = pair_rows ? 1 : topk;
+    p.x_inv = pair_rows || topk == 1 ? 0 : (uint32_t)(((1ull << 32) + topk - 1) / topk);
     p.x_rows = pair_rows ? P : M;
     return from_hip(launch_experts(wdtype, p, stream));
 }

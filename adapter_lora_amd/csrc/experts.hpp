@@ -7,6 +7,7 @@
 #include "common.hpp"
 #include "formats.hpp"
 #include "kernels.hpp"
+#include "ring_product.hpp"
 #include "row_stage.hpp"
 
 namespace mlora {
@@ -134,77 +135,183 @@ hipError_t launch_moe_group(const int32_t* topk_ids, int P, int E, int32_t* pair
 }
 
 // ---------------------------------------------------------------- shares and tiles
-// 16 zero bytes: what rows of x read past K
-__device__ const uint4 k_zeros = {0, 0, 0, 0};
+// The x row of pair f < 2^24: f, or f / topk by its reciprocal (2^32 / topk rounded
+// up, exact for these f).
+__device__ __forceinline__ uint32_t pair_row(const ExpertsParams& p, uint32_t f) {
+    return p.x_inv ? __umulhi(f, p.x_inv) : f;
+}
 
-struct Tile {
-    int e;              // expert; -1: no such tile
-    int pos, rows;      // its sorted positions [pos, pos + rows)
-    int rt, rts;        // row tile of the expert, and how many it has
-    int64_t in;         // the tile's number among the expert's
-    int64_t total;      // all tiles
+// The experts' shares, expert 64 c + l in lane l: first position and pairs.  Offsets
+// are clamped into the list, so whatever they hold, no position lies outside it.
+template <int NC> struct Shares {
+    int pos[NC], n[NC];
+    __device__ __forceinline__ Shares(const int32_t* offsets, int E, int P) {
+        const int lane = lane_id();
+        int o0[NC], o1[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            o0[c] = offsets[min(c * kWave + lane, E)];
+            o1[c] = offsets[min(c * kWave + lane + 1, E)];
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            pos[c] = min(max(o0[c], 0), P);
+            n[c] = max(min(o1[c], P) - pos[c], 0);
+        }
+    }
 };
 
-// Tile `id` of the experts' shares cut into row tiles of `height` positions, each
-// `cols` column tiles wide (64-bit: a share may have many).  Offsets are clamped
-// into the list, so whatever they hold, no position lies outside it.
-__device__ __forceinline__ Tile find_tile(const int32_t* offsets, int E, int P, int height, int cols, int64_t id) {
+// Rows [pos, pos + rows) of expert e's share, column tile ct; e = -1: none.
+struct Tile {
+    int e = -1, pos = 0, rows = 0, ct = 0;
+};
+
+// n / cols by the reciprocal 2^32 / cols rounded up, which is one too many at most.
+__device__ __forceinline__ int div_cols(const ExpertsParams& p, int n) {
+    const int q = (int)__umulhi((uint32_t)n, p.cols_inv);
+    return p.col_tiles == 1 ? n : q - (n < q * p.col_tiles);
+}
+
+// Position of set bit `nth` of a mask (wave-uniform; nth below its bits).
+__device__ __forceinline__ int nth_bit(uint64_t mask, int nth) {
     const int lane = lane_id();
-    int o0[4], o1[4];
+    const bool hit = (mask >> lane & 1) && __popcll(mask & ((1ull << lane) - 1ull)) == nth;
+    return __builtin_ctzll(__ballot(hit));
+}
+
+// Share number `nth` of those with pairs.
+template <int NC> __device__ __forceinline__ Tile find_share(const ExpertsParams& p, int nth) {
+    const Shares<NC> sh(p.offsets, p.E, p.P);
+    Tile t;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const int e = c * kWave + lane;
-        o0[c] = c * kWave < E ? offsets[min(e, E)] : 0;
-        o1[c] = c * kWave < E ? offsets[min(e + 1, E)] : 0;
-    }
-    Tile t{-1, 0, 0, 0, 0, 0, 0};
-    int64_t run = 0;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        if (c * kWave >= E) break;
-        const int a = min(max(o0[c], 0), P), n = max(min(o1[c], P) - a, 0);
-        const int tiles = (n + height - 1) / height;
-        const int inc = wave_incl_scan(tiles);
-        const int all = __builtin_amdgcn_readlane(inc, kWave - 1);
-        if (t.e < 0 && id < (run + all) * cols) {
-            const uint64_t hit = __ballot(id < (run + inc) * cols);
-            const int l = __builtin_ctzll(hit);
-            const int first = __builtin_amdgcn_readlane(inc - tiles, l);
+    for (int c = 0; c < NC; ++c) {
+        const uint64_t some = __ballot(sh.n[c] > 0);
+        const int all = __popcll(some);
+        if (t.e < 0 && nth < all) {
+            const int l = nth_bit(some, nth);
             t.e = c * kWave + l;
-            t.rts = __builtin_amdgcn_readlane(tiles, l);
-            t.in = id - (run + first) * cols;
-            t.pos = __builtin_amdgcn_readlane(a, l);
-            t.rows = __builtin_amdgcn_readlane(n, l);
+            t.pos = __builtin_amdgcn_readlane(sh.pos[c], l);
+            t.rows = __builtin_amdgcn_readlane(sh.n[c], l);
         }
-        run += all;
+        nth -= all;
     }
-    t.total = run * cols;
+    return t;
+}
+
+// Tile `id` of the shares cut into tiles of 256 rows.  Order: expert by expert, whose
+// tiles of W come back while they are near, the tiles of more than 192 rows before
+// the share's last, in bands of four row tiles.  The experts of the last kTailTiles
+// tiles together by size, so that the long ones do not begin last.
+constexpr int kTailTiles = 512;
+
+template <int NC> __device__ __forceinline__ Tile find_tile(const ExpertsParams& p, int id) {
+    const Shares<NC> sh(p.offsets, p.E, p.P);
+    const int lane = lane_id(), cols = p.col_tiles;
+    int size[NC], full[NC], before[NC];      // class of the last tile (0: none), tiles above 192, earlier experts' tiles
+    int total = 0;
+    Tile t;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int left = sh.n[c] % kRingRows;
+        size[c] = left == 0 || left > 192 ? 0 : (left + 63) / 64;
+        full[c] = sh.n[c] / kRingRows + (left > 192);
+        const int tiles = full[c] + (size[c] > 0), inc = wave_incl_scan(tiles);
+        before[c] = total + inc - tiles;
+        total += __builtin_amdgcn_readlane(inc, kWave - 1);
+    }
+    if (id >= total * cols) return t;
+    // the expert that holds the tile; the first whose tiles all belong to the tail
+    const int at = div_cols(p, id), tail = total - div_cols(p, kTailTiles);
+    int w0 = 0, w1 = NC * kWave, skip = 0, t0 = NC * kWave, tskip = 0;
+    bool found = false;
+#pragma unroll
+    for (int c = NC - 1; c >= 0; --c) {
+        const uint64_t late = __ballot(before[c] >= tail), here = __ballot(before[c] <= at);
+        if (late != 0ull) {
+            const int l = __builtin_ctzll(late);
+            t0 = c * kWave + l;
+            tskip = __builtin_amdgcn_readlane(before[c], l);
+        }
+        if (!found && here != 0ull) {
+            const int l = 63 - __builtin_clzll(here);
+            found = true;
+            w0 = c * kWave + l;
+            w1 = w0 + 1;
+            skip = __builtin_amdgcn_readlane(before[c], l);
+        }
+    }
+    if (w0 >= t0) w0 = t0, w1 = NC * kWave, skip = tskip;
+    id -= skip * cols;
+    // among experts w0 .. w1: the large tiles, then the others by size
+    int run = 0, rt = 0;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const bool in = c * kWave + lane >= w0 && c * kWave + lane < w1;
+        const int tiles = in ? full[c] : 0, inc = wave_incl_scan(tiles);
+        const uint64_t hit = __ballot(id < (run + inc) * cols);
+        if (t.e < 0 && hit != 0ull) {
+            const int l = __builtin_ctzll(hit);
+            const int rts = __builtin_amdgcn_readlane(tiles, l);
+            const int in_e = id - (run + __builtin_amdgcn_readlane(inc - tiles, l)) * cols;
+            const int band = div_cols(p, in_e) / 4, k = in_e - band * 4 * cols, deep = min(4, rts - band * 4);
+            t.e = c * kWave + l;
+            t.ct = deep == 4 ? k / 4 : deep == 3 ? (int)__umulhi((uint32_t)k, 0x55555556u) : deep == 2 ? k / 2 : k;
+            rt = band * 4 + k - t.ct * deep;
+            t.pos = __builtin_amdgcn_readlane(sh.pos[c], l);
+            t.rows = __builtin_amdgcn_readlane(sh.n[c], l);
+        }
+        run += __builtin_amdgcn_readlane(inc, kWave - 1);
+    }
+    id -= run * cols;
+    if (t.e < 0) {
+        int nth = div_cols(p, id);
+        t.ct = id - nth * cols;
+#pragma unroll
+        for (int k = 3; k > 0; --k) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const bool in = c * kWave + lane >= w0 && c * kWave + lane < w1;
+                const uint64_t some = __ballot(in && size[c] == k);
+                const int all = __popcll(some);
+                if (t.e < 0 && nth < all) {
+                    const int l = nth_bit(some, nth);
+                    t.e = c * kWave + l;
+                    t.pos = __builtin_amdgcn_readlane(sh.pos[c], l);
+                    t.rows = __builtin_amdgcn_readlane(sh.n[c], l);
+                    rt = t.rows / kRingRows;
+                }
+                nth -= all;
+            }
+        }
+    }
+    t.pos += rt * kRingRows;
+    t.rows = min(kRingRows, t.rows - rt * kRingRows);
     return t;
 }
 
 // ---------------------------------------------------------------- few rows a share
-// Work unit = (expert with at least one pair, 16 NR output columns) for all of the
+// Work unit = (expert with at least one pair, 32 output columns) for all of the
 // expert's rows, 16 TB at a time; K over eight wavefronts in blocks of 128 bytes,
 // whose partial sums join through LDS.  What bounds it: the touched experts' rows
 // of W, read once; they stream past the few rows of x.  Both are read as whole
 // 128-byte segments and change lanes through LDS (row_stage.hpp).
 constexpr int kFewThreads = 512;
 constexpr int kFewWaves = kFewThreads / kWave;
+constexpr int kFewCols = 32;
 
-constexpr int few_stage(int TB, int NR) {
-    return (NR + 1) * 128 > NR * TB * kWave ? (NR + 1) * 128 : NR * TB * kWave;
-}
-
-template <typename F, int TB, int NR>
-__global__ __launch_bounds__(kFewThreads, TB * NR == 8 ? 2 : 4) void k_experts_few(ExpertsParams p) {
-    constexpr int kStage = few_stage(TB, NR);
+template <typename F, int TB>
+__global__ __launch_bounds__(kFewThreads, 4) void k_experts_few(ExpertsParams p) {
+    constexpr int NR = kFewCols / 16;
+    constexpr int kStage = (NR + 1) * 128;           // uint4 of a wavefront: rows of W and of x, later its sums
+    static_assert(NR * TB * kWave <= kStage, "sums fit the stage");
     __shared__ uint4 smem[kFewWaves * kStage];
     const int tid = threadIdx.x;
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int lr = lane % 16, lq = lane / 16;
-    const Tile tile = find_tile(p.offsets, p.E, p.P, 1 << 24, p.col_tiles, blockIdx.x);
+    const int nth = div_cols(p, (int)blockIdx.x);
+    const Tile tile = p.E <= kWave ? find_share<1>(p, nth) : find_share<kGroupMaxE / kWave>(p, nth);
     if (tile.e < 0) return;
-    const int n0 = (int)tile.in * 16 * NR, n1 = min(n0 + 16 * NR, p.N);
+    const int n0 = ((int)blockIdx.x - nth * p.col_tiles) * 16 * NR, n1 = min(n0 + 16 * NR, p.N);
     const int Kb = p.Kb, KB = (Kb + 127) / 128;
     const int64_t row0 = (int64_t)tile.e * p.N + n0;
     const __amdgpu_buffer_rsrc_t rw = uniform_rsrc(p.W + row0 * Kb, (uint32_t)((n1 - n0) * Kb));
@@ -214,7 +321,10 @@ __global__ __launch_bounds__(kFewThreads, TB * NR == 8 ? 2 : 4) void k_experts_f
 #pragma unroll
     for (int i = 0; i < 2 * NR; ++i)
         off_w[i] = (uint32_t)(min(8 * i + lane / 8, n1 - n0 - 1) * Kb) + (lane % 8) * 16;
-    constexpr int U = TB * NR == 8 ? 4 : 4 / NR, UX = TB * NR == 8 ? 2 : TB == 1 ? U : 4 / TB;
+    // blocks in flight: W comes from HBM, x from L2.  A second block of x where 128
+    // registers hold it (spilled, 8 x (4096, 14336) in e4m3 took 93 and 102 us, with one
+    // block 75 and 77).
+    constexpr int U = 2, UX = TB == 1 && F::kWords == 1 ? 2 : 1;
     uint4 vw[U][2 * NR], vx[UX][2 * TB];
     uint32_t off_x[2 * TB];
     auto load_w = [&](int q, int kb) {
@@ -247,18 +357,11 @@ __global__ __launch_bounds__(kFewThreads, TB * NR == 8 ? 2 : 4) void k_experts_f
 #pragma unroll
         for (int i = 0; i < 2 * TB; ++i) {
             const uint32_t f = min(f_row[i], (uint32_t)p.P - 1);
-            const uint32_t row = p.x_div > 1 ? f / (uint32_t)p.x_div : f;
-            off_x[i] = 8 * i + lane / 8 < rows ? row * (uint32_t)p.ldx + (lane % 8) * 16 : kBufOff;
+            off_x[i] = 8 * i + lane / 8 < rows ? pair_row(p, f) * (uint32_t)p.ldx + (lane % 8) * 16 : kBufOff;
         }
         f_out = min(f_out, (uint32_t)p.P - 1);
 #pragma unroll
         for (int q = 0; q < UX; ++q) load_x(q, wave + q * kFewWaves);
-        float xs = 1.f, ws[4] = {1.f, 1.f, 1.f, 1.f};
-        if (F::kScaled && wave < NR * TB) {
-            xs = p.x_scale[p.x_div > 1 ? f_out / (uint32_t)p.x_div : f_out];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) ws[q] = p.w_scale[(int64_t)tile.e * p.N + min(n + q, p.N - 1)];
-        }
         typename F::Acc16 sum[NR][TB];
 #pragma unroll
         for (int r = 0; r < NR; ++r)
@@ -290,6 +393,12 @@ __global__ __launch_bounds__(kFewThreads, TB * NR == 8 ? 2 : 4) void k_experts_f
                 load_x(q % UX, b0 + (q + UX) * kFewWaves);
             }
         }
+        float xs = 1.f, ws[4] = {1.f, 1.f, 1.f, 1.f};
+        if (F::kScaled && wave < NR * TB) {
+            xs = p.x_scale[pair_row(p, f_out)];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) ws[q] = p.w_scale[(int64_t)tile.e * p.N + min(n + q, p.N - 1)];
+        }
         // join the eight partial sums in a fixed order; four columns of a row a lane
         typedef typename F::Acc16 acc_t;
         acc_t* red = reinterpret_cast<acc_t*>(st);
@@ -316,300 +425,109 @@ __global__ __launch_bounds__(kFewThreads, TB * NR == 8 ? 2 : 4) void k_experts_f
 // Work unit = (up to 256 consecutive positions of one expert's share, 256 output
 // columns), four waves, one per SIMD, K in stages of 128 bytes a row.
 //
-// Both operands go from global memory straight to LDS (no registers, no LDS write
-// instructions), whole 128-byte row segments: eight lanes a row, the chunk that a
-// lane reads permuted so that chunk c of row r comes to stand at c ^ (r / 2) % 8,
-// where operand reads (32 rows, one chunk) meet distinct banks.  Rings of XD
-// stages of x and WD of W fill the 160 KB; the loads of a stage are spread evenly
-// between the MFMAs of the one before, x first.  The operands of the last K step of
-// a stage are in registers one step early, so the one barrier of a stage stands in
-// front of that step: behind it the stage's slots are free for the next loads and
-// the following stage can be read, and no MFMA waits for either.
-//
-// A share's last tile has fewer rows: the waves of a unit with up to 192, 128 or 64
-// rows take 96 x 128, 128 x 64 and 64 x 64 outputs each instead of 128 x 128, with
-// as many fewer MFMAs, and rings as deep as 160 KB allow.
-//
-// The loads to LDS are written in assembly because the compiler waits for all of
-// them at every LDS read; they have no output registers, and the waits that their
-// data needs stand in turn().
-typedef __attribute__((address_space(3))) char lds_char_t;
+// The main loop and the forms for tiles with fewer rows (a share's last ones) stand
+// in ring_product.hpp.
 
-__device__ __forceinline__ void dma_global(const char* p, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory");
-}
-__device__ __forceinline__ void dma_buffer(u32x4_vt r, uint32_t voff, uint32_t soff, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff), "s"(r),
-                 "s"(soff)
-                 : "memory");
-}
-
-constexpr int kShareThreads = 256;
-constexpr int kShareRows = 256, kShareCols = 256;
-constexpr int kShareLds = 160 * 1024;
-
-template <typename F, int WM, int RB, int CB, int XD, int WD>
-__device__ __forceinline__ void tile_product(const ExpertsParams& p, uint4* smem, int e, int pos, int rows, int n0) {
-    constexpr int kRows = 32 * RB * WM, WN = 4 / WM;
-    static_assert(32 * CB * WN == kShareCols, "four waves share the columns");
-    constexpr int kX = kRows * 128, kW = kShareCols * 128;          // bytes of a ring slot
-    static_assert(XD >= 2 && WD >= XD && XD * kX + WD * kW <= kShareLds, "rings fit the LDS");
-    constexpr int NX = kRows / 32, NW = kShareCols / 32;            // loads of a wave and stage
-    constexpr int kLoads = NX + NW;
-    constexpr int kWords = F::kWords, MF = RB * CB;
-    constexpr int kTotal = MF * (kWords == 1 ? 4 : 2);             // MFMAs of a stage
-    constexpr int kPost = kWords == 1 ? MF : kTotal - MF / 2;      // of them behind the barrier
-    constexpr int kReads = (RB + CB) * kWords;                     // operand reads of a step
-    constexpr int kEarly = (kPost * kLoads + kTotal - 1) / kTotal; // loads issued behind the barrier
-    // what may still be on its way when a stage is read: the stages after it
-    constexpr int kAhead = (XD - 2) * NX + (WD - 2) * NW;
-
+template <typename R>
+__device__ __forceinline__ void share_tile(const ExpertsParams& p, uint4* smem, const Tile& t) {
+    const int e = t.e, pos = t.pos, rows = t.rows, n0 = t.ct * kRingCols;
+    typedef typename R::F F;
+    constexpr int RB = R::RB, CB = R::CB, NX = R::NX;
     const int tid = threadIdx.x;
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int lr = lane % 32, lh = lane / 32;
-    const int cols = min(kShareCols, p.N - n0);
-    const int Kb = p.Kb, nk = (Kb + 127) / 128;
-
-    // ---- loads: wave w takes the 8-row blocks w + 4 i, lane l row l / 8 of a block
-    const int ch = ((lane % 8) ^ (lane / 16 + 4 * (wave & 1))) * 16;   // the lane's bytes of a 128-byte segment
-    const int lrow = 8 * wave + lane / 8;
+    const int cols = min(kRingCols, p.N - n0);
     uint32_t f_in[NX];
 #pragma unroll
-    for (int i = 0; i < NX; ++i) f_in[i] = (uint32_t)p.pairs[pos + min(lrow + 32 * i, rows - 1)];
+    for (int i = 0; i < NX; ++i) f_in[i] = (uint32_t)p.pairs[pos + min(R::load_row(wave, i), rows - 1)];
     uint32_t f_out = (uint32_t)p.pairs[pos + min(tid, rows - 1)];
-    const uint64_t wa = (uint64_t)(uintptr_t)(p.W + ((int64_t)e * p.N + n0) * Kb);
-    const u32x4_vt rw = {(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)wa),
-                         (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(wa >> 32)),
-                         (uint32_t)__builtin_amdgcn_readfirstlane(cols * Kb), 0x00020000u};
-    uint32_t woff[NW];
-#pragma unroll
-    for (int i = 0; i < NW; ++i) woff[i] = (uint32_t)(min(lrow + 32 * i, cols - 1) * Kb + ch);
-    const char* xp[NX];
-    const char* const zeros = reinterpret_cast<const char*>(&k_zeros);
-    const uint32_t dst = (uint32_t)(uintptr_t)(lds_char_t*)smem + wave * 1024;
-
-    // the loads under way: stage sx of x into ring slot lx, stage sw of W into lw
-    int lx = 0, lw = 0, inc = 0;
-    uint32_t so = 0;
-    bool win = true;
-    auto begin_x = [&](int st, int slot) {
-        lx = slot;
-        inc = st + 1 < nk ? 128 : 0;                 // stages past the last read it again
-        if (st == nk - 1 && Kb % 128 != 0) {
-#pragma unroll
-            for (int i = 0; i < NX; ++i) xp[i] = st * 128 + ch < Kb ? xp[i] : zeros;
-        }
-    };
-    auto begin_w = [&](int st, int slot) {
-        lw = slot;
-        so = (uint32_t)st * 128u;
-        win = st * 128 + ch < Kb;                    // past K: zeros, and no memory is touched
-    };
-    auto load_x = [&](int i) {
-        dma_global(xp[i], dst + lx + i * 4096);
-        xp[i] += inc;
-    };
-    auto load_w = [&](int i) { dma_buffer(rw, win ? woff[i] : kBufOff, so, dst + lw + i * 4096); };
-    auto load_at = [&](int at) {                     // the loads due after MFMA `at` behind the barrier
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            if (j * kTotal / kLoads != at) continue;
-            if (j < NX) load_x(j);
-            else load_w(j - NX);
-        }
-    };
-    int xs[XD], wsl[WD];                             // ring slots of stages s, s + 1, ..
-#pragma unroll
-    for (int i = 0; i < XD; ++i) xs[i] = i * kX;
-#pragma unroll
-    for (int i = 0; i < WD; ++i) wsl[i] = XD * kX + i * kW;
-
-    // prologue: W first, whose addresses need no pair
-    begin_w(0, wsl[0]);
-#pragma unroll
-    for (int i = 0; i < NW; ++i) load_w(i);
-#pragma unroll
-    for (int i = 0; i < NX; ++i) {
-        const uint32_t f = min(f_in[i], (uint32_t)p.P - 1);     // whatever the list holds, a row of the batch
-        xp[i] = p.x + (int64_t)(p.x_div > 1 ? f / (uint32_t)p.x_div : f) * p.ldx + ch;
-    }
-    f_out = min(f_out, (uint32_t)p.P - 1);
     float my_xs = 1.f, my_ws = 1.f;
-    if constexpr (F::kScaled) {
-        my_xs = p.x_scale[p.x_div > 1 ? f_out / (uint32_t)p.x_div : f_out];
-        my_ws = p.w_scale[(int64_t)e * p.N + n0 + min(tid, cols - 1)];
-    }
+    auto x_rows = [&](const char* (&xp)[NX]) {
+        // whatever the list holds, a row of the batch
 #pragma unroll
-    for (int st = 0; st < WD - 1; ++st) {
-        if (st < XD - 1) {
-            begin_x(st, xs[st]);
-#pragma unroll
-            for (int i = 0; i < NX; ++i) load_x(i);
+        for (int i = 0; i < NX; ++i)
+            xp[i] = p.x + (int64_t)pair_row(p, min(f_in[i], (uint32_t)p.P - 1)) * p.ldx + R::load_byte(wave);
+        f_out = min(f_out, (uint32_t)p.P - 1);
+        if constexpr (F::kScaled) {
+            my_xs = p.x_scale[pair_row(p, f_out)];
+            my_ws = p.w_scale[(int64_t)e * p.N + n0 + min(tid, cols - 1)];
         }
-        if (st > 0) {
-            begin_w(st, wsl[st]);
-#pragma unroll
-            for (int i = 0; i < NW; ++i) load_w(i);
-        }
-    }
-    begin_x(XD - 1, xs[XD - 1]);
-    begin_w(WD - 1, wsl[WD - 1]);
-#pragma unroll
-    for (int i = 0; i < kPost; ++i) load_at(i);
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kAhead + kEarly) : "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    };
+    typename R::Acc acc[RB][CB];
+    ring_product<R>(smem, p.W + ((int64_t)e * p.N + n0) * p.Kb, p.Kb, cols, p.Kb, t.ct / 8 % 8 * ((p.Kb + 127) / 128) / 8, x_rows, acc);
 
-    // ---- operands: 16-byte chunks of rows lr of the wave's blocks
-    const char* const lds = reinterpret_cast<const char*>(smem);
-    int get[4];                                      // [step, word]
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const int chunk = kWords == 1 ? 2 * c + lh : 4 * (c / 2) + 2 * (c % 2) + lh;
-        get[c] = lr * 128 + (chunk ^ (lr / 2 % 8)) * 16;
-    }
-    const int xpart = wave / WN * RB * 4096, wpart = wave % WN * CB * 4096;
-    struct Ops {
-        uint4 x[RB][kWords], w[CB][kWords];
-    };
-    auto read1 = [&](Ops& o, int x0, int w0, int t, int j) {
-        const int b = j / kWords, h = j % kWords, c = t * kWords + h;
-        if (b < CB) o.w[b][h] = *reinterpret_cast<const uint4*>(lds + (w0 + wpart + get[c]) + b * 4096);
-        else o.x[b - CB][h] = *reinterpret_cast<const uint4*>(lds + (x0 + xpart + get[c]) + (b - CB) * 4096);
-    };
-    typename F::Acc32 acc[RB][CB];
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb)
-#pragma unroll
-            for (int q = 0; q < 16; ++q) acc[rb][cb][q] = 0;
-    auto mfma1 = [&](const Ops& o, int i) {
-        const int rb = i / CB, cb = i % CB;
-        acc[rb][cb] = F::mma32_step(o.w[cb], o.x[rb], acc[rb][cb]);
-    };
-    Ops oa, ob;
-#pragma unroll
-    for (int j = 0; j < kReads; ++j) read1(oa, xs[0], wsl[0], 0, j);
-
-    // The one barrier of stage s: the operands of its last step are in registers
-    // (lgkmcnt), so its ring slots are free behind it; the stages up to s + 1 have
-    // arrived, in every wave.
-    auto turn = [&](int s) {
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kAhead) : "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        begin_x(s + XD, xs[0]);
-        begin_w(s + WD, wsl[0]);
-        __builtin_amdgcn_sched_barrier(0);
-    };
-    // MFMAs [i0, i1) of a step, number `at` and on behind the barrier, with `reads`
-    // (a step's operands into o, spread evenly) and the loads that are due
-    auto run = [&](const Ops& cur, int i0, int i1, int at, Ops* next, int x0, int w0, int t) {
-#pragma unroll
-        for (int i = i0; i < i1; ++i) {
-            mfma1(cur, i);
-            if (next)
-#pragma unroll
-                for (int j = 0; j < kReads; ++j)
-                    if (i0 + j * (i1 - i0) / kReads == i) read1(*next, x0, w0, t, j);
-            load_at(at + i - i0);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    };
-    for (int s = 0; s < nk; ++s) {
-        if constexpr (kWords == 1) {
-            run(oa, 0, MF, kPost, &ob, xs[0], wsl[0], 1);
-            run(ob, 0, MF, kPost + MF, &oa, xs[0], wsl[0], 2);
-            run(oa, 0, MF, kPost + 2 * MF, &ob, xs[0], wsl[0], 3);
-            turn(s);
-            run(ob, 0, MF, 0, &oa, xs[1], wsl[1], 0);
-        } else {
-            run(oa, 0, MF / 2, kPost, &ob, xs[0], wsl[0], 1);
-            turn(s);
-            run(oa, MF / 2, MF, 0, nullptr, 0, 0, 0);
-            run(ob, 0, MF, MF - MF / 2, &oa, xs[1], wsl[1], 0);
-        }
-        const int x0 = xs[0], w0 = wsl[0];
-#pragma unroll
-        for (int i = 0; i + 1 < XD; ++i) xs[i] = xs[i + 1];
-        xs[XD - 1] = x0;
-#pragma unroll
-        for (int i = 0; i + 1 < WD; ++i) wsl[i] = wsl[i + 1];
-        wsl[WD - 1] = w0;
-    }
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    __syncthreads();                                 // the rings are free
-
-    // ---- scales, one rounding, whole row pieces through LDS
-    constexpr int kStaged = kShareRows * kShareCols * 2;
-    int* const s_f = reinterpret_cast<int*>(reinterpret_cast<char*>(smem) + kStaged);
-    float* const s_xs = reinterpret_cast<float*>(s_f + kShareRows);
-    float* const s_ws = s_xs + kShareRows;
+    // ---- scales, one rounding
+    int* const s_f = reinterpret_cast<int*>(smem);
+    float* const s_xs = reinterpret_cast<float*>(s_f + kRingRows);
+    float* const s_ws = s_xs + kRingRows;
     s_f[tid] = tid < rows ? (int)f_out : -1;
     s_xs[tid] = my_xs;
     s_ws[tid] = my_ws;
     __syncthreads();
-    const int r0 = wave / WN * RB * 32, c0 = wave % WN * CB * 32;
-    constexpr int kCh = CB * 4;                      // 16-byte chunks of a wave's row
-    auto swz = [](int row) { return kCh == 16 ? row % 16 : row / 2 % 8; };
-    uint16_t* const so16 = reinterpret_cast<uint16_t*>(smem) + wave * RB * 32 * CB * 32;
+    const int r0 = R::row0(wave), c0 = R::col0(wave);
+    uint16_t* dst[RB][2];
+    bool ok[RB][2];
+    float rs[RB];
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
-        const int row = rb * 32 + lr;
-        const float rs = F::kScaled ? s_xs[r0 + row] : 1.f;
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                float v[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] = (float)acc[rb][cb][4 * g + q];
-                if constexpr (F::kScaled) {
-                    const float4 ws = *reinterpret_cast<const float4*>(s_ws + c0 + cb * 32 + 8 * g + 4 * lh);
-                    v[0] *= rs * ws.x;
-                    v[1] *= rs * ws.y;
-                    v[2] *= rs * ws.z;
-                    v[3] *= rs * ws.w;
-                }
-                *reinterpret_cast<uint2*>(so16 + row * CB * 32 + ((cb * 4 + g) ^ swz(row)) * 8 + lh * 4) =
-                    make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-            }
+        for (int h = 0; h < 2; ++h) {
+            const int f = s_f[r0 + rb * 32 + 16 * h + lane % 16];
+            ok[rb][h] = f >= 0;
+            dst[rb][h] = p.y + (int64_t)max(f, 0) * p.ldy + n0 + c0 + 8 * store_chunk();
+        }
+        rs[rb] = s_xs[r0 + rb * 32 + lr];
     }
-    stage_order();                                   // a wave reads back what it wrote itself
 #pragma unroll
-    for (int j = 0; j < RB * 32 * kCh / kWave; ++j) {
-        const int row = j * (kWave / kCh) + lane / kCh, c = lane % kCh;
-        const uint4 v = *reinterpret_cast<const uint4*>(so16 + row * CB * 32 + (c ^ swz(row)) * 8);
-        const int f = s_f[r0 + row], n = c0 + c * 8;
-        if (f >= 0 && n < cols) *reinterpret_cast<uint4*>(p.y + (int64_t)f * p.ldy + n0 + n) = v;
+    for (int cb = 0; cb < CB; ++cb) {
+        const bool in = c0 + cb * 32 + 8 * store_chunk() < cols;       // N is a multiple of 8
+        float4 ws[4];
+        if constexpr (F::kScaled)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) ws[g] = *reinterpret_cast<const float4*>(s_ws + c0 + cb * 32 + 8 * g + 4 * lh);
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) {
+            f32x16_t v;
+#pragma unroll
+            for (int q = 0; q < 16; ++q) v[q] = (float)acc[rb][cb][q];
+            if constexpr (F::kScaled)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    v[4 * g] *= rs[rb] * ws[g].x;
+                    v[4 * g + 1] *= rs[rb] * ws[g].y;
+                    v[4 * g + 2] *= rs[rb] * ws[g].z;
+                    v[4 * g + 3] *= rs[rb] * ws[g].w;
+                }
+            store_block(v, {dst[rb][0] + cb * 32, dst[rb][1] + cb * 32}, {ok[rb][0] && in, ok[rb][1] && in});
+        }
     }
 }
 
 template <typename F>
-__global__ __launch_bounds__(kShareThreads, 1) void k_experts_tile(ExpertsParams p) {
-    __shared__ uint4 smem[kShareLds / 16];
+__global__ __launch_bounds__(kRingThreads, 1) void k_experts_tile(ExpertsParams p) {
+    __shared__ uint4 smem[kRingLds / 16];
     // 32 tiles in a row (four row tiles by eight column tiles of an expert) to each
     // of the eight L2s, every eighth workgroup on one of them
     const int v = (int)blockIdx.x / 8;
-    const int64_t id = (int64_t)(v / 32) * 256 + (int)blockIdx.x % 8 * 32 + v % 32;
-    const Tile t = find_tile(p.offsets, p.E, p.P, kShareRows, p.col_tiles, id);
+    const int id = v / 32 * 256 + (int)blockIdx.x % 8 * 32 + v % 32;
+    const Tile t = p.E <= kWave ? find_tile<1>(p, id) : find_tile<kGroupMaxE / kWave>(p, id);
     if (t.e < 0) return;
-    const int band = (int)(t.in / (4 * p.col_tiles)), in = (int)(t.in % (4 * p.col_tiles));
-    const int deep = min(4, t.rts - band * 4);
-    const int rt = band * 4 + in % deep, n0 = in / deep * kShareCols;
-    const int pos = t.pos + rt * kShareRows, rows = min(kShareRows, t.rows - rt * kShareRows);
-    if (rows > 192) tile_product<F, 2, 4, 4, 2, 3>(p, smem, t.e, pos, rows, n0);
-    else if (rows > 128) tile_product<F, 2, 3, 4, 2, 3>(p, smem, t.e, pos, rows, n0);
-    else if (rows > 64) tile_product<F, 1, 4, 2, 3, 3>(p, smem, t.e, pos, rows, n0);
-    else tile_product<F, 1, 2, 2, 4, 4>(p, smem, t.e, pos, rows, n0);
+    if (t.rows > 192) share_tile<Ring256<F>>(p, smem, t);
+    else if (t.rows > 128) share_tile<Ring192<F>>(p, smem, t);
+    else if (t.rows > 64) share_tile<Ring128<F>>(p, smem, t);
+    else share_tile<Ring64<F>>(p, smem, t);
 }
 
 // ---------------------------------------------------------------- launch
-template <typename F, int TB, int NR> hipError_t launch_few(ExpertsParams& p, hipStream_t st) {
-    p.col_tiles = (p.N + 16 * NR - 1) / (16 * NR);
+static void set_cols(ExpertsParams& p, int width) {
+    p.col_tiles = (p.N + width - 1) / width;
+    p.cols_inv = (uint32_t)(((1ull << 32) + p.col_tiles - 1) / p.col_tiles);   // (unused for one)
+}
+
+template <typename F, int TB> hipError_t launch_few(ExpertsParams& p, hipStream_t st) {
+    set_cols(p, kFewCols);
     const int shares = p.E < p.P ? p.E : p.P;
-    hipLaunchKernelGGL((k_experts_few<F, TB, NR>), dim3((unsigned)((int64_t)shares * p.col_tiles)), dim3(kFewThreads), 0,
+    hipLaunchKernelGGL((k_experts_few<F, TB>), dim3((unsigned)((int64_t)shares * p.col_tiles)), dim3(kFewThreads), 0,
                        st, p);
     return hipGetLastError();
 }
@@ -617,13 +535,26 @@ template <typename F, int TB, int NR> hipError_t launch_few(ExpertsParams& p, hi
 template <typename F> hipError_t launch_experts_as(ExpertsParams& p, hipStream_t st) {
     const int shares = p.E < p.P ? p.E : p.P;
     const int64_t extent = (int64_t)(p.x_rows - 1) * p.ldx + p.Kb;
-    if (p.P <= 16 * shares && extent < INT32_MAX) {
-        if (p.P <= 8 * shares) return launch_few<F, 1, 1>(p, st);
-        return launch_few<F, 2, 1>(p, st);
+    // The streaming form as long as 16 or 32 rows at a time take in most shares; it
+    // reads a share's W again for every further 16 or 32.  Past 8 rows a share only
+    // where the tiles would leave compute units without one.  Measured in graphs over
+    // several weights, equal shares, 16 rows at a time, 32, tiles; us:
+    //   8 x (28672, 4096), 4 rows: bf16 305 / 327 / 331, e4m3 163 / 173 / 180, int8 162 /
+    //     172 / 178; 16 rows: 325 / 328 / 337, 176 / 183 / 182, 174 / 183 / 181
+    //   8 x (4096, 14336), 4 rows: 143 / 147 / 203, 70 / 71 / 104, 70 / 72 / 103; 16 rows:
+    //     153 / 156 / 207, 75 / 77 / 106, 76 / 77 / 106; 32 rows: - / 179 / 212, - / 92 / 109,
+    //     - / 91 / 109
+    //   40 x (2848, 2064), 8 rows: 111 / 113 / 119, 65 / 70 / 62, 66 / 68 / 61; 4 of the 40
+    //     with 1 row: 17 / 18 / 45, 11 / 12 / 21, 11 / 11 / 21
+    // (shares that differ need the 32 from 8 rows on average).
+    const int64_t units = (int64_t)shares * ((p.N + kRingCols - 1) / kRingCols);
+    if (extent < INT32_MAX) {
+        if (p.P <= 8 * shares) return launch_few<F, 1>(p, st);
+        if (p.P <= 16 * shares && units < 256) return launch_few<F, 2>(p, st);
     }
-    p.col_tiles = (p.N + kShareCols - 1) / kShareCols;
-    const int64_t tiles = ((int64_t)p.P / kShareRows + shares) * p.col_tiles;
-    hipLaunchKernelGGL((k_experts_tile<F>), dim3((unsigned)((tiles + 255) / 256 * 256)), dim3(kShareThreads), 0, st, p);
+    set_cols(p, kRingCols);
+    const int64_t tiles = ((int64_t)p.P / kRingRows + shares) * p.col_tiles;
+    hipLaunchKernelGGL((k_experts_tile<F>), dim3((unsigned)((tiles + 255) / 256 * 256)), dim3(kRingThreads), 0, st, p);
     return hipGetLastError();
 }
 

@@ -89,6 +89,12 @@ struct GemmFp8Params {
     int seg_stride;              // ceil((L + 1) / 64): first-round search stride
 };
 
+}  // namespace mlora
+
+#include "gemm_ring.hpp"
+
+namespace mlora {
+
 template <typename F, typename G>
 __global__ __launch_bounds__(kGThreads, G::Waves) void k_gemm_8bit(GemmFp8Params p) {
     constexpr int kGM = G::M, kGN = G::N, kGXL = G::XL, kGWL = G::WL, kGRB = G::RB, kGCB = G::CB;
@@ -556,8 +562,21 @@ hipError_t launch_gemm_8bit(const LinearArgs& a, const void* x8, int64_t ldx8, c
     // keep the grid below 2^32 threads.)
     const int64_t ns = columns(128), nl = columns(256), K = a.K;
     const int64_t small = ((a.M + 63) / 64 * ns + 255) / 256, large = ((a.M + 127) / 128 * nl + 255) / 256;
-    if (small <= 4096 && small * (14 * 4096 + 85 * K) < large * (80 * 4096 + 200 * K))
-        return launch_gemm_8bit_as<F, G8Shape<2, 1>>(p, st);
+    const int64_t cost_s = small <= 4096 ? small * (14 * 4096 + 85 * K) : INT64_MAX;
+    const int64_t cost_l = large * (80 * 4096 + 200 * K);
+    // Tiles of 256 x 256 (gemm_ring.hpp) run at 2.7 PFLOP/s and more and lose most where
+    // they do not fill the chip: a round takes 1.3 (K = 512) to 1.65 (K = 4096) times one
+    // of the large units.  Measured calls in int8, the units' better choice against tiles
+    // (8 adapters): K = 512, 512 x 28672 33.9 / 33.7 us; K = 1024, 1024 x 14336 40.0 / 37.8;
+    // K = 2048, 768 x 8192 34.7 / 52.4; K = 4096, 300 x 28672 82.5 / 75.6, 512 x 28672 (12
+    // adapters, 36 runs) 107 / 90, 2048 x 4096 59.8 / 85.5, 4096 x 4096 105 / 88, 8192 x 4096
+    // 200 / 165, 2048 x 28672 312 / 286; K = 8192, 1024 x 8192 92 / 135.  In e4m3 4096 x 4096
+    // 98 / 86, 8192 x 4096 170 / 144, 512 x 28672 101 / 87, 2048 x 4096 55 / 79.  The sums
+    // are the same bits either way.
+    const int64_t tiles = (int64_t)((a.M + kRingRows - 1) / kRingRows) * nl;
+    const int64_t cost_r = tiles <= (1 << 22) ? (tiles + 255) / 256 * (130 * 4096 + 330 * K) : INT64_MAX;
+    if (cost_r < cost_s && cost_r < cost_l) return launch_gemm_ring<F>(p, st);
+    if (cost_s < cost_l) return launch_gemm_8bit_as<F, G8Shape<2, 1>>(p, st);
     return launch_gemm_8bit_as<F, G8Shape<4, 2>>(p, st);
 }
 

@@ -238,7 +238,8 @@ hipError_t launch_linear_8bit_many(bool int8, const LinearArgs& a, const void* W
                                    float* S, void* y, int64_t ldy, void* ws, hipStream_t st);
 
 // Pairs by expert, and the experts' products over their shares (experts.hpp).
-// Rows of W and x in bytes: Kb of values, x rows ldx apart; x row of pair f: f / x_div.
+// Rows of W and x in bytes: Kb of values, x rows ldx apart; x_inv: 2^32 / topk rounded
+// up where x has a row per token, 0 where it has one per pair.
 struct ExpertsParams {
     const char* W;
     const float* w_scale;
@@ -250,8 +251,10 @@ struct ExpertsParams {
     uint16_t* y;
     int64_t ldy;
     int E, N, Kb, P;
-    int x_div, x_rows;
+    uint32_t x_inv;
+    int x_rows;
     int col_tiles;
+    uint32_t cols_inv;      // 2^32 / col_tiles, rounded up
 };
 
 hipError_t launch_moe_group(const int32_t* topk_ids, int P, int E, int32_t* pairs, int32_t* offsets,

@@ -152,6 +152,11 @@ CASES = {
     "rows_elsewhere": (900, 2, 5, 136, 144, [300, 0, 20, 200, 1], False),
     "nothing_here": (40, 2, 3, 16, 32, [0, 0, 0], False),
     "wide": (70, 2, 2, 2312, 128, None, True),
+    "tiles_in_order": (600, 2, 6, 20008, 16, [300, 64, 0, 200, 513, 90], False),
+    "tiles_in_order_many_experts": (1500, 2, 130, 1096, 32, None, False),
+    "few_256_experts": (500, 4, 256, 40, 48, None, True),
+    "few_32_rows": (64, 2, 8, 24, 272, [30, 2, 33, 1, 31, 0, 16, 15], False),
+    "few_one_expert_of_many": (300, 1, 200, 72, 160, [0] * 150 + [300], False),
 }
 
 
