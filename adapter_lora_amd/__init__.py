@@ -737,23 +737,31 @@ class MoeGroups:
         self.E, self.count, self.topk = int(E), 0, 0
         self.pairs = torch.empty(max(int(pairs_cap), 1), dtype=_I32, device=device)
         self.offsets = torch.zeros(self.E + 1, dtype=_I32, device=device)
+        self.cap, self.device = self.pairs.shape[0], self.pairs.get_device()
+        self.pairs_ptr, self.offsets_ptr = _ptr(self.pairs), _ptr(self.offsets)
 
 
 def lora_moe_group(topk_ids: torch.Tensor, groups: MoeGroups, stream=None) -> None:
     """The pairs of topk_ids int32 [M, topk] in the experts' order: groups.pairs
     holds pair indices m * topk + k by ascending expert, groups.offsets where
     each expert's begin; ids outside [0, E) come last and belong to no share."""
-    if topk_ids.dtype is not _I32 or topk_ids.dim() != 2 or not topk_ids.is_contiguous():
+    shape = topk_ids.shape
+    if topk_ids.dtype is not _I32 or len(shape) != 2 or not topk_ids.is_contiguous():
         raise LoraError("topk_ids must be a contiguous int32 tensor [M, topk]")
-    M, topk = topk_ids.shape
-    dev = topk_ids.get_device()
-    if M * topk > groups.pairs.shape[0]:
-        raise LoraError(f"the groups hold {groups.pairs.shape[0]} pairs, {M * topk} needed")
-    if dev < 0 or groups.pairs.get_device() != dev:
+    M, topk = shape
+    count, dev = M * topk, topk_ids.get_device()
+    if count > groups.cap:
+        raise LoraError(f"the groups hold {groups.cap} pairs, {count} needed")
+    if dev < 0 or groups.device != dev:
         raise LoraError("topk_ids and the groups must live on one GPU")
-    check(lib.lora_moe_group(topk_ids.data_ptr(), M, topk, groups.E, groups.pairs.data_ptr(),
-                             groups.offsets.data_ptr(), _stream_on(dev, stream)), "lora_moe_group")
-    groups.count, groups.topk = M * topk, topk
+    status = lib.lora_moe_group(topk_ids.data_ptr(), M, topk, groups.E, groups.pairs_ptr, groups.offsets_ptr,
+                                _stream_on(dev, stream))
+    if status:
+        check(status, "lora_moe_group")
+    groups.count, groups.topk = count, topk
+
+
+_EXPERT_TYPES = {torch.bfloat16: LORA_BF16, E4M3: LORA_E4M3, torch.int8: LORA_INT8}
 
 
 def lora_moe_linear(W: torch.Tensor, x: torch.Tensor, topk: int, groups: MoeGroups, y: torch.Tensor,
@@ -764,21 +772,17 @@ def lora_moe_linear(W: torch.Tensor, x: torch.Tensor, topk: int, groups: MoeGrou
     in e4m3 or int8 with w_scale [E, N] and x_scale (one a row of x); x of W's
     type, one row per token (r = f // topk) or one per pair (r = f); y bfloat16,
     one row per pair.  Rows of y whose pair has no share are left as they are."""
-    dtype = W.dtype
-    if dtype is torch.bfloat16:
-        code = LORA_BF16
-    elif dtype is _I8:
-        code = LORA_INT8
-    elif dtype is E4M3:
-        code = LORA_E4M3
-    else:
+    dtype, shape = W.dtype, W.shape
+    code = _EXPERT_TYPES.get(dtype)
+    if code is None:
         raise LoraError(f"unsupported dtype {dtype}")
-    if W.dim() != 3 or W.shape[0] != groups.E or not W.is_contiguous():
+    if len(shape) != 3 or shape[0] != groups.E or not W.is_contiguous():
         raise LoraError(f"W must be a contiguous tensor [E, N, K] of the groups' {groups.E} experts")
-    E, N, K = W.shape
-    if x.dim() != 2 or y.dim() != 2:
+    E, N, K = shape
+    xs, ys = x.shape, y.shape
+    if len(xs) != 2 or len(ys) != 2:
         raise LoraError("x and y must be 2-D tensors")
-    P, rows = y.shape[0], x.shape[0]
+    P, rows = ys[0], xs[0]
     if P != groups.count or (P and topk != groups.topk):
         raise LoraError(f"the groups were made for {groups.count} pairs with top-{groups.topk}, y has {P} rows")
     if topk < 1 or P % topk or rows not in (P, P // topk):
@@ -794,12 +798,14 @@ def lora_moe_linear(W: torch.Tensor, x: torch.Tensor, topk: int, groups: MoeGrou
         if w_scale is None or x_scale is None:
             raise LoraError("the 8-bit types need w_scale and x_scale")
         pws, pxs = _scales(w_scale, "w_scale", E * N, dev), _scales(x_scale, "x_scale", rows, dev)
-    _together(dev, W=W, groups=groups.pairs)
-    check(lib.lora_moe_linear(code, W.data_ptr(), pws, E, N, K, groups.pairs.data_ptr(),
-                              groups.offsets.data_ptr(), px, ldx, pxs, P // topk, topk, rows == P, py, ldy,
-                              _stream_on(dev, stream)), "lora_moe_linear")
-
-
+    if W.get_device() != dev:
+        raise _elsewhere("W", W.get_device(), dev)
+    if groups.device != dev:
+        raise _elsewhere("groups", groups.device, dev)
+    status = lib.lora_moe_linear(code, W.data_ptr(), pws, E, N, K, groups.pairs_ptr, groups.offsets_ptr, px, ldx,
+                                 pxs, P // topk, topk, rows == P, py, ldy, _stream_on(dev, stream))
+    if status:
+        check(status, "lora_moe_linear")
 
 
 class MoeExperts:
