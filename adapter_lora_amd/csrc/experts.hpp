@@ -327,12 +327,20 @@ __global__ __launch_bounds__(kFewThreads, 4) void k_experts_few(ExpertsParams p)
     constexpr int U = 2, UX = TB == 1 && F::kWords == 1 ? 2 : 1;
     uint4 vw[U][2 * NR], vx[UX][2 * TB];
     uint32_t off_x[2 * TB];
-    auto load_w = [&](int q, int kb) {
+    const int steps = (KB + kFewWaves - 1) / kFewWaves;
+    const int first = k_phase(n0 / 512, steps);
+    auto block = [&](int s) {
+        const int at = s + first;
+        return s < steps ? (at < steps ? at : at - steps) * kFewWaves + wave : KB;
+    };
+    auto load_w = [&](int q, int s) {
+        const int kb = block(s);
         const bool in = kb * 128 + lane % 8 * 16 < Kb;
 #pragma unroll
         for (int i = 0; i < 2 * NR; ++i) vw[q][i] = buf_ld16_at<true>(rw, in ? off_w[i] : kBufOff, (uint32_t)kb * 128u);
     };
-    auto load_x = [&](int q, int kb) {
+    auto load_x = [&](int q, int s) {
+        const int kb = block(s);
         const bool in = kb * 128 + lane % 8 * 16 < Kb;
 #pragma unroll
         for (int i = 0; i < 2 * TB; ++i) vx[q][i] = buf_ld16_at<false>(rx, in ? off_x[i] : kBufOff, (uint32_t)kb * 128u);
@@ -352,7 +360,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void k_experts_few(ExpertsParams p)
         for (int i = 0; i < 2 * TB; ++i) f_row[i] = (uint32_t)list[min(8 * i + lane / 8, rows - 1)];
         uint32_t f_out = (uint32_t)list[min(jt * 16 + lr, rows - 1)];
 #pragma unroll
-        for (int q = 0; q < U; ++q) load_w(q, wave + q * kFewWaves);
+        for (int q = 0; q < U; ++q) load_w(q, q);
         // whatever the list holds, no row outside the batch is read or written
 #pragma unroll
         for (int i = 0; i < 2 * TB; ++i) {
@@ -361,7 +369,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void k_experts_few(ExpertsParams p)
         }
         f_out = min(f_out, (uint32_t)p.P - 1);
 #pragma unroll
-        for (int q = 0; q < UX; ++q) load_x(q, wave + q * kFewWaves);
+        for (int q = 0; q < UX; ++q) load_x(q, q);
         typename F::Acc16 sum[NR][TB];
 #pragma unroll
         for (int r = 0; r < NR; ++r)
@@ -369,7 +377,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void k_experts_few(ExpertsParams p)
             for (int t = 0; t < TB; ++t)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) sum[r][t][q] = 0;
-        for (int b0 = wave; b0 < KB; b0 += U * kFewWaves) {
+        for (int b0 = 0; b0 < steps; b0 += U) {
 #pragma unroll
             for (int q = 0; q < U; ++q) {
                 // blocks past K read zeros (no memory is touched), and add none
@@ -389,8 +397,8 @@ __global__ __launch_bounds__(kFewThreads, 4) void k_experts_few(ExpertsParams p)
                     for (int r = 0; r < NR; ++r) sum[r][t] = F::mma16(w[r][0], w[r][1], x0, x1, sum[r][t]);
                     stage_order();
                 }
-                load_w(q, b0 + (q + U) * kFewWaves);
-                load_x(q % UX, b0 + (q + UX) * kFewWaves);
+                load_w(q, b0 + q + U);
+                load_x(q % UX, b0 + q + UX);
             }
         }
         float xs = 1.f, ws[4] = {1.f, 1.f, 1.f, 1.f};
@@ -430,13 +438,13 @@ __global__ __launch_bounds__(kFewThreads, 4) void k_experts_few(ExpertsParams p)
 
 template <typename R>
 __device__ __forceinline__ void share_tile(const ExpertsParams& p, uint4* smem, const Tile& t) {
-    const int e = t.e, pos = t.pos, rows = t.rows, n0 = t.ct * kRingCols;
+    const int e = t.e, pos = t.pos, rows = t.rows, n0 = t.ct * R::kCols;
     typedef typename R::F F;
     constexpr int RB = R::RB, CB = R::CB, NX = R::NX;
     const int tid = threadIdx.x;
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int lr = lane % 32, lh = lane / 32;
-    const int cols = min(kRingCols, p.N - n0);
+    const int cols = min(R::kCols, p.N - n0);
     uint32_t f_in[NX];
 #pragma unroll
     for (int i = 0; i < NX; ++i) f_in[i] = (uint32_t)p.pairs[pos + min(R::load_row(wave, i), rows - 1)];
@@ -454,7 +462,8 @@ __device__ __forceinline__ void share_tile(const ExpertsParams& p, uint4* smem, 
         }
     };
     typename R::Acc acc[RB][CB];
-    ring_product<R>(smem, p.W + ((int64_t)e * p.N + n0) * p.Kb, p.Kb, cols, p.Kb, t.ct / 8 % 8 * ((p.Kb + 127) / 128) / 8, x_rows, acc);
+    ring_product<R>(smem, p.W + ((int64_t)e * p.N + n0) * p.Kb, p.Kb, cols, p.Kb, k_phase(n0 / 1024, (p.Kb + 127) / 128),
+                    x_rows, acc);
 
     // ---- scales, one rounding
     int* const s_f = reinterpret_cast<int*>(smem);
@@ -503,7 +512,7 @@ __device__ __forceinline__ void share_tile(const ExpertsParams& p, uint4* smem, 
     }
 }
 
-template <typename F>
+template <typename F, bool HALF>
 __global__ __launch_bounds__(kRingThreads, 1) void k_experts_tile(ExpertsParams p) {
     __shared__ uint4 smem[kRingLds / 16];
     // 32 tiles in a row (four row tiles by eight column tiles of an expert) to each
@@ -512,10 +521,17 @@ __global__ __launch_bounds__(kRingThreads, 1) void k_experts_tile(ExpertsParams 
     const int id = v / 32 * 256 + (int)blockIdx.x % 8 * 32 + v % 32;
     const Tile t = p.E <= kWave ? find_tile<1>(p, id) : find_tile<kGroupMaxE / kWave>(p, id);
     if (t.e < 0) return;
-    if (t.rows > 192) share_tile<Ring256<F>>(p, smem, t);
-    else if (t.rows > 128) share_tile<Ring192<F>>(p, smem, t);
-    else if (t.rows > 64) share_tile<Ring128<F>>(p, smem, t);
-    else share_tile<Ring64<F>>(p, smem, t);
+    if constexpr (HALF) {
+        if (t.rows > 192) share_tile<Half256<F>>(p, smem, t);
+        else if (t.rows > 128) share_tile<Half192<F>>(p, smem, t);
+        else if (t.rows > 64) share_tile<Half128<F>>(p, smem, t);
+        else share_tile<Half64<F>>(p, smem, t);
+    } else {
+        if (t.rows > 192) share_tile<Ring256<F>>(p, smem, t);
+        else if (t.rows > 128) share_tile<Ring192<F>>(p, smem, t);
+        else if (t.rows > 64) share_tile<Ring128<F>>(p, smem, t);
+        else share_tile<Ring64<F>>(p, smem, t);
+    }
 }
 
 // ---------------------------------------------------------------- launch
@@ -535,26 +551,34 @@ template <typename F, int TB> hipError_t launch_few(ExpertsParams& p, hipStream_
 template <typename F> hipError_t launch_experts_as(ExpertsParams& p, hipStream_t st) {
     const int shares = p.E < p.P ? p.E : p.P;
     const int64_t extent = (int64_t)(p.x_rows - 1) * p.ldx + p.Kb;
+    const int64_t cols = (p.N + kRingCols - 1) / kRingCols;
     // The streaming form as long as 16 or 32 rows at a time take in most shares; it
-    // reads a share's W again for every further 16 or 32.  Past 8 rows a share only
-    // where the tiles would leave compute units without one.  Measured in graphs over
-    // several weights, equal shares, 16 rows at a time, 32, tiles; us:
-    //   8 x (28672, 4096), 4 rows: bf16 305 / 327 / 331, e4m3 163 / 173 / 180, int8 162 /
-    //     172 / 178; 16 rows: 325 / 328 / 337, 176 / 183 / 182, 174 / 183 / 181
-    //   8 x (4096, 14336), 4 rows: 143 / 147 / 203, 70 / 71 / 104, 70 / 72 / 103; 16 rows:
-    //     153 / 156 / 207, 75 / 77 / 106, 76 / 77 / 106; 32 rows: - / 179 / 212, - / 92 / 109,
-    //     - / 91 / 109
-    //   40 x (2848, 2064), 8 rows: 111 / 113 / 119, 65 / 70 / 62, 66 / 68 / 61; 4 of the 40
-    //     with 1 row: 17 / 18 / 45, 11 / 12 / 21, 11 / 11 / 21
-    // (shares that differ need the 32 from 8 rows on average).
-    const int64_t units = (int64_t)shares * ((p.N + kRingCols - 1) / kRingCols);
-    if (extent < INT32_MAX) {
-        if (p.P <= 8 * shares) return launch_few<F, 1>(p, st);
-        if (p.P <= 16 * shares && units < 256) return launch_few<F, 2>(p, st);
-    }
-    set_cols(p, kRingCols);
+    // reads a share's W again for every further 16 or 32.  With short rows of W its many
+    // workgroups wait more than they read, and the tiles are ahead once most experts
+    // have rows.  Measured in graphs over several weights, shares of 0.5 to 1.5 times the
+    // rows named, 16 rows at a time / 32 / tiles; us:
+    //   8 x (28672, 4096), 6 rows: bf16 270 / 275 / 329, e4m3 149 / 152 / 171, int8 142 / 151 /
+    //     170; 10 rows: 277 / 282 / 330, 153 / 160 / 171, 150 / 160 / 171; 16 rows: 420 / 298 /
+    //     332, 231 / 173 / 172, 230 / 171 / 173
+    //   8 x (4096, 14336), 6 rows: 140 / 142 / 157, 71 / 72 / 81, 71 / 72 / 82; 16 rows: 223 / 152 /
+    //     157, 126 / 78 / 82, 111 / 78 / 82; 24 rows: - / 165 / 159, - / 86 / 82, - / 85 / 83
+    //   40 x (2848, 2064), 6 rows: 102 / 107 / 98, 66 / 72 / 56, 66 / 72 / 55; 6 of the 40 with 2
+    //     rows: 22 / 23 / 24, 16 / 17 / 15, 15 / 17 / 15; 2 of them: 10 / 10 / 21, 8 / 9 / 13, 8 / 9 / 13
+    //   64 x (2048, 1408), 6 rows: 68 / 77 / 67, 46 / 50 / 37, 45 / 50 / 38
+    const bool spread = p.Kb >= 4096 || p.P < 2 * p.E || shares * cols < 256;
+    const bool fits = extent < INT32_MAX && shares * (int64_t)((p.N + kFewCols - 1) / kFewCols) < (1 << 23);
+    if (fits && p.P <= 8 * shares && spread) return launch_few<F, 1>(p, st);
+    if (fits && p.P <= 16 * shares && (p.Kb >= 8192 || shares * cols < 256)) return launch_few<F, 2>(p, st);
+    // Tiles of half the columns while a round of whole ones would leave compute units
+    // without one.  Whole / half: 8 x (4096, 14336), 64 rows bf16 258 / 175 us, int8 132 / 89;
+    // 160 rows 326 / 226, 174 / 116; 256 rows (256 tiles) 349 / 383, 188 / 196; 64 x (2816,
+    // 2048), 64 rows 169 / 172, 84 / 93.
+    const bool half = ((int64_t)p.P / kRingRows + shares) * cols < 256;
+    set_cols(p, half ? kRingCols / 2 : kRingCols);
     const int64_t tiles = ((int64_t)p.P / kRingRows + shares) * p.col_tiles;
-    hipLaunchKernelGGL((k_experts_tile<F>), dim3((unsigned)((tiles + 255) / 256 * 256)), dim3(kRingThreads), 0, st, p);
+    const dim3 grid((unsigned)((tiles + 255) / 256 * 256));
+    if (half) hipLaunchKernelGGL((k_experts_tile<F, true>), grid, dim3(kRingThreads), 0, st, p);
+    else hipLaunchKernelGGL((k_experts_tile<F, false>), grid, dim3(kRingThreads), 0, st, p);
     return hipGetLastError();
 }
 

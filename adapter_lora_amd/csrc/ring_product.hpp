@@ -60,11 +60,10 @@ __device__ __forceinline__ void dma_buffer(u32x4_vt r, uint32_t voff, uint32_t s
 template <typename F_, int WM_, int RB_, int CB_, int XD_, int WD_> struct Ring {
     typedef F_ F;
     static constexpr int WM = WM_, RB = RB_, CB = CB_, XD = XD_, WD = WD_;
-    static constexpr int WN = 4 / WM, kRows = 32 * RB * WM;
-    static_assert(32 * CB * WN == kRingCols, "four waves share the columns");
-    static constexpr int kX = kRows * 128, kW = kRingCols * 128;      // bytes of a ring slot
+    static constexpr int WN = 4 / WM, kRows = 32 * RB * WM, kCols = 32 * CB * WN;
+    static constexpr int kX = kRows * 128, kW = kCols * 128;          // bytes of a ring slot
     static_assert(XD >= 2 && WD >= XD && XD * kX + WD * kW <= kRingLds, "rings fit the LDS");
-    static constexpr int NX = kRows / 32, NW = kRingCols / 32;        // loads of a wave and stage
+    static constexpr int NX = kRows / 32, NW = kCols / 32;            // loads of a wave and stage
     typedef typename F::Acc32 Acc;
     // the first row and column of a wave's part
     __device__ static int row0(int wave) { return wave / WN * RB * 32; }
@@ -78,6 +77,11 @@ template <typename F> using Ring256 = Ring<F, 2, 4, 4, 2, 3>;
 template <typename F> using Ring192 = Ring<F, 2, 3, 4, 2, 3>;
 template <typename F> using Ring128 = Ring<F, 1, 4, 2, 3, 3>;
 template <typename F> using Ring64 = Ring<F, 1, 2, 2, 4, 4>;
+// half the columns
+template <typename F> using Half256 = Ring<F, 2, 4, 2, 3, 4>;
+template <typename F> using Half192 = Ring<F, 2, 3, 2, 4, 4>;
+template <typename F> using Half128 = Ring<F, 2, 2, 2, 5, 5>;
+template <typename F> using Half64 = Ring<F, 2, 1, 2, 6, 6>;
 
 // acc[rb][cb]: columns 32 cb + 8 (q / 4) + 4 (l / 32) + q % 4 of row 32 rb + l % 32 of
 // the wave's part.  W: the tile's rows, `cols` of them, Kb bytes of K each, ldw apart
@@ -85,10 +89,7 @@ template <typename F> using Ring64 = Ring<F, 1, 2, 2, 4, 4>;
 // loads (load_row(wave, i), any row that may be read past the tile's), load_byte
 // added.  On return every wave is done with the LDS.
 //
-// The stages of K begin at k0 and go round: where all tiles that stream W at a time read
-// the same bytes of rows a power of two apart, few of the memory's channels serve
-// them (8 experts of 28672 x 4096 in bf16, 64 rows each: 4.6 TB/s; with eight
-// different k0 5.3).
+// The stages of K begin at k0 and go round.
 template <typename R, typename XRows>
 __device__ __forceinline__ void ring_product(uint4* smem, const char* W, int64_t ldw, int cols, int Kb, int k0, XRows x_rows,
                                              typename R::Acc (&acc)[R::RB][R::CB]) {

@@ -21,6 +21,18 @@
 
 namespace mlora {
 
+// Where the products that stream W begin their `steps` steps of K, which then go round:
+// by groups of neighbouring tiles, spread evenly (the golden ratio's multiples).  Where
+// all that stream at a time read the same bytes of rows a power of two apart, few of
+// the memory's channels serve them: the experts of few rows, 8 x (28672, 4096) in bf16,
+// 335 us from step 0, 265 so, and (4096, 4096) 57 and 41.  Neighbours that all differ
+// lose what two of their row tiles share in the L2 (8192 rows of 8 x (4096, 14336) in
+// tiles 965 us, in groups of four tiles 921), and eight starts in turn, tile by tile,
+// fall in step with the channels again (40 rows of 8 x (28672, 4096) 441 us, 339).
+__device__ __forceinline__ int k_phase(int group, int steps) {
+    return (int)__umulhi((uint32_t)group * 0x9E3779B1u, (uint32_t)steps);
+}
+
 struct StageAt {
     int put[2];       // row l / 8 (+ 8), chunk l % 8
     int get[2];       // row l % 16, chunk l / 16 (+ 4)

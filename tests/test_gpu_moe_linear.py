@@ -157,7 +157,38 @@ CASES = {
     "few_256_experts": (500, 4, 256, 40, 48, None, True),
     "few_32_rows": (64, 2, 8, 24, 272, [30, 2, 33, 1, 31, 0, 16, 15], False),
     "few_one_expert_of_many": (300, 1, 200, 72, 160, [0] * 150 + [300], False),
+    # tiles of all 256 columns: 256 and more of them
+    "whole_tiles": (3000, 2, 40, 1800, 272, [1, 64, 65, 128, 129, 192, 193, 256, 257, 513, 0, 700], False),
+    "whole_tiles_short_k": (1200, 4, 64, 1032, 32, None, True),
+    "whole_tiles_long_k": (640, 2, 8, 8200, 2064, None, False),
+    "whole_tiles_few_rows": (40, 8, 130, 520, 144, None, False),
+    # starts of K that differ
+    "few_of_256": (60, 4, 256, 40, 48, None, True),
+    "few_wide": (6, 2, 5, 2600, 4112, None, False),
+    "few_wide_32_rows": (30, 2, 4, 1600, 8208, None, True),
+    "few_wide_odd_steps": (4, 4, 16, 4104, 1552, None, False),
+    "half_tiles_wide": (250, 2, 3, 5000, 1424, [400, 3, 97], False),
 }
+WHOLE_TILES = [k for k in CASES if k.startswith("whole")]
+FEW = [k for k in CASES if k.startswith("few") and k != "few_256_experts"]
+
+
+def form(kind, P, E, N, K):
+    """The form that the size rule takes."""
+    Kb, shares, cols = K * (2 if kind == "bf16" else 1), min(E, P), -(-N // 256)
+    if P <= 8 * shares and (Kb >= 4096 or P < 2 * E or shares * cols < 256):
+        return "few"
+    if P <= 16 * shares and (Kb >= 8192 or shares * cols < 256):
+        return "few"
+    return "half tiles" if (P // 256 + shares) * cols < 256 else "whole tiles"
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_cases_reach_every_form(kind):
+    def forms(names):
+        return {form(kind, c[0] * c[1], *c[2:5]) for c in (CASES[k] for k in names)}
+    assert forms(WHOLE_TILES) == {"whole tiles"} and forms(FEW) == {"few"}
+    assert forms(["tile_ragged", "tile_long_k", "tile_257_rows", "half_tiles_wide"]) == {"half tiles"}
 
 
 @pytest.mark.parametrize("kind", list(TYPES))
