@@ -161,9 +161,11 @@ template <int NC> struct Shares {
     }
 };
 
-// Rows [pos, pos + rows) of expert e's share, column tile ct; e = -1: none.
+// Rows [pos, pos + rows) of expert e's share, column tile ct; e = -1: none.  alone: they
+// are the whole share.
 struct Tile {
     int e = -1, pos = 0, rows = 0, ct = 0;
+    bool alone = false;
 };
 
 // n / cols by the reciprocal 2^32 / cols rounded up, which is one too many at most.
@@ -284,6 +286,7 @@ template <int NC> __device__ __forceinline__ Tile find_tile(const ExpertsParams&
             }
         }
     }
+    t.alone = t.rows <= kRingRows;
     t.pos += rt * kRingRows;
     t.rows = min(kRingRows, t.rows - rt * kRingRows);
     return t;
@@ -299,7 +302,7 @@ constexpr int kFewThreads = 512;
 constexpr int kFewWaves = kFewThreads / kWave;
 constexpr int kFewCols = 32;
 
-template <typename F, int TB>
+template <typename F, int TB, bool NT>
 __global__ __launch_bounds__(kFewThreads, 4) void k_experts_few(ExpertsParams p) {
     constexpr int NR = kFewCols / 16;
     constexpr int kStage = (NR + 1) * 128;           // uint4 of a wavefront: rows of W and of x, later its sums
@@ -337,7 +340,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void k_experts_few(ExpertsParams p)
         const int kb = block(s);
         const bool in = kb * 128 + lane % 8 * 16 < Kb;
 #pragma unroll
-        for (int i = 0; i < 2 * NR; ++i) vw[q][i] = buf_ld16_at<true>(rw, in ? off_w[i] : kBufOff, (uint32_t)kb * 128u);
+        for (int i = 0; i < 2 * NR; ++i) vw[q][i] = buf_ld16_at<NT>(rw, in ? off_w[i] : kBufOff, (uint32_t)kb * 128u);
     };
     auto load_x = [&](int q, int s) {
         const int kb = block(s);
@@ -370,6 +373,15 @@ __global__ __launch_bounds__(kFewThreads, 4) void k_experts_few(ExpertsParams p)
         f_out = min(f_out, (uint32_t)p.P - 1);
 #pragma unroll
         for (int q = 0; q < UX; ++q) load_x(q, q);
+        // the scales come with the first blocks where the registers hold them (with 32 rows
+        // int8 spilled)
+        float xs = 1.f, ws[4] = {1.f, 1.f, 1.f, 1.f};
+        auto scales = [&]() {
+            xs = p.x_scale[pair_row(p, f_out)];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) ws[q] = p.w_scale[(int64_t)tile.e * p.N + min(n + q, p.N - 1)];
+        };
+        if constexpr (F::kScaled && TB == 1) scales();
         typename F::Acc16 sum[NR][TB];
 #pragma unroll
         for (int r = 0; r < NR; ++r)
@@ -401,12 +413,8 @@ __global__ __launch_bounds__(kFewThreads, 4) void k_experts_few(ExpertsParams p)
                 load_x(q % UX, b0 + q + UX);
             }
         }
-        float xs = 1.f, ws[4] = {1.f, 1.f, 1.f, 1.f};
-        if (F::kScaled && wave < NR * TB) {
-            xs = p.x_scale[pair_row(p, f_out)];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) ws[q] = p.w_scale[(int64_t)tile.e * p.N + min(n + q, p.N - 1)];
-        }
+        if constexpr (F::kScaled && TB > 1)
+            if (wave < NR * TB) scales();
         // join the eight partial sums in a fixed order; four columns of a row a lane
         typedef typename F::Acc16 acc_t;
         acc_t* red = reinterpret_cast<acc_t*>(st);
@@ -436,7 +444,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void k_experts_few(ExpertsParams p)
 // The main loop and the forms for tiles with fewer rows (a share's last ones) stand
 // in ring_product.hpp.
 
-template <typename R>
+template <typename R, bool NT = false>
 __device__ __forceinline__ void share_tile(const ExpertsParams& p, uint4* smem, const Tile& t) {
     const int e = t.e, pos = t.pos, rows = t.rows, n0 = t.ct * R::kCols;
     typedef typename R::F F;
@@ -462,7 +470,7 @@ __device__ __forceinline__ void share_tile(const ExpertsParams& p, uint4* smem, 
         }
     };
     typename R::Acc acc[RB][CB];
-    ring_product<R>(smem, p.W + ((int64_t)e * p.N + n0) * p.Kb, p.Kb, cols, p.Kb, k_phase(n0 / 1024, (p.Kb + 127) / 128),
+    ring_product<R, NT>(smem, p.W + ((int64_t)e * p.N + n0) * p.Kb, p.Kb, cols, p.Kb, k_phase(n0 / 1024, (p.Kb + 127) / 128),
                     x_rows, acc);
 
     // ---- scales, one rounding
@@ -521,16 +529,18 @@ __global__ __launch_bounds__(kRingThreads, 1) void k_experts_tile(ExpertsParams 
     const int id = v / 32 * 256 + (int)blockIdx.x % 8 * 32 + v % 32;
     const Tile t = p.E <= kWave ? find_tile<1>(p, id) : find_tile<kGroupMaxE / kWave>(p, id);
     if (t.e < 0) return;
+    // With up to 192 rows W bounds the tile, and is not kept if no other reads it.
+    const bool once = p.whole_lines && t.alone;
     if constexpr (HALF) {
         if (t.rows > 192) share_tile<Half256<F>>(p, smem, t);
-        else if (t.rows > 128) share_tile<Half192<F>>(p, smem, t);
-        else if (t.rows > 64) share_tile<Half128<F>>(p, smem, t);
-        else share_tile<Half64<F>>(p, smem, t);
+        else if (t.rows > 128) once ? share_tile<Half192<F>, true>(p, smem, t) : share_tile<Half192<F>>(p, smem, t);
+        else if (t.rows > 64) once ? share_tile<Half128<F>, true>(p, smem, t) : share_tile<Half128<F>>(p, smem, t);
+        else once ? share_tile<Half64<F>, true>(p, smem, t) : share_tile<Half64<F>>(p, smem, t);
     } else {
         if (t.rows > 192) share_tile<Ring256<F>>(p, smem, t);
-        else if (t.rows > 128) share_tile<Ring192<F>>(p, smem, t);
-        else if (t.rows > 64) share_tile<Ring128<F>>(p, smem, t);
-        else share_tile<Ring64<F>>(p, smem, t);
+        else if (t.rows > 128) once ? share_tile<Ring192<F>, true>(p, smem, t) : share_tile<Ring192<F>>(p, smem, t);
+        else if (t.rows > 64) once ? share_tile<Ring128<F>, true>(p, smem, t) : share_tile<Ring128<F>>(p, smem, t);
+        else once ? share_tile<Ring64<F>, true>(p, smem, t) : share_tile<Ring64<F>>(p, smem, t);
     }
 }
 
@@ -543,32 +553,39 @@ static void set_cols(ExpertsParams& p, int width) {
 template <typename F, int TB> hipError_t launch_few(ExpertsParams& p, hipStream_t st) {
     set_cols(p, kFewCols);
     const int shares = p.E < p.P ? p.E : p.P;
-    hipLaunchKernelGGL((k_experts_few<F, TB>), dim3((unsigned)((int64_t)shares * p.col_tiles)), dim3(kFewThreads), 0,
-                       st, p);
+    const dim3 grid((unsigned)(shares * p.col_tiles)), block(kFewThreads);
+    if (p.whole_lines) hipLaunchKernelGGL((k_experts_few<F, TB, true>), grid, block, 0, st, p);
+    else hipLaunchKernelGGL((k_experts_few<F, TB, false>), grid, block, 0, st, p);
     return hipGetLastError();
 }
 
 template <typename F> hipError_t launch_experts_as(ExpertsParams& p, hipStream_t st) {
     const int shares = p.E < p.P ? p.E : p.P;
+    // W is read past the caches where its rows are whole lines: 8 x (28672, 4096) in bf16,
+    // 8 rows 299 -> 273 us here, 64 rows 353 -> 333 in tiles.  Of lines that two rows
+    // share the second read then comes from afar too: 40 x (2848, 2064), 8 rows in tiles
+    // 98 -> 127 us.
+    p.whole_lines = p.Kb % 128 == 0 && (uintptr_t)p.W % 128 == 0;
     const int64_t extent = (int64_t)(p.x_rows - 1) * p.ldx + p.Kb;
-    const int64_t cols = (p.N + kRingCols - 1) / kRingCols;
-    // The streaming form as long as 16 or 32 rows at a time take in most shares; it
-    // reads a share's W again for every further 16 or 32.  With short rows of W its many
-    // workgroups wait more than they read, and the tiles are ahead once most experts
-    // have rows.  Measured in graphs over several weights, shares of 0.5 to 1.5 times the
-    // rows named, 16 rows at a time / 32 / tiles; us:
-    //   8 x (28672, 4096), 6 rows: bf16 270 / 275 / 329, e4m3 149 / 152 / 171, int8 142 / 151 /
-    //     170; 10 rows: 277 / 282 / 330, 153 / 160 / 171, 150 / 160 / 171; 16 rows: 420 / 298 /
-    //     332, 231 / 173 / 172, 230 / 171 / 173
-    //   8 x (4096, 14336), 6 rows: 140 / 142 / 157, 71 / 72 / 81, 71 / 72 / 82; 16 rows: 223 / 152 /
-    //     157, 126 / 78 / 82, 111 / 78 / 82; 24 rows: - / 165 / 159, - / 86 / 82, - / 85 / 83
-    //   40 x (2848, 2064), 6 rows: 102 / 107 / 98, 66 / 72 / 56, 66 / 72 / 55; 6 of the 40 with 2
-    //     rows: 22 / 23 / 24, 16 / 17 / 15, 15 / 17 / 15; 2 of them: 10 / 10 / 21, 8 / 9 / 13, 8 / 9 / 13
-    //   64 x (2048, 1408), 6 rows: 68 / 77 / 67, 46 / 50 / 37, 45 / 50 / 38
-    const bool spread = p.Kb >= 4096 || p.P < 2 * p.E || shares * cols < 256;
+    const int64_t cols = (p.N + kRingCols - 1) / kRingCols, units = shares * cols;
+    // The streaming form as long as 16 rows at a time take in most shares (it reads a
+    // share's W again for every further 16).  With short rows of W its many workgroups
+    // wait more than they read, and the tiles are ahead once most experts have rows.
+    // Up to twice the rows in its form of 32 where the tiles would leave compute units
+    // without one, or come in one short round.  Measured in graphs over several weights,
+    // shares of 0.5 to 1.5 times the rows named, 16 rows at a time / 32 / tiles; us:
+    //   8 x (28672, 4096), 8 rows: bf16 273 / 280 / 304, int8 146 / 155 / 156; 16 rows: - / 300 /
+    //     310, - / 172 / 162
+    //   8 x (4096, 14336), 8 rows: 143 / 145 / 138, 72 / 74 / 72; 16 rows: - / 153 / 140, - / 78 / 73
+    //   8 x (4096, 4096), 8 rows: 42 / 44 / 58, 24 / 26 / 30; 16 rows: - / 45 / 57, - / 26 / 31
+    //   64 x (2816, 2048), 8 rows: 117 / 123 / 122, 72 / 78 / 66
+    //   64 x (2048, 1408), 8 rows: 71 / 77 / 60, 46 / 50 / 35
+    //   40 x (2848, 2064), 8 rows: 96 / 103 / 98, 62 / 68 / 56; 6 of the 40 with 2 rows: 22 / 23 / 24,
+    //     15 / 17 / 15; 2 of them: 10 / 10 / 21, 8 / 9 / 13
+    // (e4m3 within 4 % of int8.)
     const bool fits = extent < INT32_MAX && shares * (int64_t)((p.N + kFewCols - 1) / kFewCols) < (1 << 23);
-    if (fits && p.P <= 8 * shares && spread) return launch_few<F, 1>(p, st);
-    if (fits && p.P <= 16 * shares && (p.Kb >= 8192 || shares * cols < 256)) return launch_few<F, 2>(p, st);
+    if (fits && p.P <= 8 * shares && (p.Kb >= 4096 || p.P < 2 * p.E || units < 256)) return launch_few<F, 1>(p, st);
+    if (fits && p.P <= 16 * shares && (units < 128 || (units < 256 && p.Kb <= 8192))) return launch_few<F, 2>(p, st);
     // Tiles of half the columns while a round of whole ones would leave compute units
     // without one.  Whole / half: 8 x (4096, 14336), 64 rows bf16 258 / 175 us, int8 132 / 89;
     // 160 rows 326 / 226, 174 / 116; 256 rows (256 tiles) 349 / 383, 188 / 196; 64 x (2816,

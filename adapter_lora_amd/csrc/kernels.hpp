@@ -255,6 +255,7 @@ struct ExpertsParams {
     int x_rows;
     int col_tiles;
     uint32_t cols_inv;      // 2^32 / col_tiles, rounded up
+    bool whole_lines;       // rows of W begin at cache lines of their own
 };
 
 hipError_t launch_moe_group(const int32_t* topk_ids, int P, int E, int32_t* pairs, int32_t* offsets,

@@ -50,10 +50,16 @@ typedef __attribute__((address_space(3))) char lds_char_t;
 __device__ __forceinline__ void dma_global(const char* p, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory");
 }
-__device__ __forceinline__ void dma_buffer(u32x4_vt r, uint32_t voff, uint32_t soff, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff), "s"(r),
-                 "s"(soff)
-                 : "memory");
+// NT: read once, not kept in the caches
+template <bool NT> __device__ __forceinline__ void dma_buffer(u32x4_vt r, uint32_t voff, uint32_t soff, uint32_t lds) {
+    if constexpr (NT)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds" ::"s"(lds), "v"(voff),
+                     "s"(r), "s"(soff)
+                     : "memory");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff),
+                     "s"(r), "s"(soff)
+                     : "memory");
 }
 
 // WM waves share the rows, 4 / WM the columns; a wave takes RB x CB blocks of 32 x 32.
@@ -62,7 +68,7 @@ template <typename F_, int WM_, int RB_, int CB_, int XD_, int WD_> struct Ring 
     static constexpr int WM = WM_, RB = RB_, CB = CB_, XD = XD_, WD = WD_;
     static constexpr int WN = 4 / WM, kRows = 32 * RB * WM, kCols = 32 * CB * WN;
     static constexpr int kX = kRows * 128, kW = kCols * 128;          // bytes of a ring slot
-    static_assert(XD >= 2 && WD >= XD && XD * kX + WD * kW <= kRingLds, "rings fit the LDS");
+    static_assert(XD >= 2 && WD >= XD && WD <= XD + 1 && XD * kX + WD * kW <= kRingLds, "rings fit the LDS");
     static constexpr int NX = kRows / 32, NW = kCols / 32;            // loads of a wave and stage
     typedef typename F::Acc32 Acc;
     // the first row and column of a wave's part
@@ -89,8 +95,8 @@ template <typename F> using Half64 = Ring<F, 2, 1, 2, 6, 6>;
 // loads (load_row(wave, i), any row that may be read past the tile's), load_byte
 // added.  On return every wave is done with the LDS.
 //
-// The stages of K begin at k0 and go round.
-template <typename R, typename XRows>
+// The stages of K begin at k0 and go round.  NT: no other tile reads these rows of W.
+template <typename R, bool NT = false, typename XRows>
 __device__ __forceinline__ void ring_product(uint4* smem, const char* W, int64_t ldw, int cols, int Kb, int k0, XRows x_rows,
                                              typename R::Acc (&acc)[R::RB][R::CB]) {
     typedef typename R::F F;
@@ -102,7 +108,8 @@ __device__ __forceinline__ void ring_product(uint4* smem, const char* W, int64_t
     constexpr int kPost = kWords == 1 ? MF : kTotal - MF / 2;      // of them behind the barrier
     constexpr int kReads = (RB + CB) * kWords;                     // operand reads of a step
     constexpr int kEarly = (kPost * kLoads + kTotal - 1) / kTotal; // loads issued behind the barrier
-    // what may still be on its way when a stage is read: the stages after it
+    // what may still be on its way when a stage is read: the stages after it (W of the
+    // stage WD on is issued behind x of the one XD on)
     constexpr int kAhead = (XD - 2) * NX + (WD - 2) * NW;
 
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
@@ -146,7 +153,7 @@ __device__ __forceinline__ void ring_product(uint4* smem, const char* W, int64_t
         dma_global(xin ? xp[i] : zeros, dst + lx + i * 4096);
         xp[i] += inc;
     };
-    auto load_w = [&](int i) { dma_buffer(rw, win ? woff[i] : kBufOff, so, dst + lw + i * 4096); };
+    auto load_w = [&](int i) { dma_buffer<NT>(rw, win ? woff[i] : kBufOff, so, dst + lw + i * 4096); };
     auto load_at = [&](int at) {                     // the loads due after MFMA `at` behind the barrier
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {

@@ -168,6 +168,11 @@ CASES = {
     "few_wide_32_rows": (30, 2, 4, 1600, 8208, None, True),
     "few_wide_odd_steps": (4, 4, 16, 4104, 1552, None, False),
     "half_tiles_wide": (250, 2, 3, 5000, 1424, [400, 3, 97], False),
+    # rows of W of whole cache lines, shares of one tile (W not kept) and of more
+    "few_lines": (6, 2, 5, 600, 1152, None, False),
+    "few_lines_32_rows": (30, 2, 4, 600, 640, [20, 33, 1], True),
+    "half_tiles_lines": (500, 2, 4, 648, 512, [64, 128, 192, 300], False),
+    "whole_tiles_lines": (700, 4, 40, 1800, 384, [60, 100, 192, 256, 257, 513], False),
 }
 WHOLE_TILES = [k for k in CASES if k.startswith("whole")]
 FEW = [k for k in CASES if k.startswith("few") and k != "few_256_experts"]
@@ -178,7 +183,7 @@ def form(kind, P, E, N, K):
     Kb, shares, cols = K * (2 if kind == "bf16" else 1), min(E, P), -(-N // 256)
     if P <= 8 * shares and (Kb >= 4096 or P < 2 * E or shares * cols < 256):
         return "few"
-    if P <= 16 * shares and (Kb >= 8192 or shares * cols < 256):
+    if P <= 16 * shares and (shares * cols < 128 or shares * cols < 256 and Kb <= 8192):
         return "few"
     return "half tiles" if (P // 256 + shares) * cols < 256 else "whole tiles"
 
