@@ -672,7 +672,7 @@ def lora_quantize_rows(x: torch.Tensor, out8: torch.Tensor, scale: torch.Tensor,
     if len(shape) != 2:
         raise LoraError("x must be a 2-D tensor")
     code, dev = _dtype_code(x.dtype), x.get_device()
-    int8 = out8.dtype is _I8
+    int8 = out8 is not None and out8.dtype is _I8
     po8, ldo8 = _matrix(out8, "out8", shape, _I8 if int8 else E4M3, dev)
     px, ldx = _matrix(x, "x", shape, x.dtype, dev)
     quantize = lib.lora_quantize_rows_int8 if int8 else lib.lora_quantize_rows

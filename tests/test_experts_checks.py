@@ -179,6 +179,14 @@ def test_binding_refusals_int8(no_launch):
             ml.lora_linear_int8(tb, W8_, sn_, x8_, s_, x_, seg, y_, ws)
 
 
+def test_quantize_rows_without_an_output(monkeypatch):
+    """Refused by the library, as a LoraError, not by an attribute of None."""
+    monkeypatch.setattr(ml, "_cur_device", lambda: 0)
+    monkeypatch.setattr(ml, "_raw_stream", lambda device: 0)
+    with pytest.raises(ml.LoraError):
+        ml.lora_quantize_rows(z(4, 64), None, z(4, dtype=F32))
+
+
 # ---------------------------------------------------------------- pins of the oracle
 def test_group_pins():
     pairs, offsets = X.group([[2, 0], [5, 2], [-1, 0], [2, 9]], 6)
