@@ -17,26 +17,23 @@ namespace mlora {
 // ascending f, pairs of experts outside [0, E) last; offsets [E + 1]: the first
 // position of each expert and the end of the last.
 //
-// A stable counting sort.  A workgroup of 16 wavefronts places kGroupChunk pairs,
-// and counts all the others itself: how many of each expert stand before its own
-// and how many there are in all.  So one launch does without a word between
-// workgroups; reading the ids again costs each workgroup 4 P bytes from the L2
-// (65536 pairs, four workgroups: 256 KB each), and one workgroup is all there is
-// up to 16384 pairs.
+// A stable counting sort.  A workgroup of 16 wavefronts places `chunk` pairs, and
+// counts all the others itself: how many of each expert stand before its own and how
+// many there are in all.  So one launch does without a word between workgroups;
+// reading the ids again costs each workgroup 4 P bytes from the L2.
 constexpr int kGroupThreads = 1024;
 constexpr int kGroupWaves = kGroupThreads / kWave;
-constexpr int kGroupChunk = 16 * kGroupThreads;
 constexpr int kGroupMaxE = 256;
 constexpr int kGroupCached = 4;                    // ids of a wavefront's first passes, kept in registers
 
-__global__ __launch_bounds__(kGroupThreads) void k_moe_group(const int32_t* __restrict__ ids, int P, int E,
+__global__ __launch_bounds__(kGroupThreads) void k_moe_group(const int32_t* __restrict__ ids, int P, int E, int chunk,
                                                              int32_t* __restrict__ pairs,
                                                              int32_t* __restrict__ offsets) {
     __shared__ int s_row[kGroupWaves][kGroupMaxE + 1];   // counts, then next positions, of each wavefront
     __shared__ int s_before[kGroupMaxE + 1], s_after[kGroupMaxE + 1];
     const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int NB = E + 1;
-    const int b0 = (int)blockIdx.x * kGroupChunk, b1 = min(P, b0 + kGroupChunk);
+    const int b0 = (int)blockIdx.x * chunk, b1 = min(P, b0 + chunk);
     // a wavefront's part: passes of 64 pairs
     const int passes = (b1 - b0 + kGroupThreads - 1) / kGroupThreads;
     const int c0 = min(b1, b0 + wave * passes * kWave), c1 = min(b1, c0 + passes * kWave);
@@ -47,8 +44,18 @@ __global__ __launch_bounds__(kGroupThreads) void k_moe_group(const int32_t* __re
     for (int i = tid; i < NB; i += kGroupThreads) s_before[i] = s_after[i] = 0;
     __syncthreads();
     auto bucket = [&](int v) { return (uint32_t)v < (uint32_t)E ? v : E; };
-    for (int i = tid; i < b0; i += kGroupThreads) atomicAdd(&s_before[bucket(ids[i])], 1);
-    for (int i = b1 + tid; i < P; i += kGroupThreads) atomicAdd(&s_after[bucket(ids[i])], 1);
+    auto count_others = [&](int* sums, int lo, int hi) {       // P < 2^24 + 1
+        for (int i = lo + tid; i < hi; i += 4 * kGroupThreads) {
+            int v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = ids[min(i + j * kGroupThreads, P - 1)];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (i + j * kGroupThreads < hi) atomicAdd(&sums[bucket(v[j])], 1);
+        }
+    };
+    count_others(s_before, 0, b0);
+    count_others(s_after, b1, P);
 
     // lanes of the pass whose expert is the same, one ballot per bit
     const int nbits = 32 - __clz(E);
@@ -129,8 +136,13 @@ hipError_t launch_moe_group(const int32_t* topk_ids, int P, int E, int32_t* pair
         hipLaunchKernelGGL(k_moe_group_none, dim3(1), dim3(kWave), 0, st, E + 1, offsets);
         return hipGetLastError();
     }
-    hipLaunchKernelGGL(k_moe_group, dim3((unsigned)((P + kGroupChunk - 1) / kGroupChunk)), dim3(kGroupThreads), 0,
-                       st, topk_ids, P, E, pairs, offsets);
+    // As many workgroups as place their pairs in one pass, until the others' ids are what
+    // takes the time (1 / 4 / 16 passes: 9186 pairs of 64 experts 4.4 / 5.6 / 9.1 us, 32768 of
+    // 128 6.9 / 8.1 / 17.8, 65536 of 256 10.6 / 11.8 / 22.2, 524288 of 64 99 / 88 / 97, 2^23
+    // 23800 / 6290 / 1760; one token 2.6).
+    const int chunk = (P <= 65536 ? 1 : 16) * kGroupThreads;
+    hipLaunchKernelGGL(k_moe_group, dim3((unsigned)((P + chunk - 1) / chunk)), dim3(kGroupThreads), 0, st, topk_ids, P, E,
+                       chunk, pairs, offsets);
     return hipGetLastError();
 }
 
