@@ -1,7 +1,8 @@
 // The shared projection in 8 bits beside the adapters for more tokens than one
 // decode launch takes (see linear_fp8.hpp for the formula): lora_shrink writes
-// S, then one product on e4m3 operands whose epilogue scales the sums by xs
-// ws, adds S B_i^T and rounds y once.
+// S, then one product on e4m3 or integer operands whose epilogue scales the sums by
+// xs ws, adds S B_i^T and rounds y once.  Batches that fill the chip with them take
+// tiles of 256 x 256 (gemm_ring.hpp); the units here are for the others.
 //
 // Work unit = (32 RB consecutive sorted positions, 128 CB output columns of one
 // slice); the rows of a unit may belong to several segments and to tokens

@@ -3,6 +3,11 @@
 // and gemm_fp8.hpp for the call): the main loop of ring_product.hpp, then the
 // scales, the deltas of the tile's segments and one rounding.
 //
+// What bounds it: the matrix unit and the clock that its power leaves.  512 tokens to
+// 28672 columns, K = 4096, and 8192 tokens to 4096, the calls with their shrink: int8 90
+// and 166 us (in units of 128 x 256 103 and 189), e4m3 87 and 144 (101 and 170); the
+// kernel's share in int8 82 and 150.
+//
 // Segments: the tile's rows may belong to several and to tokens without an adapter.
 // S goes to LDS once as a bf16 hi / lo pair; each segment multiplies its rows of it,
 // picked by a mask on the operand, with its adapter's B rows on the same 32 x 32

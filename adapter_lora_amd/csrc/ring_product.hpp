@@ -25,7 +25,8 @@
 //
 // Tiles with fewer rows: the waves of one with up to 192, 128 or 64 rows take
 // 96 x 128, 128 x 64 and 64 x 64 outputs each instead of 128 x 128, with as many
-// fewer MFMAs, and rings as deep as 160 KB allow.
+// fewer MFMAs, and rings as deep as 160 KB allow.  Tiles of 128 columns likewise, for
+// grids that would not fill the chip.
 //
 // The loads to LDS are written in assembly because the compiler waits for all of
 // them at every LDS read; they have no output registers, and the waits that their
