@@ -193,21 +193,22 @@ __device__ __forceinline__ int nth_bit(uint64_t mask, int nth) {
     return __builtin_ctzll(__ballot(hit));
 }
 
-// Share number `nth` of those with pairs.
-template <int NC> __device__ __forceinline__ Tile find_share(const ExpertsParams& p, int nth) {
+// Part `nth` of the shares cut into parts of up to ROWS positions.
+template <int NC, int ROWS> __device__ __forceinline__ Tile find_part(const ExpertsParams& p, int nth) {
     const Shares<NC> sh(p.offsets, p.E, p.P);
     Tile t;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-        const uint64_t some = __ballot(sh.n[c] > 0);
-        const int all = __popcll(some);
-        if (t.e < 0 && nth < all) {
-            const int l = nth_bit(some, nth);
+        const int parts = (sh.n[c] + ROWS - 1) / ROWS, inc = wave_incl_scan(parts);
+        const uint64_t past = __ballot(nth < inc);
+        if (t.e < 0 && past != 0ull) {
+            const int l = __builtin_ctzll(past);
+            const int before = (nth - __builtin_amdgcn_readlane(inc - parts, l)) * ROWS;
             t.e = c * kWave + l;
-            t.pos = __builtin_amdgcn_readlane(sh.pos[c], l);
-            t.rows = __builtin_amdgcn_readlane(sh.n[c], l);
+            t.pos = __builtin_amdgcn_readlane(sh.pos[c], l) + before;
+            t.rows = min(ROWS, __builtin_amdgcn_readlane(sh.n[c], l) - before);
         }
-        nth -= all;
+        nth -= __builtin_amdgcn_readlane(inc, kWave - 1);
     }
     return t;
 }
@@ -305,19 +306,22 @@ template <int NC> __device__ __forceinline__ Tile find_tile(const ExpertsParams&
 }
 
 // ---------------------------------------------------------------- few rows a share
-// Work unit = (expert with at least one pair, 32 output columns) for all of the
-// expert's rows, 16 TB at a time; K over eight wavefronts in blocks of 128 bytes,
-// whose partial sums join through LDS.  What bounds it: the touched experts' rows
+// Work unit = (up to 64 positions of an expert's share, 32 output columns), 16 TB of them
+// at a time; K over eight wavefronts in blocks of 128 bytes, whose partial sums join
+// through LDS.  What bounds it: the touched experts' rows
 // of W, read once; they stream past the few rows of x.  Both are read as whole
 // 128-byte segments and change lanes through LDS (row_stage.hpp).
 //
 // Measured: 8 rows each of 8 experts of 28672 x 4096 in bf16 273 us, 1.88 GB at 6.9 TB/s (a
 // large copy, read and written, 5.1); one token to 4 of 40 experts of 2848 x 2064 in int8
 // 9.7 us, 23.5 MB: with W in the caches 5.6, of which the share is found in 0.5, the
-// loads are issued in 1.5, multiplied in 1.4, joined and stored in 0.3.
+// loads are issued in 1.5, multiplied in 1.4, joined and stored in 0.3.  64 positions a
+// unit, for routing that is far from even: 512 rows over 64 x (2816, 2048) in bf16 118 us
+// evenly, with half of them on one expert 135 (141 in one unit), with all 50 (144); in
+// units of 32 134 and 49.
 constexpr int kFewThreads = 512;
 constexpr int kFewWaves = kFewThreads / kWave;
-constexpr int kFewCols = 32;
+constexpr int kFewCols = 32, kFewRows = 64;
 
 template <typename F, int TB, bool NT>
 __global__ __launch_bounds__(kFewThreads, 4) void k_experts_few(ExpertsParams p) {
@@ -329,7 +333,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void k_experts_few(ExpertsParams p)
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int lr = lane % 16, lq = lane / 16;
     const int nth = div_cols(p, (int)blockIdx.x);
-    const Tile tile = p.E <= kWave ? find_share<1>(p, nth) : find_share<kGroupMaxE / kWave>(p, nth);
+    const Tile tile = p.E <= kWave ? find_part<1, kFewRows>(p, nth) : find_part<kGroupMaxE / kWave, kFewRows>(p, nth);
     if (tile.e < 0) return;
     const int n0 = ((int)blockIdx.x - nth * p.col_tiles) * 16 * NR, n1 = min(n0 + 16 * NR, p.N);
     const int Kb = p.Kb, KB = (Kb + 127) / 128;
@@ -579,8 +583,8 @@ static void set_cols(ExpertsParams& p, int width) {
 
 template <typename F, int TB> hipError_t launch_few(ExpertsParams& p, hipStream_t st) {
     set_cols(p, kFewCols);
-    const int shares = p.E < p.P ? p.E : p.P;
-    const dim3 grid((unsigned)(shares * p.col_tiles)), block(kFewThreads);
+    const int parts = (p.E < p.P ? p.E : p.P) + p.P / kFewRows;
+    const dim3 grid((unsigned)(parts * p.col_tiles)), block(kFewThreads);
     if (p.whole_lines) hipLaunchKernelGGL((k_experts_few<F, TB, true>), grid, block, 0, st, p);
     else hipLaunchKernelGGL((k_experts_few<F, TB, false>), grid, block, 0, st, p);
     return hipGetLastError();
@@ -610,7 +614,7 @@ template <typename F> hipError_t launch_experts_as(ExpertsParams& p, hipStream_t
     //   40 x (2848, 2064), 8 rows: 96 / 103 / 98, 62 / 68 / 56; 6 of the 40 with 2 rows: 22 / 23 / 24,
     //     15 / 17 / 15; 2 of them: 10 / 10 / 21, 8 / 9 / 13
     // (e4m3 within 4 % of int8.)
-    const bool fits = extent < INT32_MAX && shares * (int64_t)((p.N + kFewCols - 1) / kFewCols) < (1 << 23);
+    const bool fits = extent < INT32_MAX && (shares + p.P / kFewRows) * (int64_t)((p.N + kFewCols - 1) / kFewCols) < (1 << 23);
     if (fits && p.P <= 8 * shares && (p.Kb >= 4096 || p.P < 2 * p.E || units < 256)) return launch_few<F, 1>(p, st);
     if (fits && p.P <= 16 * shares && (units < 128 || (units < 256 && p.Kb <= 8192))) return launch_few<F, 2>(p, st);
     // Tiles of half the columns while a round of whole ones would leave compute units

@@ -163,6 +163,8 @@ CASES = {
     "whole_tiles_long_k": (640, 2, 8, 8200, 2064, None, False),
     "whole_tiles_few_rows": (40, 8, 130, 520, 144, None, False),
     # starts of K that differ
+    "few_parts": (130, 1, 40, 72, 160, [65, 1, 64], False),
+    "few_parts_of_200": (200, 2, 200, 40, 48, [0] * 60 + [129, 0, 64] + [0] * 120 + [200, 5], True),
     "few_of_256": (60, 4, 256, 40, 48, None, True),
     "few_wide": (6, 2, 5, 2600, 4112, None, False),
     "few_wide_32_rows": (30, 2, 4, 1600, 8208, None, True),
