@@ -3,7 +3,8 @@
 //   mma16: 16 rows by 16 columns over a lane's two blocks of either operand
 //          (64 values of bf16, 128 of the 8-bit formats);
 //   mma32: 32 by 32 over two blocks (32 and 64 values);
-//   mma32_step: 32 by 32 over kWords blocks, the least the format takes.
+//   mma32_step: 32 by 32 over kWords blocks, the least the format takes;
+//   kExact: sums have no roundings, so parts of K may be added in any order.
 // Which values of K a lane's blocks hold does not matter as long as both operands
 // agree.  Lane l supplies row / column l % 16 (l % 32) and receives rows
 // 4 (l / 16) + q of column l % 16, or 8 (q / 4) + 4 (l / 32) + q % 4 of l % 32.
@@ -33,6 +34,7 @@ struct FmtE4m3 {
     typedef f32x16_t Acc32;
     static constexpr int kWords = 2;
     static constexpr bool kScaled = true;
+    static constexpr bool kExact = false;
     __device__ static __forceinline__ Acc16 mma16(const uint4& a0, const uint4& a1, const uint4& b0,
                                                   const uint4& b1, Acc16 c) {
         return mfma_e4m3(a0, a1, b0, b1, c);
@@ -54,6 +56,7 @@ struct FmtInt8 {
     typedef i32x16_t Acc32;
     static constexpr int kWords = 1;
     static constexpr bool kScaled = true;
+    static constexpr bool kExact = true;
     __device__ static __forceinline__ i32x4_t op(const uint4& v) {
         return i32x4_t{(int)v.x, (int)v.y, (int)v.z, (int)v.w};
     }
@@ -78,6 +81,7 @@ struct FmtBf16 {
     typedef f32x16_t Acc32;
     static constexpr int kWords = 1;
     static constexpr bool kScaled = false;
+    static constexpr bool kExact = false;
     __device__ static __forceinline__ Acc16 mma16(const uint4& a0, const uint4& a1, const uint4& b0,
                                                   const uint4& b1, Acc16 c) {
         return mfma_bf16(a1, b1, mfma_bf16(a0, b0, c));

@@ -20,7 +20,8 @@
 //     Only after its share of W8 is read and multiplied does a workgroup look
 //     at the slots, which are full by then; each wavefront then adds the
 //     deltas of every eighth segment to its own partial sums, and the eight
-//     partial sums join through LDS in a fixed order.
+//     partial sums join through LDS in a fixed order.  Partial sums of integers
+//     join as integers, before the scales, and the deltas beside them.
 // Both read rows as whole 128-byte segments and change lanes through LDS
 // (row_stage.hpp).  A consumer waits for producers only, which wait for
 // nothing and come first in the grid; the waits are bounded and report
@@ -334,17 +335,42 @@ __global__ __launch_bounds__(kFpThreads, TB * NR == 8 ? 2 : 4) void k_linear_8bi
             load_x(q % UX, b0 + (q + UX) * kFpWaves);
         }
     }
+    // e4m3: a wavefront's scaled part of the base sum, to which its deltas are added.
+    // Integers: the parts wait in LDS and join as integers, because one alone may be past
+    // the 24 bits of fp32 where the whole sum is small; the deltas join beside them.
     f32x4_t acc[NR][TB];
+    typename F::Acc16* parts = reinterpret_cast<typename F::Acc16*>(st);
 #pragma unroll
     for (int r = 0; r < NR; ++r)
 #pragma unroll
-        for (int t = 0; t < TB; ++t)
+        for (int t = 0; t < TB; ++t) {
+            if constexpr (F::kExact) parts[(r * TB + t) * kWave + lane] = sum[r][t];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) acc[r][t][q] = (float)sum[r][t][q] * (xs[t] * ws[r][q]);
+            for (int q = 0; q < 4; ++q) acc[r][t][q] = F::kExact ? 0.f : (float)sum[r][t][q] * (xs[t] * ws[r][q]);
+        }
+    // the block of outputs that this wavefront joins and stores: columns 16 jr + 4 lq + q of
+    // token 16 jt + lr
+    const int jr = wave / TB, jt = wave % TB;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    float my_xs = xs[0], my_ws[4];
+#pragma unroll
+    for (int t = 1; t < TB; ++t) my_xs = jt == t ? xs[t] : my_xs;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) my_ws[q] = jr == 0 ? ws[0][q] : ws[NR - 1][q];
+    auto join_base = [&]() {             // behind a barrier, in front of another before st is written
+        if (wave >= NR * TB) return;
+        typename F::Acc16 all = reinterpret_cast<const typename F::Acc16*>(smem)[wave * kWave + lane];
+#pragma unroll
+        for (int w = 1; w < kFpWaves; ++w)
+            all += reinterpret_cast<const typename F::Acc16*>(smem + w * kStage)[wave * kWave + lane];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = (float)all[q] * (my_xs * my_ws[q]);
+    };
 
     // ---- deltas
     const int q_rp = seg_ok && q_p0 < q_p1 && (!kTableChecks || range_ok) ? rank_l : 0;
-    if (__ballot(q_rp > 0) != 0ull) {
+    const bool deltas = __ballot(q_rp > 0) != 0ull;      // the same in every wavefront
+    if (deltas) {
         // B rows of the wavefront's first segments, in flight while S is read
         constexpr int PB = TB * NR >= 4 ? 2 : 3;
         uint4 pb[PB][NR][2];
@@ -365,6 +391,7 @@ __global__ __launch_bounds__(kFpThreads, TB * NR == 8 ? 2 : 4) void k_linear_8bi
         if (wave == 0 && q_rp > 0)
             for (int i = q_p0; i < q_p1; ++i) s_rp[i] = q_rp;
         __syncthreads();
+        if constexpr (F::kExact) join_base();
         // S: the slots of every position's own rank, four a thread in flight
         // together; positions and columns without one become zeros
         const uint32_t want = tag ^ p.wc.poll_xor;
@@ -455,25 +482,33 @@ __global__ __launch_bounds__(kFpThreads, TB * NR == 8 ? 2 : 4) void k_linear_8bi
     }
 
     // ---- join the eight partial sums; four columns of one token per lane
-    float4* red = reinterpret_cast<float4*>(st);
+    if constexpr (F::kExact)
+        if (!deltas) {
+            __syncthreads();
+            join_base();
+        }
+    if (!F::kExact || deltas) {
+        float4* red = reinterpret_cast<float4*>(st);
 #pragma unroll
-    for (int r = 0; r < NR; ++r)
+        for (int r = 0; r < NR; ++r)
 #pragma unroll
-        for (int t = 0; t < TB; ++t)
-            red[(r * TB + t) * kWave + lane] =
-                make_float4(acc[r][t][0], acc[r][t][1], acc[r][t][2], acc[r][t][3]);
-    __syncthreads();
+            for (int t = 0; t < TB; ++t)
+                red[(r * TB + t) * kWave + lane] =
+                    make_float4(acc[r][t][0], acc[r][t][1], acc[r][t][2], acc[r][t][3]);
+        __syncthreads();
+    }
     if (wave >= NR * TB) return;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (!F::kExact || deltas) {
 #pragma unroll
-    for (int w = 0; w < kFpWaves; ++w) {
-        const float4 f = reinterpret_cast<const float4*>(smem + w * kStage)[wave * kWave + lane];
-        v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+        for (int w = 0; w < kFpWaves; ++w) {
+            const float4 f = reinterpret_cast<const float4*>(smem + w * kStage)[wave * kWave + lane];
+            v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+        }
     }
     int m = tok[0];
 #pragma unroll
-    for (int t = 1; t < TB; ++t) m = wave % TB == t ? tok[t] : m;
-    const int n = n0 + wave / TB * 16 + lq * 4;          // slices are multiples of 8 wide
+    for (int t = 1; t < TB; ++t) m = jt == t ? tok[t] : m;
+    const int n = n0 + jr * 16 + lq * 4;          // slices are multiples of 8 wide
     if (m >= 0 && n < n1)
         *reinterpret_cast<uint2*>(p.y + (int64_t)m * p.ldy + n) =
             make_uint2(f32_to_bf16(v[0]) | (f32_to_bf16(v[1]) << 16), f32_to_bf16(v[2]) | (f32_to_bf16(v[3]) << 16));
