@@ -115,9 +115,9 @@ __global__ __launch_bounds__(kGroupThreads) void k_moe_group(const int32_t* __re
         const int rank = __popcll(same & below);
         if (act) pairs[s_before[b] + my[b] + rank] = f;
         // every lane has read its position before the first of its equals moves it
-        __builtin_amdgcn_wave_barrier();
+        stage_order();
         if (act && rank == 0) my[b] += __popcll(same);
-        __builtin_amdgcn_wave_barrier();
+        stage_order();
     };
 #pragma unroll
     for (int i = 0; i < kGroupCached; ++i)

@@ -27,6 +27,7 @@
 // everything about its rows in one memory round trip.
 #include "common.hpp"
 #include "kernels.hpp"
+#include "row_stage.hpp"
 #include "wave_groups.hpp"
 
 namespace mlora {
@@ -117,6 +118,7 @@ __global__ __launch_bounds__(kSegThreads) void k_build_segments(
         const bool act = c0 + i * kWave + lane < c1;
         const unsigned long long pe = peers_of(b, act);
         if (act && __popcll(pe & lt) == 0) my[b] += __popcll(pe);
+        stage_order();
     };
 #pragma unroll
     for (int i = 0; i < kCachedPasses; ++i)
@@ -242,9 +244,9 @@ __global__ __launch_bounds__(kSegThreads) void k_build_segments(
             }
         }
         // every lane has read its offset before the group's first lane moves it
-        __builtin_amdgcn_wave_barrier();
+        stage_order();
         if (act && rank_w == 0) my[b] += __popcll(peers);
-        __builtin_amdgcn_wave_barrier();
+        stage_order();
     };
 #pragma unroll
     for (int i = 0; i < kCachedPasses; ++i)
