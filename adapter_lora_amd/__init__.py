@@ -729,16 +729,25 @@ def lora_linear_int8(table: LoraTable, W8: torch.Tensor, w_scale: torch.Tensor, 
 # ------------------------------------------------------------------------- experts' products
 class MoeGroups:
     """Device buffers of a batch's (token, chosen expert) pairs by expert: up to
-    `pairs_cap` pairs (tokens times top-k) over E experts."""
+    `pairs_cap` pairs (tokens times top-k) over E experts.  `pairs` and `offsets` are
+    the same tensors for the object's life: the calls keep their addresses."""
 
     def __init__(self, pairs_cap: int, E: int, device="cuda"):
         if not 1 <= E <= 256:
             raise LoraError("expert count out of range")
         self.E, self.count, self.topk = int(E), 0, 0
-        self.pairs = torch.empty(max(int(pairs_cap), 1), dtype=_I32, device=device)
-        self.offsets = torch.zeros(self.E + 1, dtype=_I32, device=device)
+        self._pairs = torch.empty(max(int(pairs_cap), 1), dtype=_I32, device=device)
+        self._offsets = torch.zeros(self.E + 1, dtype=_I32, device=device)
         self.cap, self.device = self.pairs.shape[0], self.pairs.get_device()
         self.pairs_ptr, self.offsets_ptr = _ptr(self.pairs), _ptr(self.offsets)
+
+    @property
+    def pairs(self) -> torch.Tensor:
+        return self._pairs
+
+    @property
+    def offsets(self) -> torch.Tensor:
+        return self._offsets
 
 
 def lora_moe_group(topk_ids: torch.Tensor, groups: MoeGroups, stream=None) -> None:
