@@ -596,8 +596,11 @@ def _stream_on(dev: int, stream) -> int:
 
 
 def _scales(t: torch.Tensor, name: str, n: int, dev: int) -> int:
-    """Device address of one fp32 scale per row of an 8-bit tensor."""
-    if t.dtype is not _F32 or t.numel() < n or not t.is_contiguous():
+    """Device address of one fp32 scale per row of an 8-bit tensor: the first n
+    values of a longer vector, but not of a matrix with others between them."""
+    held = t.numel()
+    if t.dtype is not _F32 or held < n or not t.is_contiguous() or \
+            (held > n and t.dim() > 1 and t.shape[-1] != 1):
         raise LoraError(f"{name} must be contiguous fp32 with {n} values")
     on = t.get_device()
     if on != dev or on < 0:
