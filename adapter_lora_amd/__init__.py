@@ -740,7 +740,7 @@ class MoeGroups:
             raise LoraError("expert count out of range")
         self.E, self.count, self.topk = int(E), 0, 0
         self._pairs = torch.empty(max(int(pairs_cap), 1), dtype=_I32, device=device)
-        self._offsets = torch.zeros(self.E + 1, dtype=_I32, device=device)
+        self._offsets = torch.empty(self.E + 1, dtype=_I32, device=device)
         self.cap, self.device = self.pairs.shape[0], self.pairs.get_device()
         self.pairs_ptr, self.offsets_ptr = _ptr(self.pairs), _ptr(self.offsets)
 

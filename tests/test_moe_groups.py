@@ -20,6 +20,16 @@ def test_buffers_stay_what_the_calls_know(name):
     assert (g.pairs_ptr, g.offsets_ptr) == (g.pairs.data_ptr(), g.offsets.data_ptr())
 
 
+def test_construction_writes_nothing(monkeypatch):
+    """A fill on the constructing stream could land after another stream's first groups."""
+    def filled(*args, **kw):
+        pytest.fail("the buffers are filled")
+    monkeypatch.setattr(torch, "zeros", filled)
+    monkeypatch.setattr(torch, "full", filled)
+    g = ml.MoeGroups(8, 4, device="cpu")
+    assert g.pairs.shape == (8,) and g.offsets.shape == (5,) and g.count == 0
+
+
 class Reached(Exception):
     pass
 
