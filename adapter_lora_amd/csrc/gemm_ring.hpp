@@ -21,13 +21,21 @@
 
 namespace mlora {
 
+// A wave-uniform entry of a table that the launch only reads, by way of the scalar
+// cache.  (Behind the loads to LDS the compiler takes the tables as changed and reads
+// them as vectors, whose waits then include the B rows in flight.)
+template <typename T> __device__ __forceinline__ T table_entry(const T* table, int i) {
+    typedef const __attribute__((address_space(4))) T entry_t;
+    return reinterpret_cast<entry_t*>(reinterpret_cast<uintptr_t>(table))[i];
+}
+
 // Keeps a block of sums together in accumulation registers: split into its elements
-// across the branches below, they are spilled.
+// across the branches below, the sums are spilled.  (11 other values in int8 and 12 in
+// e4m3 still are, before and behind the main loop, none within it.)
 template <typename A> __device__ __forceinline__ void keep_block(A& v) { asm volatile("" : "+a"(v)); }
 
 template <typename R>
 __device__ __forceinline__ void ring_tile(const GemmFp8Params& p, uint4* smem, int sl, int p0, int rows, int n0, int cols) {
-    typedef typename R::F F;
     constexpr int RB = R::RB, CB = R::CB, NX = R::NX, kM = R::kRows;
     const LinearArgs& a = p.a;
     const int tid = threadIdx.x;
@@ -77,16 +85,16 @@ __device__ __forceinline__ void ring_tile(const GemmFp8Params& p, uint4* smem, i
             g.end = __builtin_amdgcn_readlane(srch1, s + 1);
             id = __builtin_amdgcn_readlane(q_id, s);
         } else {
-            g.beg = __builtin_amdgcn_readfirstlane(a.seg_indptr[s]);
-            g.end = __builtin_amdgcn_readfirstlane(a.seg_indptr[s + 1]);
-            id = __builtin_amdgcn_readfirstlane(a.req_to_lora[s]);
+            g.beg = __builtin_amdgcn_readfirstlane(table_entry(a.seg_indptr, s));
+            g.end = __builtin_amdgcn_readfirstlane(table_entry(a.seg_indptr, s + 1));
+            id = __builtin_amdgcn_readfirstlane(table_entry(a.req_to_lora, s));
         }
         if (g.beg >= p0 + rows) return g;
         const bool id_ok = id >= 0 && id < L;   // never index past the table
         table_fault(a.err, !id_ok);
         if (!id_ok) return g;
-        g.rp = quick ? __builtin_amdgcn_readlane(q_rk, id) : __builtin_amdgcn_readfirstlane(a.rank[id]);
-        g.bo = quick ? readlane64(q_bo, id) : readlane64(a.b_off[id], 0);
+        g.rp = quick ? __builtin_amdgcn_readlane(q_rk, id) : __builtin_amdgcn_readfirstlane(table_entry(a.rank, id));
+        g.bo = quick ? readlane64(q_bo, id) : readlane64(table_entry(a.b_off, id), 0);
         return g;
     };
     auto load_b = [&](uint4 (&b)[CB][4], const Seg& g) {
@@ -131,8 +139,9 @@ __device__ __forceinline__ void ring_tile(const GemmFp8Params& p, uint4* smem, i
     ring_product<R>(smem, reinterpret_cast<const char*>(p.W) + (int64_t)n0 * p.ldw, p.ldw, cols, a.K, 0, x_rows, sum);
 
     // ---- scales: row 32 rb + lr, columns 32 cb + 8 (q / 4) + 4 lh + q % 4 of the wave's part
-    constexpr int kStaged = kRingRows * kRingCols * 2;
-    int* const s_tok = reinterpret_cast<int*>(reinterpret_cast<char*>(smem) + kStaged);
+    constexpr int kScalesAt = 2 * kM * kSLD * 2;     // behind S's two halves
+    static_assert(kScalesAt % 16 == 0 && kScalesAt + 3 * kRingRows * 4 <= kRingLds, "S and the scales fit the LDS");
+    int* const s_tok = reinterpret_cast<int*>(reinterpret_cast<char*>(smem) + kScalesAt);
     float* const s_xs = reinterpret_cast<float*>(s_tok + kRingRows);
     float* const s_ws = s_xs + kRingRows;
     s_tok[tid] = my_tok;
@@ -166,7 +175,6 @@ __device__ __forceinline__ void ring_tile(const GemmFp8Params& p, uint4* smem, i
 
     uint16_t* const sHi = reinterpret_cast<uint16_t*>(smem);
     uint16_t* const sLo = sHi + kM * kSLD;
-    static_assert(2 * kM * kSLD * 2 <= kStaged, "S in front of the scales");
     if (lora) {
         first_segment();
         load_s();
