@@ -566,7 +566,7 @@ hipError_t launch_gemm_8bit(const LinearArgs& a, const void* x8, int64_t ldx8, c
     const int64_t cost_s = small <= 4096 ? small * (14 * 4096 + 85 * K) : INT64_MAX;
     const int64_t cost_l = large * (80 * 4096 + 200 * K);
     // Tiles of 256 x 256 (gemm_ring.hpp) run at 2.7 PFLOP/s and more and lose most where
-    // they do not fill the chip: a round takes 1.3 (K = 512) to 1.65 (K = 4096) times one
+    // they do not fill the chip: a round takes 1.2 (K = 512) to 1.6 (K = 4096) times one
     // of the large units.  Measured calls in int8, the units' better choice against tiles
     // (8 adapters): K = 512, 512 x 28672 33.9 / 33.7 us; K = 1024, 1024 x 14336 40.0 / 37.8;
     // K = 2048, 768 x 8192 34.7 / 52.4; K = 4096, 300 x 28672 82.5 / 75.6, 512 x 28672 (12
@@ -574,9 +574,19 @@ hipError_t launch_gemm_8bit(const LinearArgs& a, const void* x8, int64_t ldx8, c
     // 200 / 165, 2048 x 28672 312 / 286; K = 8192, 1024 x 8192 92 / 135.  In e4m3 4096 x 4096
     // 98 / 86, 8192 x 4096 170 / 144, 512 x 28672 101 / 87, 2048 x 4096 55 / 79.  The sums
     // are the same bits either way.
+    //
+    // A tile walks the segments of its 256 rows one after the other, which small units
+    // hide behind each other and large ones have half as many of.  The host knows the
+    // slots, not the segments: it counts every slot as used evenly.  Measured in e4m3,
+    // units against tiles: 394 x 608 to 28800 with 8 / 16 / 48 / 256 slots 39.9 / 43.4 / 64.2
+    // / 177 us against 38.7 / 45.4 / 77.0 / 246; 975 x 1344 to 11496 with 32 / 60 / 128 53.7 / 63.0
+    // / 97.3 and 52.6 / 65.5 / 112; 512 x 4096 to 28672 with 60 / 128 / 256 145 / 207 / 283 and 134
+    // / 198 / 288; 2079 x 4480 to 7096 with 256 192 and 154.
     const int64_t tiles = (int64_t)((a.M + kRingRows - 1) / kRingRows) * nl;
-    const int64_t cost_r = tiles <= (1 << 22) ? (tiles + 255) / 256 * (130 * 4096 + 330 * K) : INT64_MAX;
-    if (cost_r < cost_s && cost_r < cost_l) return launch_gemm_ring<F>(p, st);
+    const int64_t slots = a.L < a.M ? a.L : a.M;
+    auto met = [&](int64_t rows) { return std::min(slots, slots * rows / a.M + 1); };
+    const int64_t cost_r = tiles <= (1 << 22) ? (tiles + 255) / 256 * (115 * 4096 + 330 * K + 10240 * met(256)) : INT64_MAX;
+    if (cost_r < (cost_s < cost_l ? cost_s : cost_l + large * 6144 * met(128))) return launch_gemm_ring<F>(p, st);
     if (cost_s < cost_l) return launch_gemm_8bit_as<F, G8Shape<2, 1>>(p, st);
     return launch_gemm_8bit_as<F, G8Shape<4, 2>>(p, st);
 }

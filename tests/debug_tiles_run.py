@@ -13,6 +13,7 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 sys.path.insert(0, ROOT)
 import adapter_lora_amd as ml  # noqa: E402
 from tests import test_gpu_int8, test_gpu_linear_fp8  # noqa: E402
+from tests.linear_forms import form  # noqa: E402
 
 PAD = 64
 
@@ -55,13 +56,14 @@ def linear(Case, M, K, sizes, ranks=(16, 32), special=False):
 
 
 FP8, INT8 = test_gpu_linear_fp8.Case, test_gpu_int8.Case
-TILES = (500, 1024, [28672])
+TILES, SLOTS = (500, 1024, [28672]), (2000, 1024, [8192])
+assert form(*TILES, 2) == form(*SLOTS, 80) == ("tiles",)
 out = {"lib": os.path.basename(ml._abi.LIB_PATH)}
 out["tiles_fp8"] = linear(FP8, *TILES)
 out["tiles_fp8_special"] = linear(FP8, *TILES, special=True)
 out["tiles_int8"] = linear(INT8, *TILES)
-out["tiles_int8_slots"] = linear(INT8, *TILES, ranks=[16, 32] * 40)
-out["tiles_int8_special_slots"] = linear(INT8, *TILES, ranks=[16, 32] * 40, special=True)
+out["tiles_int8_slots"] = linear(INT8, *SLOTS, ranks=[16, 32] * 40)
+out["tiles_int8_special_slots"] = linear(INT8, *SLOTS, ranks=[16, 32] * 40, special=True)
 out["decode_int8"] = linear(INT8, 40, 256, [72])
 out["groups_int8"] = linear(INT8, 150, 2048, [72])
 out["units_int8"] = linear(INT8, 150, 256, [264])

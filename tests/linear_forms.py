@@ -11,20 +11,23 @@ def decode_form(M, K, sizes):
     return "decode", 1 if M <= 16 else 2 if M <= 32 else 4, 2 if wide else 1
 
 
-def form(M, K, sizes):
+def form(M, K, sizes, L):
     """("decode", tokens / 16, columns / 16), ("groups", columns / 16), ("units", rows,
-    columns) or ("tiles",)."""
+    columns) or ("tiles",), with a table of L slots."""
     if M <= 64:
         return decode_form(M, K, sizes)
     N, groups = sum(sizes), -(-M // 64)
     if groups * -(-N // 32) <= 256 and K >= 2048:
         return "groups", 2 if groups * (N // 32) >= 192 else 1
 
-    def cost(rows, width, fixed, per_k):
-        units = -(-M // rows) * sum(-(-n // width) for n in sizes)
-        return -(-units // 256) * (fixed * 4096 + per_k * K)
-    small, large, tiles = cost(64, 128, 14, 85), cost(128, 256, 80, 200), cost(256, 256, 130, 330)
-    if tiles < small and tiles < large:
+    def rounds(rows, width):
+        return -(-(-(-M // rows) * sum(-(-n // width) for n in sizes)) // 256)
+
+    def met(rows):                       # segments that so many rows belong to
+        return min(L, M, min(L, M) * rows // M + 1)
+    small, large = rounds(64, 128) * (14 * 4096 + 85 * K), rounds(128, 256) * (80 * 4096 + 200 * K)
+    tiles = rounds(256, 256) * (115 * 4096 + 330 * K + 10240 * met(256))
+    if tiles < (small if small < large else large + rounds(128, 256) * 6144 * met(128)):
         return ("tiles",)
     return ("units", 64, 128) if small < large else ("units", 128, 256)
 

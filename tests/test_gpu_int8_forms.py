@@ -12,19 +12,25 @@ from tests.test_gpu_int8 import Case
 SIZES = {**paths.FORMS, **{"large_" + k: v for k, v in paths.LARGE.items()}}
 
 
+def case_form(case):
+    M, K, sizes, ranks = case[:4]
+    return form(M, K, sizes, len(ranks))
+
+
 def test_sizes_reach_every_form():
-    reached = {form(M, K, sizes) for M, K, sizes, _ in SIZES.values()}
-    assert reached | {form(*c[:3]) for c in ring.CASES.values()} == EVERY_FORM
-    assert {form(*c[:3]) for n, c in SIZES.items() if n.startswith("large_")} == {("units", 128, 256)}
-    assert all(form(*c[:3])[2] == 2 for n, c in SIZES.items() if n.startswith("wide_"))
-    assert all(form(*c[:3]) == ("groups", 2) for n, c in SIZES.items() if n.startswith("groups_wide"))
+    reached = {case_form(c) for c in SIZES.values()}
+    tiles = [n for n, c in ring.CASES.items() if case_form(c) == ("tiles",)]
+    assert set(ring.CASES) - set(tiles) <= {"many_slots"} and reached | {("tiles",)} == EVERY_FORM
+    assert {case_form(c) for n, c in SIZES.items() if n.startswith("large_")} == {("units", 128, 256)}
+    assert all(case_form(c)[2] == 2 for n, c in SIZES.items() if n.startswith("wide_"))
+    assert all(case_form(c) == ("groups", 2) for n, c in SIZES.items() if n.startswith("groups_wide"))
 
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("name", list(SIZES))
 def test_every_form_matches_oracle(name):
     M, K, sizes, ranks = SIZES[name]
-    print(name, form(M, K, sizes), flush=True)
+    print(name, case_form(SIZES[name]), flush=True)
     c = Case(M, K, sizes, ranks, None, seed=len(name))
     y = c.run()
     c.check(y)

@@ -31,7 +31,7 @@ SIZES = {
 
 
 def test_sizes_reach_every_form():
-    assert {form(M, K, sizes) for M, sizes in SIZES.values()} == EVERY_FORM
+    assert {form(M, K, sizes, 3) for M, sizes in SIZES.values()} == EVERY_FORM
 
 
 def cancelling(rows, width, g):

@@ -11,7 +11,8 @@ import pytest
 import torch
 
 from tests import test_gpu_moe_linear as X
-from tests.test_gpu_ring_tiles import KINDS, takes_tiles
+from tests.linear_forms import form
+from tests.test_gpu_ring_tiles import KINDS
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -53,8 +54,8 @@ def test_infinities_beside_eighty_slots(kind):
     """More slots than lanes, so that segments are looked up in memory, and an infinity in
     the B of a late slot: it stays with its tokens."""
     import adapter_lora_amd as ml
-    M, K, N, L = 512, 1040, 28672, 80
-    assert takes_tiles(M, K, [N])
+    M, K, N, L = 2000, 1040, 8192, 80
+    assert form(M, K, [N], L) == ("tiles",)
     c = KINDS[kind](M, K, [N], [16, 32] * (L // 2), (torch.arange(M) % (L + 1) - 1).tolist(), seed=4)
     clean = c.run()
     c.check(clean)
