@@ -188,8 +188,8 @@ __device__ __forceinline__ void fp8_producer(const Fp8Params& p, uint32_t tag, u
 // from memory (p.S, an earlier launch's), and a consumer takes the columns'
 // product for one group of 64 sorted positions; the groups of a column tile
 // follow each other on one L2 (every eighth workgroup).  With TB = 4 and NR = 1 the
-// 128 registers are full: one value (SLOTS) or six are spilled across the loop over K,
-// none within it.
+// 128 registers are full: in e4m3 one value (SLOTS) or six, in int8 two (SLOTS) or none
+// are spilled across the loop over K, none within it.
 template <typename F, int TB, int NR, bool SLOTS>
 __global__ __launch_bounds__(kFpThreads, TB * NR == 8 ? 2 : 4) void k_linear_8bit(Fp8Params p) {
     constexpr int kStage = fp8_stage(TB, NR);

@@ -661,8 +661,9 @@ lora_status lora_moe_group(const int32_t* topk_ids, int32_t M, int32_t topk, int
  *   types (NULL for LORA_BF16, whose sums have no scales);
  *   pairs, offsets: lora_moe_group's, of the same M, topk and E.
  * N a multiple of 8; K and ldx of 8 (16 for the 8-bit types), K at most 131056
- * (LORA_UNSUPPORTED past it).  Sums are fp32 (LORA_INT8: 32-bit integers; LORA_E4M3:
- * as in lora_linear_fp8), y is rounded once.  No row of x past its share's is
+ * (LORA_UNSUPPORTED past it, and where the tiles of 256 x 256 outputs, (M*topk / 256 +
+ * min(E, M*topk) + 1) * ceil(N / 256) at most, are more than 2^23).  Sums are fp32
+ * (LORA_INT8: 32-bit integers; LORA_E4M3: as in lora_linear_fp8), y is rounded once.  No row of x past its share's is
  * read, and none of y written, whatever pairs and offsets hold.
  */
 lora_status lora_moe_linear(int32_t wdtype, const void* W, const float* w_scale, int32_t E,
